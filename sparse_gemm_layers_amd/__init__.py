@@ -2,7 +2,8 @@
 linear-layer GEMMs for AMD Instinct MI355X (gfx950).
 
 A thin Python binding over the C ABI of ``libsg.so`` (declared in
-``include/sg.h``; the measurement helpers in ``include/sg_probe.h``).  The functions only marshal arguments: PyTorch supplies
+``include/sg.h``; the measurement helpers in ``include/sg_probe.h``; the
+mixture-of-experts operators in ``sparse_gemm_layers_amd/include/sg_moe.h``).  The functions only marshal arguments: PyTorch supplies
 device memory and the current HIP stream; every step runs in the library's
 HIP kernels.  There is no CPU fallback: if ``libsg.so`` is missing or the
 tensors are not on a GPU, the call raises.
@@ -39,6 +40,15 @@ from ._binding import (
     sparse24_w4_packed_bytes,
     sparse24_pack_w4,
 )
+from ._moe import (
+    moe_route,
+    moe_route_backward,
+    w4_packed_bytes,
+    w4_pack,
+    w4a16_gemm_groupwise_packed,
+    w4a16_moe_mlp_workspace,
+    w4a16_moe_mlp,
+)
 
 __all__ = [
     "SgError", "lib", "fp8_quant_groupwise", "int4_quant_groupwise",
@@ -51,4 +61,6 @@ __all__ = [
     "fp8_sparse24_gemm_groupwise_packed_batched", "fp8_sparse24_gemm_groupwise_packed_grouped",
     "w8a16_sparse24_gemm_groupwise", "w8a16_sparse24_gemm_groupwise_packed", "w4a16_sparse24_gemm_groupwise",
     "w4a16_sparse24_gemm_groupwise_packed", "sparse24_w4_packed_bytes", "sparse24_pack_w4",
+    "moe_route", "moe_route_backward", "w4_packed_bytes", "w4_pack", "w4a16_gemm_groupwise_packed",
+    "w4a16_moe_mlp_workspace", "w4a16_moe_mlp",
 ]

@@ -32,7 +32,7 @@ CFLAGS = [
     # matrix-core results in VGPRs: the promotion FMAs read them directly
     # instead of copying them out of AGPRs
     "-mllvm", "-amdgpu-mfma-vgpr-form",
-    "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+    "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "include"), "-I", CSRC,
     "-Wall", "-Wno-unused-function",
 ]
 

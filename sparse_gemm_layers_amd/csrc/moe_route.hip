@@ -1,0 +1,462 @@
+// Routing of tokens to experts and its gradient.
+//
+// One wave per token, grid-striding over tokens; lane l holds experts l, l + 64,
+// ... (VPL of them), so each load of a row is one contiguous piece.  The choice
+// must not depend on fp32 rounding: two experts whose keys lie next to each
+// other have to come out in the same order however the scores are computed.
+// Without a bias the key is the logit itself, which fp32 holds exactly.  With
+// one, scores and keys are computed in fp64 (full-rate on CDNA4) and rounded to
+// an ordered 32-bit integer; rounding is monotone, so the largest integer marks
+// the largest key, and the fp64 values decide among equals alone.
+#include "common.h"
+#include "sg_moe.h"
+
+namespace sg {
+
+struct RouteArgs {
+  const void* logits;
+  int64_t ldl;
+  int64_t T;
+  int E, k;
+  const float* bias;
+  int n_group, per, topk_group, top2, sigmoid, renorm;
+  float scale;
+  int32_t* ids;
+  float* weights;
+};
+
+struct RouteGradArgs {
+  const float* grad;
+  const void* logits;
+  int64_t ldl, T;
+  int E, k;
+  const int32_t* ids;
+  int sigmoid, renorm;
+  float scale;
+  void* out;
+  int64_t ldd;
+};
+
+constexpr int RT_WAVES = 4, RT_EMAX = 1024, RT_KMAX = 64, RT_GMAX = 64;
+
+#if SG_DEVICE_PASS
+__device__ __forceinline__ float rt_load(const void* p, int64_t i, bool bf16) {
+  return bf16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[i]) : reinterpret_cast<const float*>(p)[i];
+}
+
+// fp32 -> unsigned integers of the same order; 0 is below every number (it
+// stands for an expert that is out).  -0 and +0 give one integer.
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t u = __float_as_uint(f + 0.0f);
+  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+// One step of a reduction over the wave's lanes: the value CTRL moves here, 0
+// where it moves none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp0(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+// row_shr 1, 2, 4, 8, then each row's last lane into the next rows: lane 63
+// ends with the whole wave's result.
+#define SG_WAVE_STEPS(STEP) \
+  STEP(0x111, 0xf) STEP(0x112, 0xf) STEP(0x114, 0xf) STEP(0x118, 0xf) STEP(0x142, 0xa) STEP(0x143, 0xc)
+
+__device__ __forceinline__ float lane_value(float v, int l) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), l));
+}
+__device__ __forceinline__ double lane_value(double v, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, l);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l);
+  return __builtin_bit_cast(double, (uint64_t)lo | ((uint64_t)hi << 32));
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#define STEP(C, R) v = max(v, dpp0<C, R>(v));
+  SG_WAVE_STEPS(STEP)
+#undef STEP
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#define STEP(C, R) v += __uint_as_float(dpp0<C, R>(__float_as_uint(v)));
+  SG_WAVE_STEPS(STEP)
+#undef STEP
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+#define STEP(C, R)                                                                        \
+  {                                                                                       \
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);                                   \
+    const uint64_t d = dpp0<C, R>((uint32_t)u) | ((uint64_t)dpp0<C, R>((uint32_t)(u >> 32)) << 32); \
+    v += __builtin_bit_cast(double, d);                                                   \
+  }
+  SG_WAVE_STEPS(STEP)
+#undef STEP
+  return lane_value(v, 63);
+}
+#undef SG_WAVE_STEPS
+
+__device__ __forceinline__ double wave_max_slow(double v) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v = fmax(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
+// Orders this wave's LDS accesses of its lanes before against those after.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The lowest expert among the marked ones (lane l's bit i: expert i 64 + l).
+template <int VPL>
+__device__ __forceinline__ int lowest(const bool (&mark)[VPL]) {
+  int e = -1;
+#pragma unroll
+  for (int i = VPL - 1; i >= 0; --i) {
+    const uint64_t b = __ballot(mark[i]);
+    if (b) e = i * 64 + __builtin_ctzll(b);
+  }
+  return e;
+}
+
+// The groups that stay, as a bit mask.  val (LDS, one value per expert, -inf:
+// out) holds what a group's value is taken from.  LPG lanes share a group (a
+// power of two) and join their two largest by exchange.
+__device__ __forceinline__ uint64_t pick_groups(const double* val, const RouteArgs& a, int lane) {
+  const double low = -__builtin_inf();
+  const int lpg = 1 << (31 - __builtin_clz(64 / a.n_group));
+  const int grp = lane / lpg, sub = lane & (lpg - 1);
+  double b0 = low, b1 = low;
+  if (grp < a.n_group) {
+    for (int m = sub; m < a.per; m += lpg) {
+      const double v = val[grp * a.per + m];
+      b1 = fmax(b1, fmin(b0, v));
+      b0 = fmax(b0, v);
+    }
+  }
+  for (int o = 1; o < lpg; o <<= 1) {
+    const double c0 = __shfl_xor(b0, o, 64), c1 = __shfl_xor(b1, o, 64);
+    b1 = fmax(fmax(b1, c1), fmin(b0, c0));
+    b0 = fmax(b0, c0);
+  }
+  const double v = a.top2 && b1 > low ? b0 + b1 : b0;
+  int rank = 0;
+  for (int g = 0; g < a.n_group; ++g) {
+    const double o = __shfl(v, g * lpg, 64);
+    rank += (o > v || (o == v && g < grp)) ? 1 : 0;
+  }
+  uint64_t keep = 0;
+  const uint64_t b = __ballot(grp < a.n_group && sub == 0 && rank < a.topk_group);
+  for (int g = 0; g < a.n_group; ++g) keep |= ((b >> (g * lpg)) & 1ull) << g;
+  return keep;
+}
+#endif  // SG_DEVICE_PASS
+
+// F64: scores of every expert in fp64 (a bias, or groups by their two largest
+// scores); otherwise the keys are the logits and only the chosen experts'
+// weights are computed.
+template <int VPL, bool F64, bool BF16>
+__global__ void __launch_bounds__(64 * RT_WAVES) k_moe_route(RouteArgs a) {
+#if SG_DEVICE_PASS
+  extern __shared__ double rt_lds[];   // n_group > 1: VPL * 64 group values per wave
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  double* const val = rt_lds + wave * (VPL * 64);
+  const double low = -__builtin_inf();
+
+  float bias[VPL];
+  bool bok[VPL];
+  int grp[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const int e = i * 64 + lane;
+    const float b = a.bias && e < a.E ? a.bias[e] : 0.0f;
+    bok[i] = e < a.E && b > -__builtin_inff();
+    bias[i] = fminf(b, 3.402823466e38f);
+    grp[i] = a.n_group > 1 ? e / a.per : 0;
+  }
+
+  for (int64_t t = (int64_t)blockIdx.x * RT_WAVES + wave; t < a.T; t += (int64_t)gridDim.x * RT_WAVES) {
+    float x[VPL];
+    bool lok[VPL], ok[VPL];   // enters the softmax; may be chosen
+    uint32_t top32 = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = i * 64 + lane;
+      const float v = e < a.E ? rt_load(a.logits, t * a.ldl + e, BF16) : -__builtin_inff();
+      lok[i] = v > -__builtin_inff();   // false for NaN
+      ok[i] = lok[i] && bok[i];
+      x[i] = fminf(v, 3.402823466e38f);
+      if (lok[i]) top32 = max(top32, ordered(x[i]));
+    }
+    top32 = wave_max(top32);
+    const float top = __uint_as_float((top32 >> 31) ? top32 ^ 0x80000000u : ~top32);   // unused when top32 == 0
+
+    double s[VPL], sum = 1.0;
+    if (F64) {
+      double part = 0.0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (a.sigmoid) {
+          s[i] = lok[i] ? 1.0 / (1.0 + exp(-(double)x[i])) : 0.0;
+        } else {
+          s[i] = lok[i] ? exp((double)x[i] - (double)top) : 0.0;
+          part += s[i];
+        }
+      }
+      if (!a.sigmoid) {
+        sum = wave_sum(part);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) s[i] = top32 ? s[i] / sum : 0.0;
+      }
+    } else if (!a.sigmoid) {
+      float part = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) part += lok[i] ? expf(x[i] - top) : 0.0f;
+      sum = (double)wave_sum(part);
+    }
+
+    double key[VPL];   // fp64 key, where it is not the logit
+    uint32_t k32[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      key[i] = F64 && a.bias ? s[i] + (double)bias[i] : (double)x[i];
+      k32[i] = ok[i] ? ordered((float)key[i]) : 0u;
+    }
+    if (a.n_group > 1) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        val[i * 64 + lane] = !ok[i] ? low : F64 && a.top2 && !a.bias ? s[i] : key[i];
+      wave_sync();
+      const uint64_t keep = pick_groups(val, a, lane);
+      wave_sync();
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (!((keep >> (grp[i] & 63)) & 1)) k32[i] = 0u;
+    }
+
+    // k rounds: the largest key of the wave, the lowest expert among equals
+    int my_id = -1;
+    double my_s = 0.0;   // F64: the chosen score of this lane's slot
+    float my_x = 0.0f;   // otherwise its logit
+    for (int j = 0; j < a.k; ++j) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) m = max(m, k32[i]);
+      m = wave_max(m);
+      if (m == 0) break;
+      bool hit[VPL];
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        hit[i] = k32[i] == m;
+        if (F64) n += __builtin_popcountll(__ballot(hit[i]));
+      }
+      if (F64 && n > 1) {   // equal after rounding: the fp64 keys decide
+        double b = low;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) b = hit[i] ? fmax(b, key[i]) : b;
+        b = wave_max_slow(b);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) hit[i] = hit[i] && key[i] == b;
+      }
+      const int e = lowest<VPL>(hit);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if ((e >> 6) == i) {   // uniform
+          if (F64) {
+            const double v = lane_value(s[i], e & 63);
+            if (lane == j) my_s = v;
+          } else {
+            const float v = lane_value(x[i], e & 63);
+            if (lane == j) my_x = v;
+          }
+          if (lane == (e & 63)) k32[i] = 0u;
+        }
+      }
+      if (lane == j) my_id = e;
+    }
+
+    double w = my_s;
+    if (!F64) w = a.sigmoid ? 1.0 / (1.0 + exp(-(double)my_x)) : exp((double)my_x - (double)top) / sum;
+    if (my_id < 0) w = 0.0;
+    if (a.renorm) w = w / fmax(wave_sum(w), 1e-300);
+    if (lane < a.k) {
+      a.ids[t * a.k + lane] = my_id;
+      a.weights[t * a.k + lane] = (float)(w * (double)a.scale);
+    }
+  }
+#endif  // SG_DEVICE_PASS
+}
+
+// One wave per token.  Lane j < k computes the gradient through slot j; the row
+// is put together in LDS (zero, then the chosen experts) and leaves in
+// contiguous pieces.  ALL: softmax weights kept as they are, where every
+// probability of the row enters.
+template <int VPL, bool ALL, bool BF16>
+__global__ void __launch_bounds__(64 * RT_WAVES) k_moe_route_grad(RouteGradArgs a) {
+#if SG_DEVICE_PASS
+  extern __shared__ float rt_row[];   // VPL * 64 per wave
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  float* const row = rt_row + wave * (VPL * 64);
+
+  for (int64_t t = (int64_t)blockIdx.x * RT_WAVES + wave; t < a.T; t += (int64_t)gridDim.x * RT_WAVES) {
+    const int id = lane < a.k ? a.ids[t * a.k + lane] : -1;
+    const bool in = id >= 0 && id < a.E;
+    const float g = in ? a.grad[t * a.k + lane] : 0.0f;
+    float v = in ? rt_load(a.logits, t * a.ldl + id, BF16) : -__builtin_inff();
+    if (!(v > -__builtin_inff())) v = -__builtin_inff();   // NaN is out too
+    v = fminf(v, 3.402823466e38f);
+    const bool live = v > -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) row[i * 64 + lane] = 0.0f;
+
+    float d = 0.0f, dot = 0.0f, top = 0.0f, z = 1.0f;
+    float x[VPL];
+    if (ALL) {
+      uint32_t top32 = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int e = i * 64 + lane;
+        const float u = e < a.E ? rt_load(a.logits, t * a.ldl + e, BF16) : -__builtin_inff();
+        x[i] = u > -__builtin_inff() ? fminf(u, 3.402823466e38f) : -__builtin_inff();
+        if (x[i] > -__builtin_inff()) top32 = max(top32, ordered(x[i]));
+      }
+      top32 = wave_max(top32);
+      top = top32 == 0 ? 0.0f : __uint_as_float((top32 >> 31) ? top32 ^ 0x80000000u : ~top32);
+      float part = 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        x[i] = expf(x[i] - top);
+        part += x[i];
+      }
+      z = top32 == 0 ? 0.0f : 1.0f / wave_sum(part);
+      const float p = live ? expf(v - top) * z : 0.0f;
+      dot = wave_sum(g * p);
+    } else if (a.sigmoid) {
+      // s and 1 - s each from its own exponential: neither loses its small values
+      const double en = exp(-(double)v), s = live ? 1.0 / (1.0 + en) : 0.0;
+      const double c = live ? 1.0 / (1.0 + exp((double)v)) : 0.0;
+      if (a.renorm) {
+        const double r = s / fmax(wave_sum(s), 1e-300);
+        const double q = wave_sum((double)g * r);
+        d = (float)((double)a.scale * r * c * ((double)g - q));
+      } else {
+        d = (float)((double)a.scale * (double)g * s * c);
+      }
+    } else {   // softmax over the chosen
+      const uint32_t top32 = wave_max(live ? ordered(v) : 0u);
+      const float m = top32 == 0 ? 0.0f : __uint_as_float((top32 >> 31) ? top32 ^ 0x80000000u : ~top32);
+      const float ex = live ? expf(v - m) : 0.0f;
+      const float r = ex / fmaxf(wave_sum(ex), 1e-37f);
+      d = a.scale * r * (g - wave_sum(g * r));
+    }
+
+    wave_sync();
+    if (in) row[id] = ALL ? g : d;
+    wave_sync();
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = i * 64 + lane;
+      if (e >= a.E) continue;
+      const float o = ALL ? a.scale * (x[i] * z) * (row[e] - dot) : row[e];
+      if (BF16) reinterpret_cast<uint16_t*>(a.out)[t * a.ldd + e] = (uint16_t)f32_to_bf16(o);
+      else reinterpret_cast<float*>(a.out)[t * a.ldd + e] = o;
+    }
+    wave_sync();
+  }
+#endif  // SG_DEVICE_PASS
+}
+
+// VPL: the smallest of 1, 2, 4, 8, 16 that holds E experts in 64 lanes.
+template <bool F64, bool BF16>
+static void launch_route(const RouteArgs& a, hipStream_t st) {
+  const unsigned grid = grid_for(a.T, RT_WAVES, 2048);
+  const int vpl = a.E <= 64 ? 1 : a.E <= 128 ? 2 : a.E <= 256 ? 4 : a.E <= 512 ? 8 : 16;
+  const size_t lds = a.n_group > 1 ? (size_t)RT_WAVES * vpl * 64 * sizeof(double) : 0;
+  switch (vpl) {
+    case 1: k_moe_route<1, F64, BF16><<<grid, 64 * RT_WAVES, lds, st>>>(a); break;
+    case 2: k_moe_route<2, F64, BF16><<<grid, 64 * RT_WAVES, lds, st>>>(a); break;
+    case 4: k_moe_route<4, F64, BF16><<<grid, 64 * RT_WAVES, lds, st>>>(a); break;
+    case 8: k_moe_route<8, F64, BF16><<<grid, 64 * RT_WAVES, lds, st>>>(a); break;
+    default: k_moe_route<16, F64, BF16><<<grid, 64 * RT_WAVES, lds, st>>>(a); break;
+  }
+}
+
+template <bool ALL, bool BF16>
+static void launch_route_grad(const RouteGradArgs& a, hipStream_t st) {
+  const unsigned grid = grid_for(a.T, RT_WAVES, 2048);
+  const int vpl = a.E <= 64 ? 1 : a.E <= 128 ? 2 : a.E <= 256 ? 4 : a.E <= 512 ? 8 : 16;
+  const size_t lds = (size_t)RT_WAVES * vpl * 64 * sizeof(float);
+  switch (vpl) {
+    case 1: k_moe_route_grad<1, ALL, BF16><<<grid, 64 * RT_WAVES, lds, st>>>(a); break;
+    case 2: k_moe_route_grad<2, ALL, BF16><<<grid, 64 * RT_WAVES, lds, st>>>(a); break;
+    case 4: k_moe_route_grad<4, ALL, BF16><<<grid, 64 * RT_WAVES, lds, st>>>(a); break;
+    case 8: k_moe_route_grad<8, ALL, BF16><<<grid, 64 * RT_WAVES, lds, st>>>(a); break;
+    default: k_moe_route_grad<16, ALL, BF16><<<grid, 64 * RT_WAVES, lds, st>>>(a); break;
+  }
+}
+
+}  // namespace sg
+
+using namespace sg;
+
+extern "C" sg_status sg_moe_route(const void* logits, sg_dtype l_dt, int64_t T, int64_t E, int64_t ldl,
+                                  const float* bias, int k, sg_score score, int n_group, int topk_group,
+                                  sg_group_score group_score, int renormalize, float scale, int32_t* ids,
+                                  float* weights, hipStream_t stream) {
+  if (!logits || !ids || !weights) return SG_ERR_NULL;
+  if (l_dt != SG_F32 && l_dt != SG_BF16) return SG_ERR_UNSUPPORTED;
+  if (score != SG_SCORE_SOFTMAX && score != SG_SCORE_SIGMOID) return SG_ERR_UNSUPPORTED;
+  if (group_score != SG_GROUP_MAX && group_score != SG_GROUP_TOP2) return SG_ERR_UNSUPPORTED;
+  if (T <= 0 || E <= 0 || E > RT_EMAX || ldl < E || k < 1 || k > RT_KMAX || k > E) return SG_ERR_SHAPE;
+  if (n_group < 1 || n_group > RT_GMAX || E % n_group || topk_group < 1 || topk_group > n_group) return SG_ERR_SHAPE;
+  if (k > topk_group * (E / n_group)) return SG_ERR_SHAPE;
+  if (!aligned(logits, dtype_size(l_dt)) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(weights, 4))
+    return SG_ERR_ALIGN;
+  RouteArgs a;
+  a.logits = logits; a.ldl = ldl; a.T = T; a.E = (int)E; a.k = k; a.bias = bias;
+  a.n_group = n_group; a.per = (int)(E / n_group); a.topk_group = topk_group;
+  a.top2 = group_score == SG_GROUP_TOP2; a.sigmoid = score == SG_SCORE_SIGMOID; a.renorm = renormalize != 0;
+  a.scale = scale; a.ids = ids; a.weights = weights;
+  clear_hip_error();
+  const bool f64 = bias || (n_group > 1 && a.top2);
+  if (l_dt == SG_BF16) {
+    if (f64) launch_route<true, true>(a, stream);
+    else launch_route<false, true>(a, stream);
+  } else {
+    if (f64) launch_route<true, false>(a, stream);
+    else launch_route<false, false>(a, stream);
+  }
+  return launch_status();
+}
+
+extern "C" sg_status sg_moe_route_backward(const float* grad, const void* logits, sg_dtype l_dt, int64_t T, int64_t E,
+                                           int64_t ldl, const int32_t* ids, int k, sg_score score, int renormalize,
+                                           float scale, void* dlogits, int64_t ldd, hipStream_t stream) {
+  if (!grad || !logits || !ids || !dlogits) return SG_ERR_NULL;
+  if (l_dt != SG_F32 && l_dt != SG_BF16) return SG_ERR_UNSUPPORTED;
+  if (score != SG_SCORE_SOFTMAX && score != SG_SCORE_SIGMOID) return SG_ERR_UNSUPPORTED;
+  if (T <= 0 || E <= 0 || E > RT_EMAX || ldl < E || ldd < E || k < 1 || k > RT_KMAX || k > E) return SG_ERR_SHAPE;
+  if (!aligned(grad, 4) || !aligned(logits, dtype_size(l_dt)) || !aligned(ids, 4) ||
+      !aligned(dlogits, dtype_size(l_dt)))
+    return SG_ERR_ALIGN;
+  RouteGradArgs a;
+  a.grad = grad; a.logits = logits; a.ldl = ldl; a.T = T; a.E = (int)E; a.k = k; a.ids = ids;
+  a.sigmoid = score == SG_SCORE_SIGMOID; a.renorm = renormalize != 0; a.scale = scale;
+  a.out = dlogits; a.ldd = ldd;
+  clear_hip_error();
+  const bool all = score == SG_SCORE_SOFTMAX && !renormalize;
+  if (l_dt == SG_BF16) {
+    if (all) launch_route_grad<true, true>(a, stream);
+    else launch_route_grad<false, true>(a, stream);
+  } else {
+    if (all) launch_route_grad<true, false>(a, stream);
+    else launch_route_grad<false, false>(a, stream);
+  }
+  return launch_status();
+}
