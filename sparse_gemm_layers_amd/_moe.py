@@ -2,11 +2,16 @@
 (``sparse_gemm_layers_amd/include/sg_moe.h``).  Argument marshalling only."""
 
 import ctypes
+import functools
 
 import torch
 
-from ._binding import (SgError, _FB, _check, _dtype_code, _gpu2d, _i64, _int, _p, _positive, _ptr,
-                       _row_stride, _stream, _want, lib)
+from ._binding import SgError, _FB, _check, _i64, _int, _p, _positive, _ptr, _stream, lib
+
+# A call on a few tokens costs the host more than the GPU (a launch alone is 4 us), so
+# operands are checked by one expression each, which names the fault only where there is
+# one, and addresses go to ctypes as integers: a one-token linear layer took 12.5 us with
+# the other modules' helpers and takes 7.6 us with these.
 
 _f32 = ctypes.c_float
 
@@ -41,20 +46,56 @@ def _lib():
     return h
 
 
-def _want_rows(t, name, dtype, shape, device):
-    """A contiguous GPU tensor of one dtype and shape (None entries: any size)."""
+def _refuse(t, name, dtypes, shape, device):
+    """Raises with the first thing that is wrong about operand t."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise SgError(f"{name} must be a GPU tensor")
     if t.device != device:
         raise SgError(f"{name} is on {t.device}, the operands on {device}")
-    if t.dtype != dtype:
-        raise SgError(f"{name}: dtype {t.dtype} not supported ({str(dtype).replace('torch.', '')})")
-    if t.dim() != len(shape) or any(w is not None and w != h for w, h in zip(shape, t.shape)):
-        raise SgError(f"{name} must have shape [{', '.join('*' if w is None else str(w) for w in shape)}], "
-                      f"got {list(t.shape)}")
-    if not t.is_contiguous():
-        raise SgError(f"{name} must be contiguous")
-    return t
+    if t.dtype not in dtypes:
+        want = " or ".join(str(d).replace("torch.", "") for d in dtypes)
+        raise SgError(f"{name}: dtype {t.dtype} not supported ({want})")
+    if tuple(t.shape) != shape:
+        raise SgError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    raise SgError(f"{name} must be contiguous")
+
+
+def _rows(t, name, dtype, shape, device):
+    """Address of a contiguous GPU tensor of one dtype and shape."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape
+            and t.is_contiguous() and t.device == device):
+        _refuse(t, name, (dtype,), shape, device)
+    return t.data_ptr()
+
+
+def _matrix(t, name, dtypes):
+    """(rows, columns, row stride) of a GPU matrix with unit column stride, none of them 0."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise SgError(f"{name} must be a GPU tensor")
+    if t.dim() != 2:
+        raise SgError(f"{name} must be 2-D with unit column stride")
+    if t.dtype not in dtypes:
+        _refuse(t, name, dtypes, None, t.device)
+    r, c = t.shape
+    ld, one = t.stride()
+    if r < 1 or c < 1 or (one != 1 and c > 1):
+        raise SgError(f"{name} must be 2-D with unit column stride and no empty side, got {[r, c]}, strides {[ld, one]}")
+    return r, c, (ld if r > 1 else c)
+
+
+def _result(t, name, dtypes, shape, device):
+    """Row stride of an output matrix that the caller gave."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.device == device and t.dtype in dtypes and t.shape == shape):
+        _refuse(t, name, dtypes, shape, device)
+    return _matrix(t, name, dtypes)[2]
+
+
+def _current_stream(t):
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+_CODE = {torch.float32: 0, torch.bfloat16: 1}
+_BF = (torch.bfloat16,)
 
 
 def _score_code(score):
@@ -74,25 +115,29 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, n_group: int = 
     largest score + bias, "top2") stay.  Weights are the scores of the chosen,
     divided by their sum if `renormalize`, times `scale`.  Ties go to the lowest
     index; -inf or NaN takes an expert out."""
-    _gpu2d(logits, "logits")
-    T, E = logits.shape
-    _positive(T=T, E=E, k=k)
-    dt = _dtype_code(logits, "logits")
+    T, E, ld = _matrix(logits, "logits", _FB)
+    dev = logits.device
+    if k < 1:
+        raise SgError(f"k must be at least 1, got {k}")
     sc = _score_code(score)
     if group_score not in _GROUP_SCORES:
         raise SgError(f"group_score must be 'max' or 'top2', got {group_score!r}")
-    if bias is not None:
-        _want_rows(bias, "bias", torch.float32, (E,), logits.device)
+    pb = None if bias is None else _rows(bias, "bias", torch.float32, (E,), dev)
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        pi = ids.data_ptr()
+    else:
+        pi = _rows(ids, "ids", torch.int32, (T, k), dev)
     if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    _want_rows(ids, "ids", torch.int32, (T, k), logits.device)
-    _want_rows(weights, "weights", torch.float32, (T, k), logits.device)
-    st = _lib().sg_moe_route(_p(logits), dt, T, E, _row_stride(logits), _p(bias), k, sc, n_group, topk_group,
-                             _GROUP_SCORES[group_score], int(bool(renormalize)), scale, _p(ids), _p(weights),
-                             _stream(logits))
-    _check(st, "sg_moe_route")
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        pw = weights.data_ptr()
+    else:
+        pw = _rows(weights, "weights", torch.float32, (T, k), dev)
+    st = _lib().sg_moe_route(logits.data_ptr(), _CODE[logits.dtype], T, E, ld, pb, k, sc, n_group, topk_group,
+                             _GROUP_SCORES[group_score], 1 if renormalize else 0, scale, pi, pw,
+                             _current_stream(logits))
+    if st:
+        _check(st, "sg_moe_route")
     return ids, weights
 
 
@@ -101,22 +146,26 @@ def moe_route_backward(grad, logits, ids, score: str = "softmax", renormalize: b
     """Gradient of moe_route's weights: grad float32 [T, k], the logits and ids of
     the forward call -> dlogits [T, E] of the logits' dtype (the choice of experts
     held fixed; groups and bias enter through ids alone)."""
-    _gpu2d(logits, "logits")
-    T, E = logits.shape
-    _positive(T=T, E=E)
-    dt = _dtype_code(logits, "logits")
+    T, E, ld = _matrix(logits, "logits", _FB)
+    dev = logits.device
     sc = _score_code(score)
-    _want_rows(ids, "ids", torch.int32, (T, None), logits.device)
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise SgError("ids must be int32 [T, k]")
     k = ids.shape[1]
-    _positive(k=k)
-    _want_rows(grad, "grad", torch.float32, (T, k), logits.device)
+    if k < 1:
+        raise SgError("k must be at least 1, got 0")
+    pi = _rows(ids, "ids", torch.int32, (T, k), dev)
+    pg = _rows(grad, "grad", torch.float32, (T, k), dev)
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    _gpu2d(_want(dlogits, "dlogits", (logits.dtype,), (T, E), logits.device), "dlogits")
-    st = _lib().sg_moe_route_backward(_p(grad), _p(logits), dt, T, E, _row_stride(logits), _p(ids), k, sc,
-                                      int(bool(renormalize)), scale, _p(dlogits), _row_stride(dlogits),
-                                      _stream(logits))
-    _check(st, "sg_moe_route_backward")
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        ldd = E
+    else:
+        ldd = _result(dlogits, "dlogits", (logits.dtype,), (T, E), dev)
+    st = _lib().sg_moe_route_backward(pg, logits.data_ptr(), _CODE[logits.dtype], T, E, ld, pi, k, sc,
+                                      1 if renormalize else 0, scale, dlogits.data_ptr(), ldd,
+                                      _current_stream(logits))
+    if st:
+        _check(st, "sg_moe_route_backward")
     return dlogits
 
 
@@ -125,6 +174,7 @@ def w4_packed_bytes(n: int, k: int, gc: int = 128) -> int:
     return int(_lib().sg_w4_packed_bytes(n, k, gc))
 
 
+@functools.lru_cache(maxsize=1024)
 def _packed_bytes(n, k, gc):
     need = w4_packed_bytes(n, k, gc)
     if need < 0:
@@ -151,7 +201,7 @@ def w4_pack(wq, s, gc: int = 128, packed=None):
         raise SgError(f"s must have shape {[*batch, n, k // gc]}, got {list(s.shape)}")
     if packed is None:
         packed = torch.empty((*batch, need), dtype=torch.uint8, device=wq.device)
-    _want_rows(packed, "packed", torch.uint8, (*batch, need), wq.device)
+    _rows(packed, "packed", torch.uint8, (*batch, need), wq.device)
     ldw = wq.stride(-2) if n > 1 else k // 2
     st = _lib().sg_w4_pack(L, _p(wq), ldw, wq.stride(0) if L > 1 else 0, _p(s), s.stride(-2), s.stride(-1),
                            s.stride(0) if L > 1 else 0, n, k, gc, _p(packed), _stream(wq))
@@ -159,39 +209,38 @@ def w4_pack(wq, s, gc: int = 128, packed=None):
     return packed
 
 
-def _want_w4(w, name, need, device, batch=None):
-    if not isinstance(w, torch.Tensor) or not w.is_cuda or w.dtype != torch.uint8:
-        raise SgError(f"{name} must be a uint8 GPU tensor")
-    if w.device != device:
-        raise SgError(f"{name} is on {w.device}, the operands on {device}")
-    want = (need,) if batch is None else (batch, need)
-    if tuple(w.shape) != want or not w.is_contiguous():
-        raise SgError(f"{name} must be a contiguous packed weight {list(want)}, got {list(w.shape)}")
-
-
 def w4a16_gemm_groupwise_packed(x, wpacked, n: int, gc: int = 128, out_dtype=torch.bfloat16, bias=None, y=None):
     """Y [M, n] = X . W^T + bias: x bfloat16 [M, K], wpacked from w4_pack (n rows,
     groups of gc columns), bias float32 [n]; fp32 sums, bf16 or fp32 out."""
-    _gpu2d(x, "x")
-    if x.dtype != torch.bfloat16:
-        raise SgError("x must be bfloat16")
-    M, K = x.shape
-    _positive(M=M, N=n, K=K)
-    _want_w4(wpacked, "wpacked", _packed_bytes(n, K, gc), x.device)
-    if bias is not None:
-        _want_rows(bias, "bias", torch.float32, (n,), x.device)
+    M, K, ldx = _matrix(x, "x", _BF)
+    dev = x.device
+    pw = _rows(wpacked, "wpacked", torch.uint8, (_packed_bytes(n, K, gc),), dev)
+    pb = None if bias is None else _rows(bias, "bias", torch.float32, (n,), dev)
     if y is None:
-        y = torch.empty((M, n), dtype=out_dtype, device=x.device)
-    _gpu2d(_want(y, "y", _FB, (M, n), x.device), "y")
-    st = _lib().sg_w4a16_gemm_groupwise_packed(M, n, K, _p(x), _row_stride(x), _p(wpacked), gc, _p(bias), _p(y),
-                                               _dtype_code(y, "y"), _row_stride(y), _stream(x))
-    _check(st, "sg_w4a16_gemm_groupwise_packed")
+        if out_dtype not in _CODE:
+            raise SgError(f"out_dtype {out_dtype} not supported (float32 or bfloat16)")
+        y = torch.empty((M, n), dtype=out_dtype, device=dev)
+        ldy = n
+    else:
+        ldy = _result(y, "y", _FB, (M, n), dev)
+    st = _lib().sg_w4a16_gemm_groupwise_packed(M, n, K, x.data_ptr(), ldx, pw, gc, pb, y.data_ptr(), _CODE[y.dtype],
+                                               ldy, _current_stream(x))
+    if st:
+        _check(st, "sg_w4a16_gemm_groupwise_packed")
     return y
 
 
 def w4a16_moe_mlp_workspace(t: int, k: int, e: int, d: int, f: int) -> int:
     """Bytes of workspace of a w4a16_moe_mlp call (-1: sizes out of range)."""
     return int(_lib().sg_w4a16_moe_mlp_workspace(t, k, e, d, f))
+
+
+@functools.lru_cache(maxsize=1024)
+def _moe_need(t, k, e, d, f):
+    need = w4a16_moe_mlp_workspace(t, k, e, d, f)
+    if need < 0:
+        raise SgError(f"w4a16_moe_mlp: sizes out of range (T = {t}, k = {k}, E = {e}, D = {d}, F = {f})")
+    return need
 
 
 def w4a16_moe_mlp(x, ids, weights, gate, up, down, f: int, gc: int = 128, out_dtype=torch.bfloat16, y=None,
@@ -203,34 +252,37 @@ def w4a16_moe_mlp(x, ids, weights, gate, up, down, f: int, gc: int = 128, out_dt
     w4_pack of E weights [f, D], down of E weights [D, f].  workspace: uint8, at least
     w4a16_moe_mlp_workspace(T, k, E, D, f) bytes (allocated if not given; keep it
     to one stream)."""
-    _gpu2d(x, "x")
-    if x.dtype != torch.bfloat16:
-        raise SgError("x must be bfloat16")
-    T, D = x.shape
-    _positive(T=T, D=D, F=f)
-    _want_rows(ids, "ids", torch.int32, (T, None), x.device)
+    T, D, ldx = _matrix(x, "x", _BF)
+    dev = x.device
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise SgError("ids must be int32 [T, k]")
     k = ids.shape[1]
-    _positive(k=k)
-    _want_rows(weights, "weights", torch.float32, (T, k), x.device)
-    if not isinstance(gate, torch.Tensor) or gate.dim() != 2:
+    if k < 1 or f < 1:
+        raise SgError(f"k and F must be at least 1, got {k} and {f}")
+    pi = _rows(ids, "ids", torch.int32, (T, k), dev)
+    pr = _rows(weights, "weights", torch.float32, (T, k), dev)
+    if not isinstance(gate, torch.Tensor) or gate.dim() != 2 or gate.shape[0] < 1:
         raise SgError("gate must be packed weights [E, bytes]")
     E = gate.shape[0]
-    _positive(E=E)
-    _want_w4(gate, "gate", _packed_bytes(f, D, gc), x.device, E)
-    _want_w4(up, "up", _packed_bytes(f, D, gc), x.device, E)
-    _want_w4(down, "down", _packed_bytes(D, f, gc), x.device, E)
-    need = w4a16_moe_mlp_workspace(T, k, E, D, f)
-    if need < 0:
-        raise SgError(f"w4a16_moe_mlp: sizes out of range (T = {T}, k = {k}, E = {E}, D = {D}, F = {f})")
+    gu = (E, _packed_bytes(f, D, gc))
+    pg = _rows(gate, "gate", torch.uint8, gu, dev)
+    pu = _rows(up, "up", torch.uint8, gu, dev)
+    pd = _rows(down, "down", torch.uint8, (E, _packed_bytes(D, f, gc)), dev)
+    need = _moe_need(T, k, E, D, f)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or not workspace.is_contiguous() \
-            or workspace.numel() < need or workspace.device != x.device:
-        raise SgError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {x.device}")
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or not workspace.is_contiguous() \
+            or workspace.numel() < need or workspace.device != dev:
+        raise SgError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {dev}")
     if y is None:
-        y = torch.empty((T, D), dtype=out_dtype, device=x.device)
-    _gpu2d(_want(y, "y", _FB, (T, D), x.device), "y")
-    st = _lib().sg_w4a16_moe_mlp(T, k, E, D, f, _p(x), _row_stride(x), _p(ids), _p(weights), _p(gate), _p(up),
-                                 _p(down), gc, _p(y), _dtype_code(y, "y"), _row_stride(y), _p(workspace), workspace.numel(), _stream(x))
-    _check(st, "sg_w4a16_moe_mlp")
+        if out_dtype not in _CODE:
+            raise SgError(f"out_dtype {out_dtype} not supported (float32 or bfloat16)")
+        y = torch.empty((T, D), dtype=out_dtype, device=dev)
+        ldy = D
+    else:
+        ldy = _result(y, "y", _FB, (T, D), dev)
+    st = _lib().sg_w4a16_moe_mlp(T, k, E, D, f, x.data_ptr(), ldx, pi, pr, pg, pu, pd, gc, y.data_ptr(),
+                                 _CODE[y.dtype], ldy, workspace.data_ptr(), workspace.numel(), _current_stream(x))
+    if st:
+        _check(st, "sg_w4a16_moe_mlp")
     return y
