@@ -143,45 +143,47 @@ __global__ void __launch_bounds__(512) k_w4_rows(W4Args a) {
 #endif  // SG_DEVICE_PASS
 }
 
-// Many rows: tiles of 128 W rows x 256 X rows (w4_tile.h).
+// Many rows: tiles of 256 W rows x 128 X rows (w4_tile.h).
 template <int GC, bool OUT_BF16>
 __global__ void __launch_bounds__(512) k_w4_gemm(W4Args a, int tiles_m, int tiles_n) {
 #if SG_DEVICE_PASS
-  using T = W4Tile<GC, 2, 4, 4, 4>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * T::STAGE];
+  using T = W4Tile<GC>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   int tn, tm;
   tile_coords(tiles_m, tiles_n, tn, tm);
   const int64_t n0 = (int64_t)tn * T::BN, m0 = (int64_t)tm * T::BM;
-  const int KB = (int)((a.K + 127) >> 7);
   const int l = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int xrows = (int)min((int64_t)T::BM, a.M - m0);
-  const int64_t rb = (n0 >> 4) + wave;   // the row block this wave loads
-  const __amdgpu_buffer_rsrc_t rx = w4_rsrc(a.x + m0 * a.ldx, (uint32_t)(((xrows - 1) * a.ldx + a.K) * 2));
-  const __amdgpu_buffer_rsrc_t rw =
-      w4_rsrc(a.w + rb * KB * T::P::CHUNK, rb * 16 < a.N ? (uint32_t)(KB * T::P::CHUNK) : 0u);
-  uint32_t xoff[T::XL];
+  typename T::Src s;
+  s.K = (int)a.K;
+  s.KB = (int)((a.K + 127) >> 7);
+  s.x = a.x + m0 * a.ldx;
+  s.x_bytes = (uint32_t)(((xrows - 1) * a.ldx + a.K) * 2);
 #pragma unroll
-  for (int i = 0; i < T::XL; ++i) {
+  for (int i = 0; i < 2; ++i) {
+    const int64_t rb = (n0 >> 4) + 2 * wave + i;
+    s.w[i] = a.w + rb * s.KB * T::P::CHUNK;
+    s.w_bytes[i] = rb * 16 < a.N ? (uint32_t)(s.KB * T::P::CHUNK) : 0u;
     const int r = T::x_row(i, wave, l);
-    xoff[i] = r < xrows ? (uint32_t)(r * a.ldx * 2) : W4_OUT;
+    s.xoff[i] = r < xrows ? (uint32_t)(r * a.ldx * 2) : W4_OUT;
   }
-  v4f acc[T::IW][T::JW];
-  T::multiply(lds, rx, rw, xoff, KB, (int)a.K, wave, l, acc);
-  const int wn = wave % T::NW, wm = wave / T::NW, g = l >> 4, lr = l & 15;
+  v4f acc[2][8];
+  T::template multiply<4>(lds, s, wave, l, acc);
+  const int g = l >> 4, lr = l & 15;
 #pragma unroll
-  for (int i = 0; i < T::IW; ++i) {
-    const int64_t n = n0 + (wn * T::IW + i) * 16 + 4 * g;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t n = n0 + (2 * wave + i) * 16 + 4 * g;
     float b[4] = {0.f, 0.f, 0.f, 0.f};
     if (a.bias) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) b[e] = a.bias[min(n + e, a.N - 1)];
     }
 #pragma unroll
-    for (int j = 0; j < T::JW; ++j) {
+    for (int j = 0; j < 8; ++j) {
       v4f v;
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = fmaf(acc[i][j][e], W4_UNIT, b[e]);
-      store_quad<OUT_BF16, false>(a, m0 + (wm * T::JW + j) * 16 + lr, n, v);
+      store_quad<OUT_BF16, false>(a, m0 + j * 16 + lr, n, v);
     }
   }
 #endif  // SG_DEVICE_PASS
@@ -200,7 +202,7 @@ static void launch_w4_mt(const W4Args& a, hipStream_t st) {
 template <int GC, bool OUT_BF16>
 static void launch_w4(const W4Args& a, hipStream_t st) {
   if (a.M > 256) {
-    using T = W4Tile<GC, 2, 4, 4, 4>;
+    using T = W4Tile<GC>;
     const int64_t tm = cdiv(a.M, T::BM), tn = cdiv(a.N, T::BN);
     k_w4_gemm<GC, OUT_BF16><<<(unsigned)(tm * tn), 512, 0, st>>>(a, (int)tm, (int)tn);
     return;
@@ -249,7 +251,7 @@ extern "C" sg_status sg_w4a16_gemm_groupwise_packed(int64_t M, int64_t N, int64_
   if (M <= 0 || sg_w4_packed_bytes(N, K, gc) < 0 || ldx < K || ldy < N) return SG_ERR_SHAPE;
   // 32-bit buffer offsets: 256 X rows, and a tile's 8 row blocks of chunks; a 32-bit tile count
   if (ldx >= (1LL << 22) || cdiv(K, 128) * 8 * w4_chunk(gc) >= (1LL << 31)) return SG_ERR_SHAPE;
-  if (M >= (1LL << 31) || cdiv(M, 256) * cdiv(N, 128) > 0x7fffffffLL) return SG_ERR_SHAPE;
+  if (M >= (1LL << 31) || cdiv(M, 128) * cdiv(N, 256) > 0x7fffffffLL) return SG_ERR_SHAPE;
   if (!aligned(x, 16) || (ldx * 2) % 16 || !aligned(wpacked, 16) || !aligned(bias, 4) || !aligned(y, dtype_size(y_dt)))
     return SG_ERR_ALIGN;
   W4Args a;

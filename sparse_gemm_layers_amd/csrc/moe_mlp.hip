@@ -197,81 +197,94 @@ __global__ void __launch_bounds__(512) k_moe_down_rows(MoeArgs a) {
 #endif  // SG_DEVICE_PASS
 }
 
-// Many pairs per expert: tiles of MOE_BM pairs of one expert.  Gate and up: 64
-// rows of each, a wave's sub-tile rows 0, 1 are gate's and 2, 3 the same rows of up's.
+#if SG_DEVICE_PASS
+// The tile's product over its first `rows` pairs, in steps of 32.
+template <int GC>
+__device__ __forceinline__ void multiply_rows(uint8_t* lds, const typename W4Tile<GC>::Src& s, int rows, int wave,
+                                              int l, v4f (&acc)[2][8]) {
+  using T = W4Tile<GC>;
+  if (rows > 96) T::template multiply<4>(lds, s, wave, l, acc);
+  else if (rows > 64) T::template multiply<3>(lds, s, wave, l, acc);
+  else if (rows > 32) T::template multiply<2>(lds, s, wave, l, acc);
+  else T::template multiply<1>(lds, s, wave, l, acc);
+}
+#endif  // SG_DEVICE_PASS
+
+// Many pairs per expert: tiles of MOE_BM pairs of one expert.  Gate and up: 128
+// rows of each, a wave's first slot is gate's row block, its second the same of up's.
 template <int GC>
 __global__ void __launch_bounds__(512) k_moe_gate_up(MoeArgs a, int tiles_n) {
 #if SG_DEVICE_PASS
-  using T = W4Tile<GC, 2, 4, 4, 2>;
+  using T = W4Tile<GC>;
   static_assert(T::BM == MOE_BM, "tile");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * T::STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   const int tile = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
   if (tile >= a.tile[0]) return;
-  const int e = a.tile[1 + 2 * tile], m0 = a.tile[2 + 2 * tile], last = a.off[e + 1];
-  const int KB = (a.D + 127) >> 7;
+  const int e = a.tile[1 + 2 * tile], m0 = a.tile[2 + 2 * tile], rows = min(T::BM, a.off[e + 1] - m0);
   const int l = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int fb0 = tn * 4;   // first row block of the tile
-  // slot `wave`: sub-tile row wave % 4 of wave column wave / 4
-  const int fb = fb0 + (wave >> 2) * 2 + (wave & 1);
-  const uint8_t* const w = (wave & 2) ? a.up : a.gate;
-  const __amdgpu_buffer_rsrc_t rw = w4_rsrc(w + (int64_t)e * a.gu_bytes + (int64_t)fb * KB * T::P::CHUNK,
-                                            fb * 16 < a.F ? (uint32_t)(KB * T::P::CHUNK) : 0u);
-  const __amdgpu_buffer_rsrc_t rx = w4_rsrc(a.x, (uint32_t)(((a.T - 1) * a.ldx + a.D) * 2));
-  uint32_t xoff[T::XL];
+  typename T::Src s;
+  s.K = a.D;
+  s.KB = (a.D + 127) >> 7;
+  const int fb = tn * 8 + wave;
+  const int64_t at = (int64_t)e * a.gu_bytes + (int64_t)fb * s.KB * T::P::CHUNK;
+  s.w[0] = a.gate + at;
+  s.w[1] = a.up + at;
+  s.w_bytes[0] = s.w_bytes[1] = fb * 16 < a.F ? (uint32_t)(s.KB * T::P::CHUNK) : 0u;
+  s.x = a.x;
+  s.x_bytes = (uint32_t)(((a.T - 1) * a.ldx + a.D) * 2);
 #pragma unroll
-  for (int i = 0; i < T::XL; ++i) {
-    const int r = m0 + T::x_row(i, wave, l);
-    xoff[i] = r < last ? (uint32_t)((int64_t)(a.list[r] / a.k) * a.ldx * 2) : W4_OUT;
+  for (int u = 0; u < 2; ++u) {
+    const int r = T::x_row(u, wave, l);
+    s.xoff[u] = r < rows ? (uint32_t)((int64_t)(a.list[m0 + r] / a.k) * a.ldx * 2) : W4_OUT;
   }
-  v4f acc[T::IW][T::JW];
-  T::multiply(lds, rx, rw, xoff, KB, a.D, wave, l, acc);
-  const int wn = wave % T::NW, wm = wave / T::NW, g = l >> 4, lr = l & 15;
+  v4f acc[2][8];
+  multiply_rows<GC>(lds, s, rows, wave, l, acc);
+  const int f = fb * 16 + 4 * (l >> 4), lr = l & 15;
+  if (f >= a.F) return;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int j = 0; j < 8; ++j) {
+    if (16 * j + lr >= rows) continue;
+    float h[4];
 #pragma unroll
-    for (int j = 0; j < T::JW; ++j) {
-      const int f = (fb0 + wn * 2 + i) * 16 + 4 * g, r = m0 + (wm * T::JW + j) * 16 + lr;
-      if (r >= last || f >= a.F) continue;
-      float h[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) h[q] = silu(acc[i][j][q] * W4_UNIT) * (acc[i + 2][j][q] * W4_UNIT);
-      *reinterpret_cast<uint2*>(a.h + (int64_t)r * a.F + f) =
-          make_uint2(f32x2_to_bf16x2(h[0], h[1]), f32x2_to_bf16x2(h[2], h[3]));
-    }
+    for (int q = 0; q < 4; ++q) h[q] = silu(acc[0][j][q] * W4_UNIT) * (acc[1][j][q] * W4_UNIT);
+    *reinterpret_cast<uint2*>(a.h + (int64_t)(m0 + 16 * j + lr) * a.F + f) =
+        make_uint2(f32x2_to_bf16x2(h[0], h[1]), f32x2_to_bf16x2(h[2], h[3]));
+  }
 #endif  // SG_DEVICE_PASS
 }
 
 template <int GC>
 __global__ void __launch_bounds__(512) k_moe_down(MoeArgs a, int tiles_n) {
 #if SG_DEVICE_PASS
-  using T = W4Tile<GC, 2, 4, 4, 2>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * T::STAGE];
+  using T = W4Tile<GC>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   const int tile = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
   if (tile >= a.tile[0]) return;
-  const int e = a.tile[1 + 2 * tile], m0 = a.tile[2 + 2 * tile], last = a.off[e + 1];
-  const int KB = (a.F + 127) >> 7;
+  const int e = a.tile[1 + 2 * tile], m0 = a.tile[2 + 2 * tile], rows = min(T::BM, a.off[e + 1] - m0);
   const int l = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rb = tn * 8 + wave, rows = min(T::BM, last - m0);
-  const __amdgpu_buffer_rsrc_t rw = w4_rsrc(a.down + (int64_t)e * a.d_bytes + (int64_t)rb * KB * T::P::CHUNK,
-                                            rb * 16 < a.D ? (uint32_t)(KB * T::P::CHUNK) : 0u);
-  const __amdgpu_buffer_rsrc_t rx = w4_rsrc(a.h + (int64_t)m0 * a.F, (uint32_t)(rows * a.F * 2));
-  uint32_t xoff[T::XL];
+  typename T::Src s;
+  s.K = a.F;
+  s.KB = (a.F + 127) >> 7;
+  s.x = a.h + (int64_t)m0 * a.F;
+  s.x_bytes = (uint32_t)(rows * a.F * 2);
+  const int rb0 = tn * 16 + 2 * wave;
 #pragma unroll
-  for (int i = 0; i < T::XL; ++i) {
+  for (int i = 0; i < 2; ++i) {
+    s.w[i] = a.down + (int64_t)e * a.d_bytes + (int64_t)(rb0 + i) * s.KB * T::P::CHUNK;
+    s.w_bytes[i] = (rb0 + i) * 16 < a.D ? (uint32_t)(s.KB * T::P::CHUNK) : 0u;
     const int r = T::x_row(i, wave, l);
-    xoff[i] = r < rows ? (uint32_t)(r * a.F * 2) : W4_OUT;
+    s.xoff[i] = r < rows ? (uint32_t)(r * a.F * 2) : W4_OUT;
   }
-  v4f acc[T::IW][T::JW];
-  T::multiply(lds, rx, rw, xoff, KB, a.F, wave, l, acc);
-  const int wn = wave % T::NW, wm = wave / T::NW, g = l >> 4, lr = l & 15;
+  v4f acc[2][8];
+  multiply_rows<GC>(lds, s, rows, wave, l, acc);
+  const int g = l >> 4, lr = l & 15;
 #pragma unroll
-  for (int j = 0; j < T::JW; ++j) {
-    const int r = (wm * T::JW + j) * 16 + lr;
-    if (r >= rows) continue;
-    float* const row = a.o + (int64_t)a.list[m0 + r] * a.D;
+  for (int j = 0; j < 8; ++j) {
+    if (16 * j + lr >= rows) continue;
+    float* const row = a.o + (int64_t)a.list[m0 + 16 * j + lr] * a.D;
 #pragma unroll
-    for (int i = 0; i < T::IW; ++i) {
-      const int n = (tn * 8 + wn * T::IW + i) * 16 + 4 * g;
+    for (int i = 0; i < 2; ++i) {
+      const int n = (rb0 + i) * 16 + 4 * g;
       if (n < a.D) *reinterpret_cast<v4f*>(row + n) = acc[i][j] * W4_UNIT;
     }
   }
@@ -328,7 +341,7 @@ static void launch_moe(const MoeArgs& a, bool bf16, hipStream_t st) {
     k_moe_gate_up_rows<GC><<<dim3((unsigned)cdiv(a.F, 16), gy), 512, 0, st>>>(a);
     k_moe_down_rows<GC><<<dim3((unsigned)cdiv(a.D, 16), gy), 512, 0, st>>>(a);
   } else {
-    const int tm = (int)moe_tiles(a.P, a.E), ng = (int)cdiv(a.F, 64), nd = (int)cdiv(a.D, 128);
+    const int tm = (int)moe_tiles(a.P, a.E), ng = (int)cdiv(a.F, 128), nd = (int)cdiv(a.D, 256);
     k_moe_gate_up<GC><<<(unsigned)(tm * ng), 512, 0, st>>>(a, ng);
     k_moe_down<GC><<<(unsigned)(tm * nd), 512, 0, st>>>(a, nd);
   }

@@ -56,14 +56,15 @@ __device__ __forceinline__ float w4_code(uint32_t w) {
 
 // Eight codes -> eight bf16 (exact: a sixteenth of a 4-bit integer has at most
 // three significant bits), 13 instructions: 8 conversions that pick their byte,
-// one shift for the odd codes, 4 joins of two high halves.
+// one shift for the odd codes, 4 joins of two high halves.  w4_pair<B> is the
+// B-th pair.
+template <int B>
+__device__ __forceinline__ int w4_pair(int code) {
+  return (int)__builtin_amdgcn_perm(__float_as_uint(w4_code<B>((uint32_t)code >> 4)),
+                                    __float_as_uint(w4_code<B>((uint32_t)code)), 0x07060302u);
+}
 __device__ __forceinline__ v4i w4_widen(int code) {
-  const uint32_t w = (uint32_t)code, h = w >> 4;
-  const auto join = [](float a, float b) {
-    return (int)__builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-  };
-  return (v4i){join(w4_code<0>(w), w4_code<0>(h)), join(w4_code<1>(w), w4_code<1>(h)),
-               join(w4_code<2>(w), w4_code<2>(h)), join(w4_code<3>(w), w4_code<3>(h))};
+  return (v4i){w4_pair<0>(code), w4_pair<1>(code), w4_pair<2>(code), w4_pair<3>(code)};
 }
 
 __device__ __forceinline__ v4f w4_mfma(const v4i& a, const v4i& b, const v4f& c) {

@@ -1,111 +1,229 @@
-// Tile product of the 4-bit-weight kernels at many rows: BN W rows x BM X rows
-// per workgroup of 8 waves in an NW (W) x MW (X) grid, each wave IW x JW
-// sub-tiles of 16 x 16.  One 128-wide K block per LDS stage, two stages: the
-// waves multiply stage kb while kb + 1 streams in by buffer loads that write
-// LDS.  Stage layout (bytes): X, BM rows of 256 B whose 16-byte piece c lies at
-// c ^ (row & 15), so that the 16 rows of an operand read hit different banks;
-// the 8 row blocks' codes as packed, 1 KB each; their scales, 256 B each.  Slot
-// s of the row blocks is sub-tile row s % IW of wave column s / IW.
+// Tile product of the 4-bit-weight kernels at many rows: 256 W rows x up to 128
+// X rows per workgroup of 8 waves.  A wave owns 32 W rows (two row blocks,
+// "slots" 2 w and 2 w + 1) and every X row, so each code is widened by one wave
+// alone: widening (13 instructions per 8 codes) is what the vector unit mostly
+// does.  2048 x 4096 x 4096 with groups of 128: 70 us, 980 TFLOP/s at the 1.8 GHz
+// that the card holds under this load, the matrix cores busy in 53% of its
+// cycles; a 2 x 4 grid of waves, which widens each code four times, took 83 us.
+// The price is that every wave reads every X row from LDS.
+//
+// A K block is one stage of a ring of three.  A wave's own codes and scales are
+// loaded one K block ahead of X, so that they are widened while the block
+// before is multiplied; X operands are read one pair of sub-tile columns ahead.
+// The block's single barrier stands before its last pair, whose operands are in
+// registers by then: it frees the block's stage for the loads of block kb + 3
+// and opens that of kb + 1.
+//
+// Stage (bytes): X in two halves of 64 columns, 128 rows of 128 B each, the
+// 16-byte piece c of row r at c ^ swz8q(r); the 16 slots' codes as packed, 1 KB
+// each.  The slots' scales, 256 B each, have a ring of four of their own.
 #pragma once
+
+#include <type_traits>
 
 #include "tile_epilogue.h"
 #include "w4.h"
 
 namespace sg {
 
-template <int GC, int NW_, int MW_, int IW_, int JW_>
+template <int GC>
 struct W4Tile {
   using P = W4<GC>;
-  static constexpr int NW = NW_, MW = MW_, IW = IW_, JW = JW_;
-  static_assert(NW * MW == 8, "8 waves");
-  static constexpr int BN = NW * IW * 16, BM = MW * JW * 16;
-  static_assert(BN == 128, "one W row block per wave and stage");
-  static constexpr int W_OFF = BM * 256, S_OFF = W_OFF + 8 * W4_CODES, STAGE = S_OFF + 8 * 256;
-  static_assert(2 * STAGE <= 160 * 1024, "LDS");
-  static constexpr int XL = BM / 32;      // X loads per wave and stage: 4 rows each
+  static constexpr int BN = 256, BM = 128;
+  static constexpr int W_OFF = BM * 256, STAGE = W_OFF + 16 * W4_CODES;
+  static constexpr int S_OFF = 3 * STAGE, S_STAGE = 16 * 256;   // scales: a ring of four
+  static constexpr int LDS = S_OFF + 4 * S_STAGE;
+  static_assert(LDS <= 160 * 1024, "LDS");
+  static constexpr int LOADS = 8;   // of one wave and stage
 
 #if SG_DEVICE_PASS
-  // The X row that lane l's load i fills.
-  __device__ static __forceinline__ int x_row(int i, int wave, int l) { return 4 * (8 * i + wave) + (l >> 4); }
+  struct Src {
+    const void *x, *w[2];             // w: this wave's two row blocks, each from its first chunk
+    uint32_t x_bytes, w_bytes[2];     // at most 2^31; 0: the row block is not there
+    uint32_t xoff[2];                 // byte offset in x of this lane's rows, W4_OUT: not there
+    int K, KB;
+  };
+  // The X rows that lane l loads, u = 0, 1.
+  __device__ static __forceinline__ int x_row(int u, int wave, int l) { return 8 * (8 * u + wave) + (l >> 3); }
 
-  // rw: the row block that this wave loads (slot `wave` of the stage).  Its
-  // scales take 64 NG of the 256 bytes that one load of 4 bytes a lane fills.
-  __device__ static __forceinline__ void issue(uint8_t* st, __amdgpu_buffer_rsrc_t rx, __amdgpu_buffer_rsrc_t rw,
-                                               const uint32_t (&xoff)[XL], int kb, int K, int wave, int l) {
-    // rows 4 (8 i + wave) + (l >> 4): the same row mod 16 for every i
-    const int c = (l & 15) ^ ((4 * wave + (l >> 4)) & 15);
-    const bool in = kb * 128 + c * 8 < K;
-#pragma unroll
-    for (int i = 0; i < XL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (w4_lds_t*)(st + (8 * i + wave) * 1024), 16,
-                                               in && xoff[i] != W4_OUT ? xoff[i] + c * 16 : W4_OUT, kb * 256, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (w4_lds_t*)(st + W_OFF + wave * W4_CODES), 16, (uint32_t)(16 * l),
-                                             kb * P::CHUNK, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (w4_lds_t*)(st + S_OFF + wave * 256), 4,
-                                             l < 16 * P::NG ? (uint32_t)(W4_CODES + 4 * l) : W4_OUT, kb * P::CHUNK, 0,
-                                             0);
-  }
 
-  __device__ static __forceinline__ void compute(const uint8_t* st, int wn, int wm, int l, v4f (&acc)[IW][JW]) {
+  // acc[i][j] (rows of slot 2 wave + i, X rows 16 j + l % 16, in units of
+  // W4_UNIT) over all K blocks, for the first 32 JP X rows.
+  template <int JP>
+  __device__ static __forceinline__ void multiply(uint8_t* lds, const Src& s, int wave, int l, v4f (&acc)[2][8]) {
     const int g = l >> 4, lr = l & 15;
-    v4i aw[IW][4];
-    v4f sw[IW][P::NG];
 #pragma unroll
-    for (int i = 0; i < IW; ++i) {
-      const int rb = wn * IW + i;
-      const v4i cw = *reinterpret_cast<const v4i*>(st + W_OFF + rb * W4_CODES + 16 * l);
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) aw[i][q] = w4_widen(cw[q]);
-#pragma unroll
-      for (int u = 0; u < P::NG; ++u)
-        sw[i][u] = *reinterpret_cast<const v4f*>(st + S_OFF + rb * 256 + u * 64 + 16 * g);
-    }
-#pragma unroll
-    for (int j = 0; j < JW; ++j) {
-      v4i bx[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        bx[q] = *reinterpret_cast<const v4i*>(st + ((wm * JW + j) * 16 + lr) * 256 + (((4 * q + g) ^ lr) << 4));
-#pragma unroll
-      for (int i = 0; i < IW; ++i)
-#pragma unroll
-        for (int u = 0; u < P::NG; ++u) {
-          v4f p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int q = u * P::QPG; q < (u + 1) * P::QPG; ++q) p = w4_mfma(aw[i][q], bx[q], p);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(p[e], sw[i][u][e], acc[i][j][e]);
-        }
-    }
-  }
+      for (int j = 0; j < 8; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+    int cur = 0, nxt = STAGE, far = 2 * STAGE;   // the stages of kb, kb + 1, kb + 2
 
-  // acc = the wave's sums (in units of W4_UNIT) over all K blocks.  xoff: byte
-  // offset of each of the lane's X rows in rx, W4_OUT for a row that is not there.
-  __device__ static __forceinline__ void multiply(uint8_t* lds, __amdgpu_buffer_rsrc_t rx, __amdgpu_buffer_rsrc_t rw,
-                                                  const uint32_t (&xoff)[XL], int KB, int K, int wave, int l,
-                                                  v4f (&acc)[IW][JW]) {
+    // Loads past the last K block go through descriptors without records: they
+    // read zeros and touch no memory.  The columns past K of the last block are W4_OUT.
+    const int c = 8 * ((l & 7) ^ swz8q(l >> 3));   // first column of this lane's piece; its rows mod 8 are l >> 3
+    uint32_t xv[2][2], xlast[2][2];
 #pragma unroll
-    for (int i = 0; i < IW; ++i)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int j = 0; j < JW; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-    const int wn = wave % NW, wm = wave / NW;
-    uint8_t* const s0 = lds;
-    uint8_t* const s1 = lds + STAGE;
-    issue(s0, rx, rw, xoff, 0, K, wave, l);
-    wait_vmcnt<0>();
-    __syncthreads();
-    for (int kb = 0; kb < KB; kb += 2) {
-      if (kb + 1 < KB) issue(s1, rx, rw, xoff, kb + 1, K, wave, l);
-      compute(s0, wn, wm, l, acc);
-      wait_vmcnt<0>();
-      __syncthreads();
-      if (kb + 1 < KB) {
-        if (kb + 2 < KB) issue(s0, rx, rw, xoff, kb + 2, K, wave, l);
-        compute(s1, wn, wm, l, acc);
-        wait_vmcnt<0>();
-        __syncthreads();
+      for (int h = 0; h < 2; ++h) {
+        xv[u][h] = s.xoff[u] == W4_OUT ? W4_OUT : s.xoff[u] + 2 * (64 * h + c);
+        xlast[u][h] = (s.KB - 1) * 128 + 64 * h + c < s.K ? xv[u][h] : W4_OUT;
       }
+    const uint32_t cv = 16 * l, sv = l < 16 * P::NG ? (uint32_t)(W4_CODES + 4 * l) : W4_OUT;
+    const auto load_codes = [&](int i, int stage, int kb) {
+      const bool in = kb < s.KB;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(w4_rsrc(s.w[i], in ? s.w_bytes[i] : 0u),
+                                               (w4_lds_t*)(lds + stage + W_OFF + (2 * wave + i) * W4_CODES), 16, cv,
+                                               in ? kb * P::CHUNK : 0, 0, 0);
+    };
+    // load group b: codes of b + 1, scales and X of b, one at a time
+    const auto load_one = [&](int n, int codes, int x, int b) {
+      const bool in = b < s.KB;
+      if (n < 2) {
+        load_codes(n, codes, b + 1);
+      } else if (n < 4) {
+        const int i = n - 2;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            w4_rsrc(s.w[i], in ? s.w_bytes[i] : 0u),
+            (w4_lds_t*)(lds + S_OFF + (b & 3) * S_STAGE + (2 * wave + i) * 256), 4, sv, in ? b * P::CHUNK : 0, 0, 0);
+      } else {
+        const int u = (n - 4) >> 1, h = n & 1;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            w4_rsrc(s.x, in ? s.x_bytes : 0u), (w4_lds_t*)(lds + x + h * (BM * 128) + (8 * u + wave) * 1024), 16,
+            b == s.KB - 1 ? xlast[u][h] : xv[u][h], in ? b * 256 : 0, 0, 0);
+      }
+    };
+    const auto load = [&](int codes, int x, int b) {
+#pragma unroll
+      for (int n = 0; n < LOADS; ++n) load_one(n, codes, x, b);
+    };
+    load_codes(0, cur, 0);
+    load_codes(1, cur, 0);
+    load(nxt, cur, 0);
+    load(far, nxt, 1);
+    const int q0 = lr * 128 + ((g ^ swz8q(lr)) << 4), q1 = lr * 128 + (((4 + g) ^ swz8q(lr)) << 4);
+    const int wo = W_OFF + 2 * wave * W4_CODES + 16 * l, so = S_OFF + 2 * wave * 256 + 16 * g;   // of this wave's two slots
+    // X operands of pair jj, columns 32 q .. 32 q + 31
+    const auto read_x = [&](v4i (&bx)[2][4], int stage, int jj, int q) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        bx[b][q] = *reinterpret_cast<const v4i*>(lds + stage + (q & 1 ? q1 : q0) + (q >> 1) * (BM * 128) +
+                                                 (2 * jj + b) * 2048);
+    };
+
+    v4i aw[2][2][4], bx[2][4], cw[2];
+    v4f p[2][2][2], sw[2][2];   // sums of the group in work and of the one before, and their scales
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sw[t][i] = (v4f){0.f, 0.f, 0.f, 0.f};
+        p[t][i][0] = p[t][i][1] = sw[t][i];
+      }
+    wait_vmcnt<2 * LOADS>();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) cw[i] = *reinterpret_cast<const v4i*>(lds + cur + wo + i * W4_CODES);
+    lds_barrier();           // block 0's codes are in registers: block 3's may take their place
+    load(cur, far, 2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) aw[0][i][q] = w4_widen(cw[i][q]);
+    wait_vmcnt<2 * LOADS>();
+    lds_barrier();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) read_x(bx, cur, 0, q);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) cw[i] = *reinterpret_cast<const v4i*>(lds + nxt + wo + i * W4_CODES);
+
+    // One K block: JP pairs of sub-tile columns, 16 matrix instructions each.
+    // What else there is to do is spread between those by hand, and the order is
+    // kept: the compiler's own left the matrix cores idle half of the time, both
+    // waves of a SIMD widening or both multiplying.  After each matrix
+    // instruction come, where due, the scaling of one 16 x 16 sum of the group
+    // before, a part of the next block's widening, the operands of the next
+    // pair in place of those just used, and a load of block kb + 3.
+    // PA: which half of aw holds this block; PU: which of p its first group.
+    const auto block = [&](int kb, auto pa, auto pu) {
+      constexpr int PA = decltype(pa)::value, PU = decltype(pu)::value;
+      constexpr int L = 4 * P::QPG;   // matrix instructions per group
+      const uint8_t* const sp = lds + so + (kb & 3) * S_STAGE;
+      v4i ahead[2];   // codes of kb + 2
+#pragma unroll
+      for (int jj = 0; jj < JP; ++jj) {
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+          const int q = t >> 2, i = (t >> 1) & 1, c = t & 1;
+          const int u = jj * P::NG + t / L, in = t % L;   // group of the block, instruction of the group
+          const int now = (PU + u) & 1, old = now ^ 1;
+          const int oj = u == 0 ? JP - 1 : (u - 1) / P::NG;   // pair of the group before
+          if (in == 0) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              sw[now][k] = *reinterpret_cast<const v4f*>(sp + k * 256 + (t / L) * 64);
+          }
+          p[now][i][c] = w4_mfma(aw[PA][i][q], bx[c][q], in < 4 ? (v4f){0.f, 0.f, 0.f, 0.f} : p[now][i][c]);
+          if (in % P::QPG == P::QPG / 2) {
+            const int k = in / P::QPG, ki = k >> 1, kc = k & 1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[ki][2 * oj + kc][e] = fmaf(p[old][ki][kc][e], sw[old][ki][e], acc[ki][2 * oj + kc][e]);
+          }
+#pragma unroll
+          for (int d = (jj * 16 + t) * 2 / JP; d < (jj * 16 + t + 1) * 2 / JP; ++d) {
+            const int wi = (d >> 2) & 1, wq = d >> 3;
+            const int w = cw[wi][wq];
+            aw[PA ^ 1][wi][wq][d & 3] = (d & 3) == 0   ? w4_pair<0>(w)
+                                        : (d & 3) == 1 ? w4_pair<1>(w)
+                                        : (d & 3) == 2 ? w4_pair<2>(w)
+                                                       : w4_pair<3>(w);
+          }
+          if (jj == JP - 1) {
+            if (t == 2) {
+              // own loads of kb + 1 have landed (kb + 2's may fly); every wave holds its last operands of kb
+              wait_vmcnt<LOADS>();
+              lds_barrier();
+            }
+            if (t == 11) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) ahead[k] = *reinterpret_cast<const v4i*>(lds + far + wo + k * W4_CODES);
+            }
+            if (t >= 3 && t < 11) load_one(t - 3, nxt, cur, kb + 3);   // block kb + 1's codes are in registers
+          }
+          if ((t & 3) == 3) {
+            if (jj < JP - 1) read_x(bx, cur, jj + 1, q);
+            else read_x(bx, nxt, 0, q);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) cw[i] = ahead[i];
+      const int was = cur;
+      cur = nxt;
+      nxt = far;
+      far = was;
+    };
+    using Z = std::integral_constant<int, 0>;
+    using O = std::integral_constant<int, 1>;
+    using S1 = std::integral_constant<int, (JP * P::NG) & 1>;   // an odd number of groups leaves p the other way round
+    int kb = 0;
+    for (; kb + 1 < s.KB; kb += 2) {
+      block(kb, Z{}, Z{});
+      block(kb + 1, O{}, S1{});
     }
+    if (kb < s.KB) block(kb, Z{}, Z{});
+    // the last group's sums; which of p holds them depends on the parity of all groups
+    const bool odd = ((s.KB * JP * P::NG) & 1) != 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[i][2 * JP - 2 + c][e] = fmaf(odd ? p[0][i][c][e] : p[1][i][c][e], odd ? sw[0][i][e] : sw[1][i][e],
+                                           acc[i][2 * JP - 2 + c][e]);
+    wait_vmcnt<0>();   // loads past the end write their zeros before LDS is given up
   }
 #endif  // SG_DEVICE_PASS
 };
