@@ -6,7 +6,7 @@
 // core with fp32 sums; each group's partial sum is scaled in fp32, so the
 // weight is never rounded.  W is the left operand: lane 16 g + r of a result
 // tile holds columns n = 4 g .. 4 g + 3 of row m = r.
-#include "w4.h"
+#include "w4_rows.h"
 #include "w4_tile.h"
 #include "sg_moe.h"
 
@@ -60,85 +60,61 @@ struct W4Args {
   int vec_store;
 };
 
-// Few rows (M <= 64 per grid row): a workgroup owns RB blocks of 16 W rows and
-// 16 MT X rows; its 8 waves split the K blocks and add their partial tiles in
-// LDS.  Operands come straight into registers: the packed codes are one
-// 16-byte load per lane, X rows come from L2.
-template <int GC, int RB, int MT, bool OUT_BF16>
-__global__ void __launch_bounds__(512) k_w4_rows(W4Args a) {
+// Few rows: a workgroup owns RB blocks of 16 W rows and 4 XI X rows; its 8
+// waves split the K blocks (w4_rows.h) and add their partial tiles in LDS.
+template <int GC, int RB, int XI>
+__global__ void __launch_bounds__(512) k_w4_rows(W4Args a, int out_bf16) {
 #if SG_DEVICE_PASS
-  using P = W4<GC>;
-  __shared__ __attribute__((aligned(16))) float red[W4_WAVES][RB * MT][64][4];
-  const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
+  using T = W4Rows<GC, RB, XI>;
+  constexpr int MT = T::MT;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+  const int t = threadIdx.x, l = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int KB = (int)((a.K + 127) >> 7);
-  const int64_t rb0 = (int64_t)blockIdx.x * RB, m0 = (int64_t)blockIdx.y * (16 * MT);
-  const int nrb = (int)min((int64_t)RB, ((a.N + 15) >> 4) - rb0);
-  const int xrows = (int)min((int64_t)(16 * MT), a.M - m0);
-  const __amdgpu_buffer_rsrc_t rw = w4_rsrc(a.w + rb0 * KB * P::CHUNK, (uint32_t)(nrb * KB * P::CHUNK));
-  const __amdgpu_buffer_rsrc_t rx = w4_rsrc(a.x + m0 * a.ldx, (uint32_t)(((xrows - 1) * a.ldx + a.K) * 2));
-
+  const int64_t rb0 = (int64_t)blockIdx.x * RB, m0 = (int64_t)blockIdx.y * (4 * XI);
+  const int xrows = (int)min((int64_t)(4 * XI), a.M - m0);
+  typename T::Src s;
+  s.K = (int)a.K;
+  s.KB = (int)((a.K + 127) >> 7);
+  s.x = a.x + m0 * a.ldx;
+  s.x_bytes = (uint32_t)(((xrows - 1) * a.ldx + a.K) * 2);
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    s.w[rb] = a.w + (rb0 + rb) * s.KB * T::P::CHUNK;
+    s.w_bytes[rb] = (rb0 + rb) * 16 < a.N ? (uint32_t)(s.KB * T::P::CHUNK) : 0u;
+  }
+#pragma unroll
+  for (int i = 0; i < XI; ++i) {
+    const int r = 4 * i + (l >> 4);
+    s.xoff[i] = r < xrows ? (uint32_t)(r * a.ldx * 2) : W4_OUT;
+  }
   v4f acc[RB][MT];
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[rb][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+  T::multiply(lds + wave * T::WAVE_LDS, s, wave, W4_WAVES, l, acc);
 
-  for (int kb = wave; kb < KB; kb += W4_WAVES) {
-    v4i cw[RB], bx[MT][4];
-    v4f sw[RB][P::NG];
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      cw[rb] = w4_ld16(rw, (uint32_t)(rb * KB * P::CHUNK + 16 * l), kb * P::CHUNK);
-#pragma unroll
-      for (int u = 0; u < P::NG; ++u)
-        sw[rb][u] = __builtin_bit_cast(
-            v4f, w4_ld16(rw, (uint32_t)(rb * KB * P::CHUNK + W4_CODES + 64 * u + 16 * g), kb * P::CHUNK));
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const bool in = kb * 128 + 32 * q + 8 * g < a.K;
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const int r = 16 * j + lr;
-        bx[j][q] = w4_ld16(rx, in && r < xrows ? (uint32_t)(r * a.ldx * 2 + 64 * q + 16 * g) : W4_OUT, kb * 256);
-      }
-    }
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-      v4i aw[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) aw[q] = w4_widen(cw[rb][q]);
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int u = 0; u < P::NG; ++u) {
-          v4f p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int q = u * P::QPG; q < (u + 1) * P::QPG; ++q) p = w4_mfma(aw[q], bx[j][q], p);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[rb][j][e] = fmaf(p[e], sw[rb][u][e], acc[rb][j][e]);
-        }
-    }
-  }
-
+  __syncthreads();
+  float(*const red)[RB * MT][64][4] = reinterpret_cast<float(*)[RB * MT][64][4]>(lds);
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
     for (int j = 0; j < MT; ++j) *reinterpret_cast<v4f*>(&red[wave][rb * MT + j][l][0]) = acc[rb][j];
   __syncthreads();
   for (int q = t; q < RB * MT * 64; q += 512) {
-    const int s = q >> 6, ll = q & 63, rb = s / MT, j = s % MT;
+    const int s2 = q >> 6, ll = q & 63, rb = s2 / MT, j = s2 % MT;
+    if (16 * j + (ll & 15) >= xrows) continue;
     v4f v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int w = 0; w < W4_WAVES; ++w) v += *reinterpret_cast<const v4f*>(&red[w][s][ll][0]);
+    for (int w = 0; w < W4_WAVES; ++w) v += *reinterpret_cast<const v4f*>(&red[w][s2][ll][0]);
     const int64_t n = (rb0 + rb) * 16 + 4 * (ll >> 4);
     v *= W4_UNIT;
     if (a.bias) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] += a.bias[min(n + e, a.N - 1)];
     }
-    store_quad<OUT_BF16, false>(a, m0 + 16 * j + (ll & 15), n, v);
+    if (out_bf16) store_quad<true, false>(a, m0 + 16 * j + (ll & 15), n, v);
+    else store_quad<false, false>(a, m0 + 16 * j + (ll & 15), n, v);
   }
 #endif  // SG_DEVICE_PASS
 }
@@ -189,28 +165,49 @@ __global__ void __launch_bounds__(512) k_w4_gemm(W4Args a, int tiles_m, int tile
 #endif  // SG_DEVICE_PASS
 }
 
-template <int GC, int MT, bool OUT_BF16>
-static void launch_w4_mt(const W4Args& a, hipStream_t st) {
-  const int64_t rows16 = cdiv(a.N, 16);
-  const unsigned gy = (unsigned)cdiv(a.M, 16 * MT);
-  if (MT > 1 && rows16 * gy >= 2 * 224)
-    k_w4_rows<GC, 2, MT, OUT_BF16><<<dim3((unsigned)cdiv(rows16, 2), gy), 512, 0, st>>>(a);
-  else
-    k_w4_rows<GC, 1, MT, OUT_BF16><<<dim3((unsigned)rows16, gy), 512, 0, st>>>(a);
+template <int GC, int RB, int XI>
+static void launch_w4_rows(const W4Args& a, bool b16, hipStream_t st) {
+  k_w4_rows<GC, RB, XI><<<dim3((unsigned)cdiv(a.N, 16 * RB), (unsigned)cdiv(a.M, 4 * XI)), 512, 0, st>>>(a, b16);
 }
 
-template <int GC, bool OUT_BF16>
-static void launch_w4(const W4Args& a, hipStream_t st) {
-  if (a.M > 256) {
+// Time of the busiest compute unit per K block of 128, in units that make one
+// wave of workgroups comparable: rb blocks of W rows and 4 xi X rows each
+// (w4_rows.h), or one 256 x 128 tile.  4096 x 4096 at 64 rows: xi 8, rb 2 (308)
+// 7.8 us, 12, 2 (372) 9.0, 16, 2 (436) 10.1, 16, 4 (616) 14.0; tiles 50.5.
+static int64_t w4_rows_cost(int64_t M, int64_t N, int rb, int xi) {
+  return cdiv(cdiv(N, 16 * rb) * cdiv(M, 4 * xi), 256) * (16 * xi + 90 * rb);
+}
+static int64_t w4_tile_cost(int64_t M, int64_t N) { return cdiv(cdiv(N, 256) * cdiv(M, 128), 256) * 2400; }
+
+template <int GC>
+static void launch_w4(const W4Args& a, bool b16, hipStream_t st) {
+  int rb = 1, xi = a.M <= 4 ? 1 : a.M <= 8 ? 2 : 4;
+  if (a.M > 8)
+    for (int x = 4; x <= 16 && 4 * x < a.M + 16; x += 4)
+      for (int r = 1; r <= (x == 4 ? 2 : 4); r *= 2)
+        if (w4_rows_cost(a.M, a.N, r, x) < w4_rows_cost(a.M, a.N, rb, xi)) rb = r, xi = x;
+  if (cdiv(a.M, 4 * xi) > 65535 || w4_tile_cost(a.M, a.N) < w4_rows_cost(a.M, a.N, rb, xi)) {
     using T = W4Tile<GC>;
     const int64_t tm = cdiv(a.M, T::BM), tn = cdiv(a.N, T::BN);
-    k_w4_gemm<GC, OUT_BF16><<<(unsigned)(tm * tn), 512, 0, st>>>(a, (int)tm, (int)tn);
+    if (b16) k_w4_gemm<GC, true><<<(unsigned)(tm * tn), 512, 0, st>>>(a, (int)tm, (int)tn);
+    else k_w4_gemm<GC, false><<<(unsigned)(tm * tn), 512, 0, st>>>(a, (int)tm, (int)tn);
     return;
   }
-  if (a.M <= 16) launch_w4_mt<GC, 1, OUT_BF16>(a, st);
-  else if (a.M <= 32) launch_w4_mt<GC, 2, OUT_BF16>(a, st);
-  else if (a.M <= 48) launch_w4_mt<GC, 3, OUT_BF16>(a, st);
-  else launch_w4_mt<GC, 4, OUT_BF16>(a, st);
+  switch (10 * xi + rb) {
+    case 11: launch_w4_rows<GC, 1, 1>(a, b16, st); break;
+    case 21: launch_w4_rows<GC, 1, 2>(a, b16, st); break;
+    case 41: launch_w4_rows<GC, 1, 4>(a, b16, st); break;
+    case 42: launch_w4_rows<GC, 2, 4>(a, b16, st); break;
+    case 81: launch_w4_rows<GC, 1, 8>(a, b16, st); break;
+    case 82: launch_w4_rows<GC, 2, 8>(a, b16, st); break;
+    case 84: launch_w4_rows<GC, 4, 8>(a, b16, st); break;
+    case 121: launch_w4_rows<GC, 1, 12>(a, b16, st); break;
+    case 122: launch_w4_rows<GC, 2, 12>(a, b16, st); break;
+    case 124: launch_w4_rows<GC, 4, 12>(a, b16, st); break;
+    case 161: launch_w4_rows<GC, 1, 16>(a, b16, st); break;
+    case 162: launch_w4_rows<GC, 2, 16>(a, b16, st); break;
+    default: launch_w4_rows<GC, 4, 16>(a, b16, st); break;
+  }
 }
 
 }  // namespace sg
@@ -260,9 +257,9 @@ extern "C" sg_status sg_w4a16_gemm_groupwise_packed(int64_t M, int64_t N, int64_
   clear_hip_error();
   const bool b16 = y_dt == SG_BF16;
   switch (gc) {
-    case 32: b16 ? launch_w4<32, true>(a, stream) : launch_w4<32, false>(a, stream); break;
-    case 64: b16 ? launch_w4<64, true>(a, stream) : launch_w4<64, false>(a, stream); break;
-    default: b16 ? launch_w4<128, true>(a, stream) : launch_w4<128, false>(a, stream); break;
+    case 32: launch_w4<32>(a, b16, stream); break;
+    case 64: launch_w4<64>(a, b16, stream); break;
+    default: launch_w4<128>(a, b16, stream); break;
   }
   return launch_status();
 }

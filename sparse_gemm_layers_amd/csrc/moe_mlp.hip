@@ -1,14 +1,17 @@
 // The routed gated MLP on 4-bit expert weights:
 //   y[t] = sum_j w[t, j] Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),  e = ids[t, j].
 //
-// Four launches.  (1) The pairs (t, j) are sorted by expert.  (2) Gate and up
-// products of each expert's pairs, x rows gathered by token, silu(g) u in the
-// epilogue, h in bf16 (the down product's operand on the matrix core: one
-// rounding of half a step, at most 2^-8 of the value).  (3) Down products, one fp32 row
-// per pair.  (4) Each token's k rows are weighted and summed in fp32 in slot
-// order, so results do not depend on the order of pairs within an expert.
+// Many pairs per expert, four launches.  (1) The pairs (t, j) are sorted by
+// expert.  (2) Gate and up products of each expert's pairs, x rows gathered by
+// token, silu(g) u in the epilogue, h in bf16 (the down product's operand on the
+// matrix core: one rounding of half a step, at most 2^-8 of the value).  (3) Down
+// products, one fp32 row per pair.  (4) Each token's k rows are weighted and
+// summed in fp32 in slot order, so results do not depend on the order of pairs
+// within an expert.
+// Few pairs: no sorting, the products' workgroups find their pairs; a handful of
+// pairs: no fourth launch either, the down kernel adds up each token's experts.
 #include "sg_moe.h"
-#include "w4.h"
+#include "w4_rows.h"
 #include "w4_tile.h"
 
 namespace sg {
@@ -30,15 +33,14 @@ struct MoeArgs {
   // workspace
   int* off;       // [E + 1] first sorted pair of each expert
   int* list;      // [P] pairs sorted by expert
-  int* act;       // [E + 1] number of experts with pairs, then those
   int* tile;      // [2 * max_tiles + 1] number of tiles, then expert and first sorted pair of each
-  uint16_t* h;    // [P, F], in sorted order
+  uint16_t* h;    // [P, F], in sorted order; with few pairs by pair
   float* o;       // [P, D], by pair
 };
 
 // One workgroup counts, sums and places the pairs.
 __global__ void __launch_bounds__(1024) k_moe_plan(MoeArgs a) {
-  __shared__ int cnt[MOE_EMAX], off[MOE_EMAX], tiles[MOE_EMAX], act[MOE_EMAX];
+  __shared__ int cnt[MOE_EMAX], off[MOE_EMAX], tiles[MOE_EMAX];
   const int t = threadIdx.x;
   cnt[t] = 0;
   __syncthreads();
@@ -47,17 +49,15 @@ __global__ void __launch_bounds__(1024) k_moe_plan(MoeArgs a) {
     if (e >= 0 && e < a.E) atomicAdd(&cnt[e], 1);
   }
   __syncthreads();
-  const int c = t < a.E ? cnt[t] : 0, nt = (c + MOE_BM - 1) / MOE_BM, on = c > 0;
+  const int c = t < a.E ? cnt[t] : 0, nt = (c + MOE_BM - 1) / MOE_BM;
   off[t] = c;
   tiles[t] = nt;
-  act[t] = on;
   __syncthreads();
   for (int d = 1; d < 1024; d <<= 1) {
-    const int u = t >= d ? off[t - d] : 0, v = t >= d ? tiles[t - d] : 0, w = t >= d ? act[t - d] : 0;
+    const int u = t >= d ? off[t - d] : 0, v = t >= d ? tiles[t - d] : 0;
     __syncthreads();
     off[t] += u;
     tiles[t] += v;
-    act[t] += w;
     __syncthreads();
   }
   const int first = off[t] - c;
@@ -65,9 +65,7 @@ __global__ void __launch_bounds__(1024) k_moe_plan(MoeArgs a) {
   if (t == a.E - 1) {
     a.off[a.E] = off[t];
     a.tile[0] = tiles[t];
-    a.act[0] = act[t];
   }
-  if (on) a.act[act[t]] = t;
   for (int i = 0; i < nt; ++i) {
     a.tile[1 + 2 * (tiles[t] - nt + i)] = t;
     a.tile[2 + 2 * (tiles[t] - nt + i)] = first + i * MOE_BM;
@@ -83,116 +81,273 @@ __global__ void __launch_bounds__(1024) k_moe_plan(MoeArgs a) {
 #if SG_DEVICE_PASS
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
 
-// Adds 8 waves' partial tiles (each lane 4 floats) and gives the sum to the first wave.
-template <int TILES>
-__device__ __forceinline__ void join_waves(float (*red)[TILES][64][4], const v4f (&acc)[TILES], int wave, int l,
-                                           v4f (&sum)[TILES]) {
-#pragma unroll
-  for (int i = 0; i < TILES; ++i) *reinterpret_cast<v4f*>(&red[wave][i][l][0]) = acc[i];
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < TILES; ++i) {
-    v4f v = {0.f, 0.f, 0.f, 0.f};
-    if (wave == 0) {
-#pragma unroll
-      for (int w = 0; w < W4_WAVES; ++w) v += *reinterpret_cast<const v4f*>(&red[w][i][l][0]);
-    }
-    sum[i] = v;
+// This wave's LDS accesses before are done before those after.
+__device__ __forceinline__ void wave_order() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// The pairs of expert e, in order: their number; the first one; list (this
+// wave's LDS) holds those of rank m0 .. m0 + n - 1.
+__device__ __forceinline__ int find_pairs(const int32_t* ids, int P, int e, int m0, int n, int* list, int l,
+                                          int& first) {
+  int cnt = 0;
+  first = P;
+  for (int c = 0; c < P; c += 64) {
+    const bool hit = c + l < P && ids[c + l] == e;
+    const uint64_t m = __ballot(hit);
+    const int rank = cnt + __builtin_popcountll(m & ((1ull << l) - 1)) - m0;
+    if (hit && rank >= 0 && rank < n) list[rank] = c + l;
+    if (cnt == 0 && m) first = c + __builtin_ctzll(m);
+    cnt += __builtin_popcountll(m);
   }
-  __syncthreads();
+  wave_order();
+  return cnt;
 }
 
-// acc += the K block's product of one row block (chunk at 0 of rw) with 16 X rows.
-template <int GC>
-__device__ __forceinline__ void block_product(__amdgpu_buffer_rsrc_t rw, const v4i (&bx)[4], int kb, int l, v4f& acc) {
-  using P = W4<GC>;
-  const int g = l >> 4;
-  const v4i cw = w4_ld16(rw, (uint32_t)(16 * l), kb * P::CHUNK);
-  v4f sw[P::NG];
+// The expert of workgroup row y: with fewer pairs than experts the one of pair
+// y, otherwise expert y; -1 where the pair is empty.
+__device__ __forceinline__ int row_expert(const MoeArgs& a, int y) {
+  const int e = a.P <= a.E ? a.ids[y] : y;
+  return __builtin_amdgcn_readfirstlane(e >= 0 && e < a.E ? e : -1);
+}
+
+// Adds 8 waves' partial tile i (each lane 4 floats), for the lanes of one wave.
+template <int TILES>
+__device__ __forceinline__ v4f join_waves(const uint8_t* lds, int i, int l) {
+  const float(*const red)[TILES][64][4] = reinterpret_cast<const float(*)[TILES][64][4]>(lds);
+  v4f v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int u = 0; u < P::NG; ++u)
-    sw[u] = __builtin_bit_cast(v4f, w4_ld16(rw, (uint32_t)(W4_CODES + 64 * u + 16 * g), kb * P::CHUNK));
-#pragma unroll
-  for (int u = 0; u < P::NG; ++u) {
-    v4f p = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int q = u * P::QPG; q < (u + 1) * P::QPG; ++q) p = w4_mfma(w4_widen(cw[q]), bx[q], p);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = fmaf(p[e], sw[u][e], acc[e]);
-  }
+  for (int w = 0; w < W4_WAVES; ++w) v += *reinterpret_cast<const v4f*>(&red[w][i][l][0]);
+  return v;
+}
+template <int TILES>
+__device__ __forceinline__ void give_tile(uint8_t* lds, int wave, int i, int l, const v4f& v) {
+  float(*const red)[TILES][64][4] = reinterpret_cast<float(*)[TILES][64][4]>(lds);
+  *reinterpret_cast<v4f*>(&red[wave][i][l][0]) = v;
 }
 #endif  // SG_DEVICE_PASS
 
-// Few pairs per expert: a workgroup takes one block of 16 rows of one active
-// expert's gate and up weights; its waves split the K blocks.
-template <int GC>
+// Few pairs per expert: a workgroup takes one block of 16 rows of one expert's
+// gate and up weights, finds that expert's pairs by itself (no sorting launch
+// before it: 5 us) and takes 4 XI of them a pass; its waves split the K blocks.
+template <int GC, int XI>
 __global__ void __launch_bounds__(512) k_moe_gate_up_rows(MoeArgs a) {
 #if SG_DEVICE_PASS
-  using P = W4<GC>;
-  __shared__ __attribute__((aligned(16))) float red[W4_WAVES][2][64][4];
-  if ((int)blockIdx.y >= a.act[0]) return;
-  const int e = a.act[1 + blockIdx.y], first = a.off[e], last = a.off[e + 1];
+  using T = W4Rows<GC, 2, XI>;
+  static_assert(T::MT == 1, "one sub-tile");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int KB = (a.D + 127) >> 7;
-  const int64_t at = (int64_t)e * a.gu_bytes + (int64_t)blockIdx.x * KB * P::CHUNK;
-  const __amdgpu_buffer_rsrc_t rg = w4_rsrc(a.gate + at, (uint32_t)(KB * P::CHUNK));
-  const __amdgpu_buffer_rsrc_t ru = w4_rsrc(a.up + at, (uint32_t)(KB * P::CHUNK));
-  for (int m0 = first; m0 < last; m0 += 16) {
-    const bool row = m0 + lr < last;
-    const int64_t tok = row ? a.list[m0 + lr] / a.k : 0;
-    const __amdgpu_buffer_rsrc_t rx = w4_rsrc(a.x, (uint32_t)(((a.T - 1) * a.ldx + a.D) * 2));
-    v4f acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    for (int kb = wave; kb < KB; kb += W4_WAVES) {
-      v4i bx[4];
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6), P = (int)a.P;
+  const int e = row_expert(a, blockIdx.y);
+  if (e < 0) return;
+  uint8_t* const mine = lds + wave * T::WAVE_LDS;
+  int* const list = reinterpret_cast<int*>(mine);
+  typename T::Src s;
+  s.K = a.D;
+  s.KB = (a.D + 127) >> 7;
+  s.x = a.x;
+  s.x_bytes = (uint32_t)(((a.T - 1) * a.ldx + a.D) * 2);
+  const int64_t at = (int64_t)e * a.gu_bytes + (int64_t)blockIdx.x * s.KB * T::P::CHUNK;
+  s.w[0] = a.gate + at;
+  s.w[1] = a.up + at;
+  s.w_bytes[0] = s.w_bytes[1] = (uint32_t)(s.KB * T::P::CHUNK);
+  int first, cnt = 1;
+  for (int m0 = 0; m0 < cnt; m0 += 4 * XI) {
+    cnt = find_pairs(a.ids, P, e, m0, 4 * XI, list, l, first);
+    if (cnt == 0 || (a.P <= a.E && first != (int)blockIdx.y)) return;   // the same for every wave
+    const int n = min(4 * XI, cnt - m0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        bx[q] = w4_ld16(rx, row && kb * 128 + 32 * q + 8 * g < a.D ? (uint32_t)(tok * a.ldx * 2 + 64 * q + 16 * g) + kb * 256 : 0xffffffffu, 0);
-      block_product<GC>(rg, bx, kb, l, acc[0]);
-      block_product<GC>(ru, bx, kb, l, acc[1]);
+    for (int i = 0; i < XI; ++i) {
+      const int r = 4 * i + g;
+      s.xoff[i] = r < n ? (uint32_t)((int64_t)(list[r] / a.k) * a.ldx * 2) : W4_OUT;
     }
-    v4f s[2];
-    join_waves<2>(red, acc, wave, l, s);
+    const int pair = lr < n ? list[lr] : -1;
+    wave_order();
+    v4f acc[2][1] = {{{0.f, 0.f, 0.f, 0.f}}, {{0.f, 0.f, 0.f, 0.f}}};
+    T::multiply(mine, s, wave, W4_WAVES, l, acc);
+    __syncthreads();
+    give_tile<2>(lds, wave, 0, l, acc[0][0]);
+    give_tile<2>(lds, wave, 1, l, acc[1][0]);
+    __syncthreads();
     const int f = blockIdx.x * 16 + 4 * g;
-    if (wave == 0 && row && f < a.F) {   // F is a multiple of 32
+    if (wave == 0 && pair >= 0 && f < a.F) {   // F is a multiple of 32
+      const v4f gs = join_waves<2>(lds, 0, l) * W4_UNIT, us = join_waves<2>(lds, 1, l) * W4_UNIT;
       float h[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = silu(s[0][i] * W4_UNIT) * (s[1][i] * W4_UNIT);
-      *reinterpret_cast<uint2*>(a.h + (int64_t)(m0 + lr) * a.F + f) =
+      for (int i = 0; i < 4; ++i) h[i] = silu(gs[i]) * us[i];
+      *reinterpret_cast<uint2*>(a.h + (int64_t)pair * a.F + f) =
           make_uint2(f32x2_to_bf16x2(h[0], h[1]), f32x2_to_bf16x2(h[2], h[3]));
     }
+    __syncthreads();
   }
 #endif  // SG_DEVICE_PASS
 }
 
-template <int GC>
+template <int GC, int XI>
 __global__ void __launch_bounds__(512) k_moe_down_rows(MoeArgs a) {
 #if SG_DEVICE_PASS
-  using P = W4<GC>;
-  __shared__ __attribute__((aligned(16))) float red[W4_WAVES][1][64][4];
-  if ((int)blockIdx.y >= a.act[0]) return;
-  const int e = a.act[1 + blockIdx.y], first = a.off[e], last = a.off[e + 1];
+  using T = W4Rows<GC, 1, XI>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int KB = (a.F + 127) >> 7;
-  const __amdgpu_buffer_rsrc_t rw =
-      w4_rsrc(a.down + (int64_t)e * a.d_bytes + (int64_t)blockIdx.x * KB * P::CHUNK, (uint32_t)(KB * P::CHUNK));
-  for (int m0 = first; m0 < last; m0 += 16) {
-    const bool row = m0 + lr < last;
-    const __amdgpu_buffer_rsrc_t rx = w4_rsrc(a.h + (int64_t)m0 * a.F, (uint32_t)(min(16, last - m0) * a.F * 2));
-    v4f acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-    for (int kb = wave; kb < KB; kb += W4_WAVES) {
-      v4i bx[4];
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6), P = (int)a.P;
+  const int e = row_expert(a, blockIdx.y);
+  if (e < 0) return;
+  uint8_t* const mine = lds + wave * T::WAVE_LDS;
+  int* const list = reinterpret_cast<int*>(mine);
+  typename T::Src s;
+  s.K = a.F;
+  s.KB = (a.F + 127) >> 7;
+  s.x = a.h;
+  s.x_bytes = (uint32_t)(a.P * a.F * 2);
+  s.w[0] = a.down + (int64_t)e * a.d_bytes + (int64_t)blockIdx.x * s.KB * T::P::CHUNK;
+  s.w_bytes[0] = (uint32_t)(s.KB * T::P::CHUNK);
+  int first, cnt = 1;
+  for (int m0 = 0; m0 < cnt; m0 += 4 * XI) {
+    cnt = find_pairs(a.ids, P, e, m0, 4 * XI, list, l, first);
+    if (cnt == 0 || (a.P <= a.E && first != (int)blockIdx.y)) return;
+    const int n = min(4 * XI, cnt - m0);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        bx[q] = w4_ld16(rx, row && kb * 128 + 32 * q + 8 * g < a.F ? (uint32_t)(lr * a.F * 2 + 64 * q + 16 * g) : W4_OUT, kb * 256);
-      block_product<GC>(rw, bx, kb, l, acc[0]);
+    for (int i = 0; i < XI; ++i) s.xoff[i] = 4 * i + g < n ? (uint32_t)list[4 * i + g] * (a.F * 2) : W4_OUT;
+    const int pair = lr < n ? list[lr] : -1;
+    wave_order();
+    v4f acc[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
+    T::multiply(mine, s, wave, W4_WAVES, l, acc);
+    __syncthreads();
+    give_tile<1>(lds, wave, 0, l, acc[0][0]);
+    __syncthreads();
+    const int d = blockIdx.x * 16 + 4 * g;
+    if (wave == 0 && pair >= 0 && d < a.D)
+      *reinterpret_cast<v4f*>(a.o + (int64_t)pair * a.D + d) = join_waves<1>(lds, 0, l) * W4_UNIT;
+    __syncthreads();
+  }
+#endif  // SG_DEVICE_PASS
+}
+
+// A handful of pairs (P <= 16): a workgroup takes 16 rows of every active
+// expert's down weight and adds up their weighted products itself.  X row t is
+// token t's; waves take whole experts, or parts of one's K blocks where there
+// are fewer than 8.  Duplicates of an expert in a token share a row: their
+// weights are added.
+template <int GC, int XI>
+__global__ void __launch_bounds__(512) k_moe_down_join(MoeArgs a, int out_bf16) {
+#if SG_DEVICE_PASS
+  using T = W4Rows<GC, 1, XI>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+  const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6), P = (int)a.P;
+  const int v = l < P ? a.ids[l] : -1;
+  const float wl = l < P ? a.weights[l] : 0.f;
+  const bool live = v >= 0 && v < a.E;
+  bool again = false;   // an earlier pair has this expert
+  for (int p = 0; p < P; ++p) again = again || (p < l && __builtin_amdgcn_readlane(v, p) == v);
+  uint64_t lead = __ballot(live && !again);
+  const int na = __builtin_popcountll(lead), parts = na >= W4_WAVES ? 1 : na > 0 ? W4_WAVES / na : 1;
+  typename T::Src s;
+  s.K = a.F;
+  s.KB = (a.F + 127) >> 7;
+  s.x = a.h;
+  s.x_bytes = (uint32_t)(a.P * a.F * 2);
+  s.w_bytes[0] = (uint32_t)(s.KB * T::P::CHUNK);
+  v4f sum = {0.f, 0.f, 0.f, 0.f};
+  int at = 0;   // rank of the expert in hand
+  for (; lead; lead &= lead - 1, ++at) {
+    const int turn = at % W4_WAVES;   // wave of its first part; at < na <= 16
+    if (parts == 1 ? turn != wave : wave % na != at || wave / na >= parts) continue;
+    const int e = __builtin_amdgcn_readlane(v, __builtin_ctzll(lead));
+    const uint64_t m = __ballot(v == e);
+    const auto row_pair = [&](int r) {   // token r's first pair with e
+      const uint64_t b = r < (int)a.T ? (m >> (r * a.k)) & ((1ull << a.k) - 1) : 0;
+      return b ? r * a.k + (int)__builtin_ctzll(b) : -1;
+    };
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+      const int p = row_pair(4 * i + g);
+      s.xoff[i] = p >= 0 ? (uint32_t)p * (a.F * 2) : W4_OUT;
     }
-    v4f s[1];
-    join_waves<1>(red, acc, wave, l, s);
-    const int n = blockIdx.x * 16 + 4 * g;
-    if (wave == 0 && row && n < a.D)
-      *reinterpret_cast<v4f*>(a.o + (int64_t)a.list[m0 + lr] * a.D + n) = s[0] * W4_UNIT;
+    float w = 0.f;
+    bool mine = false;   // token lr has this expert: another's infinities stay out of its sum
+    for (int j = 0; j < a.k; ++j) {
+      const int p = min(lr * a.k + j, 63);
+      const float u = __shfl(wl, p, 64);
+      const bool in = lr < (int)a.T && ((m >> p) & 1);
+      w += in ? u : 0.f;
+      mine = mine || in;
+    }
+    s.w[0] = a.down + (int64_t)e * a.d_bytes + (int64_t)blockIdx.x * s.KB * T::P::CHUNK;
+    v4f acc[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
+    T::multiply(lds + wave * T::WAVE_LDS, s, parts == 1 ? 0 : wave / na, parts, l, acc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] = mine ? fmaf(w, acc[0][0][i], sum[i]) : sum[i];
+  }
+  __syncthreads();
+  give_tile<1>(lds, wave, 0, l, sum);
+  __syncthreads();
+  const int d = blockIdx.x * 16 + 4 * g;
+  if (wave == 0 && lr < (int)a.T && d < a.D) {
+    const v4f r = join_waves<1>(lds, 0, l) * W4_UNIT;
+    if (out_bf16)
+      *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.y) + lr * a.ldy + d) =
+          make_uint2(f32x2_to_bf16x2(r[0], r[1]), f32x2_to_bf16x2(r[2], r[3]));
+    else
+      *reinterpret_cast<v4f*>(reinterpret_cast<float*>(a.y) + lr * a.ldy + d) = r;
+  }
+#endif  // SG_DEVICE_PASS
+}
+
+// Few pairs, many row blocks: a workgroup keeps R pairs' rows of one expert in LDS
+// and its waves stream row blocks of that expert's weights past them (W4Stream).
+// Dynamic LDS: 8 lists of 16 pairs, then the rows.
+template <int GC, bool DOWN>
+__global__ void __launch_bounds__(512) k_moe_stream(MoeArgs a, int R) {
+#if SG_DEVICE_PASS
+  using S = W4Stream<GC>;
+  extern __shared__ __attribute__((aligned(1024))) uint8_t moe_lds[];
+  const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6), P = (int)a.P;
+  const int e = row_expert(a, blockIdx.y);
+  if (e < 0) return;
+  int* const list = reinterpret_cast<int*>(moe_lds) + 16 * wave;
+  uint8_t* const xs = moe_lds + 512;
+  const int K = DOWN ? a.F : a.D, N = DOWN ? a.D : a.F, KB = (K + 127) >> 7, blocks = N / 16;
+  const int rb0 = blockIdx.x * W4_WAVES + wave, step = gridDim.x * W4_WAVES;
+  const int mine = rb0 < blocks ? (blocks - rb0 + step - 1) / step : 0;
+  const int64_t bytes = (int64_t)KB * S::P::CHUNK;
+  const uint8_t* const w0 = (DOWN ? a.down + e * a.d_bytes : a.gate + e * a.gu_bytes) + rb0 * bytes;
+  const uint8_t* const w1 = DOWN ? w0 : a.up + e * a.gu_bytes + rb0 * bytes;
+  int first, cnt = 1;
+  for (int m0 = 0; m0 < cnt; m0 += R) {
+    cnt = find_pairs(a.ids, P, e, m0, R, list, l, first);
+    if (cnt == 0 || (a.P <= a.E && first != (int)blockIdx.y)) return;   // the same for every wave
+    const int n = min(R, cnt - m0);
+    const int pair = lr < n ? list[lr] : -1;
+    if (DOWN)
+      S::load_x(xs, a.h, (uint32_t)(a.P * a.F * 2), K, R, n, wave, l,
+                [&](int r) { return (uint32_t)list[r] * (a.F * 2); });
+    else
+      S::load_x(xs, a.x, (uint32_t)(((a.T - 1) * a.ldx + a.D) * 2), K, R, n, wave, l,
+                [&](int r) { return (uint32_t)((int64_t)(list[r] / a.k) * a.ldx * 2); });
+    w4_wait<0>();
+    __syncthreads();
+    if (DOWN) {
+      S::run(xs, KB, R, mine, l, [&](int u) { return w0 + (int64_t)u * step * bytes; },
+             [&](int u, const v4f& acc) {
+               if (pair >= 0)
+                 *reinterpret_cast<v4f*>(a.o + (int64_t)pair * a.D + (rb0 + u * step) * 16 + 4 * g) = acc * W4_UNIT;
+             });
+    } else {
+      v4f gate;
+      S::run(xs, KB, R, 2 * mine, l, [&](int u) { return ((u & 1) ? w1 : w0) + (int64_t)(u >> 1) * step * bytes; },
+             [&](int u, const v4f& acc) {
+               if ((u & 1) == 0) {
+                 gate = acc;
+               } else if (pair >= 0) {
+                 float h[4];
+#pragma unroll
+                 for (int i = 0; i < 4; ++i) h[i] = silu(gate[i] * W4_UNIT) * (acc[i] * W4_UNIT);
+                 *reinterpret_cast<uint2*>(a.h + (int64_t)pair * a.F + (rb0 + (u >> 1) * step) * 16 + 4 * g) =
+                     make_uint2(f32x2_to_bf16x2(h[0], h[1]), f32x2_to_bf16x2(h[2], h[3]));
+               }
+             });
+    }
+    __syncthreads();
   }
 #endif  // SG_DEVICE_PASS
 }
@@ -319,13 +474,12 @@ static int64_t moe_tiles(int64_t P, int64_t E) { return cdiv(P, MOE_BM) + (P < E
 
 // Offsets of the workspace's parts; `bytes` its size.
 struct MoeSpace {
-  int64_t off, list, act, tile, h, o, bytes;
+  int64_t off, list, tile, h, o, bytes;
   MoeSpace(int64_t P, int64_t E, int64_t D, int64_t F) {
     int64_t at = 0;
     const auto part = [&](int64_t n) { const int64_t was = at; at += cdiv(n, 256) * 256; return was; };
     off = part(4 * (E + 1));
     list = part(4 * P);
-    act = part(4 * (E + 1));
     tile = part(4 * (2 * moe_tiles(P, E) + 1));
     h = part(2 * P * F);
     o = part(4 * P * D);
@@ -333,14 +487,45 @@ struct MoeSpace {
   }
 };
 
+template <int GC, int XI>
+static void launch_moe_rows(const MoeArgs& a, bool bf16, hipStream_t st) {
+  const unsigned gy = (unsigned)(a.P < a.E ? a.P : a.E);
+  k_moe_gate_up_rows<GC, XI><<<dim3((unsigned)cdiv(a.F, 16), gy), 512, 0, st>>>(a);
+  if (a.P <= 16) k_moe_down_join<GC, XI><<<(unsigned)cdiv(a.D, 16), 512, 0, st>>>(a, bf16);
+  else k_moe_down_rows<GC, XI><<<dim3((unsigned)cdiv(a.D, 16), gy), 512, 0, st>>>(a);
+}
+
+// One product by streaming: the most X rows of 16, 8, 4 that leave LDS to two
+// workgroups of a compute unit; workgroups as many as stay busy.
+static int moe_stream_rows(int64_t K) {
+  const int64_t row = cdiv(K, 128) * 256;
+  return 16 * row <= 79 * 1024 ? 16 : 8 * row <= 79 * 1024 ? 8 : 4 * row <= 79 * 1024 ? 4 : 0;
+}
+template <int GC, bool DOWN>
+static void launch_moe_stream(const MoeArgs& a, hipStream_t st) {
+  const int64_t K = DOWN ? a.F : a.D, blocks = (DOWN ? a.D : a.F) / 16, gy = a.P < a.E ? a.P : a.E;
+  const int R = moe_stream_rows(K);
+  int64_t gx = cdiv(blocks, W4_WAVES);
+  if (gx * gy > 1024) gx = cdiv(1024, gy) < gx ? cdiv(1024, gy) : gx;
+  k_moe_stream<GC, DOWN><<<dim3((unsigned)gx, (unsigned)gy), 512, 512 + R * cdiv(K, 128) * 256, st>>>(a, R);
+}
+
 template <int GC>
 static void launch_moe(const MoeArgs& a, bool bf16, hipStream_t st) {
-  k_moe_plan<<<1, 1024, 0, st>>>(a);
-  if (a.P <= 16LL * a.E) {
-    const unsigned gy = (unsigned)(a.P < a.E ? a.P : a.E);
-    k_moe_gate_up_rows<GC><<<dim3((unsigned)cdiv(a.F, 16), gy), 512, 0, st>>>(a);
-    k_moe_down_rows<GC><<<dim3((unsigned)cdiv(a.D, 16), gy), 512, 0, st>>>(a);
+  // few-rows kernels: every workgroup reads all ids, 32-bit offsets into h
+  if (a.P <= 16LL * a.E && a.P <= 2048 && a.P <= (1LL << 30) / a.F) {
+    const int64_t gy = a.P < a.E ? a.P : a.E;
+    if (gy * (a.F / 16) >= 2048 && gy * (a.D / 16) >= 2048 && moe_stream_rows(a.D) && moe_stream_rows(a.F)) {
+      launch_moe_stream<GC, false>(a, st);
+      launch_moe_stream<GC, true>(a, st);
+    } else {
+      if (a.T <= 4) launch_moe_rows<GC, 1>(a, bf16, st);
+      else if (a.T <= 8) launch_moe_rows<GC, 2>(a, bf16, st);
+      else launch_moe_rows<GC, 4>(a, bf16, st);
+      if (a.P <= 16) return;
+    }
   } else {
+    k_moe_plan<<<1, 1024, 0, st>>>(a);
     const int tm = (int)moe_tiles(a.P, a.E), ng = (int)cdiv(a.F, 128), nd = (int)cdiv(a.D, 256);
     k_moe_gate_up<GC><<<(unsigned)(tm * ng), 512, 0, st>>>(a, ng);
     k_moe_down<GC><<<(unsigned)(tm * nd), 512, 0, st>>>(a, nd);
@@ -387,7 +572,7 @@ extern "C" sg_status sg_w4a16_moe_mlp(int64_t T, int k, int64_t E, int64_t D, in
   a.gu_bytes = sg_w4_packed_bytes(F, D, gc); a.d_bytes = sg_w4_packed_bytes(D, F, gc);
   a.y = y; a.ldy = ldy;
   a.off = reinterpret_cast<int*>(w + ws.off); a.list = reinterpret_cast<int*>(w + ws.list);
-  a.act = reinterpret_cast<int*>(w + ws.act); a.tile = reinterpret_cast<int*>(w + ws.tile);
+  a.tile = reinterpret_cast<int*>(w + ws.tile);
   a.h = reinterpret_cast<uint16_t*>(w + ws.h); a.o = reinterpret_cast<float*>(w + ws.o);
   clear_hip_error();
   const bool b16 = y_dt == SG_BF16;

@@ -72,6 +72,16 @@ __device__ __forceinline__ v4f w4_mfma(const v4i& a, const v4i& b, const v4f& c)
                                                  0, 0);
 }
 
+// Waits until at most N of this wave's loads are in flight.  Nothing that touches
+// memory moves across it, nor across w4_pin: waits that count loads need them in
+// the order they are written in.
+template <int N>
+__device__ __forceinline__ void w4_wait() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void w4_pin() { asm volatile("" ::: "memory"); }
+
 // Past every descriptor's records (all hold under 2^31 bytes): such a lane reads zero.
 constexpr uint32_t W4_OUT = 0x80000000u;
 #endif  // SG_DEVICE_PASS

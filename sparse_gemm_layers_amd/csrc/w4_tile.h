@@ -120,7 +120,7 @@ struct W4Tile {
         sw[t][i] = (v4f){0.f, 0.f, 0.f, 0.f};
         p[t][i][0] = p[t][i][1] = sw[t][i];
       }
-    wait_vmcnt<2 * LOADS>();
+    w4_wait<2 * LOADS>();
 #pragma unroll
     for (int i = 0; i < 2; ++i) cw[i] = *reinterpret_cast<const v4i*>(lds + cur + wo + i * W4_CODES);
     lds_barrier();           // block 0's codes are in registers: block 3's may take their place
@@ -129,7 +129,7 @@ struct W4Tile {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int q = 0; q < 4; ++q) aw[0][i][q] = w4_widen(cw[i][q]);
-    wait_vmcnt<2 * LOADS>();
+    w4_wait<2 * LOADS>();
     lds_barrier();
 #pragma unroll
     for (int q = 0; q < 4; ++q) read_x(bx, cur, 0, q);
@@ -181,7 +181,7 @@ struct W4Tile {
           if (jj == JP - 1) {
             if (t == 2) {
               // own loads of kb + 1 have landed (kb + 2's may fly); every wave holds its last operands of kb
-              wait_vmcnt<LOADS>();
+              w4_wait<LOADS>();
               lds_barrier();
             }
             if (t == 11) {
@@ -223,7 +223,7 @@ struct W4Tile {
         for (int e = 0; e < 4; ++e)
           acc[i][2 * JP - 2 + c][e] = fmaf(odd ? p[0][i][c][e] : p[1][i][c][e], odd ? sw[0][i][e] : sw[1][i][e],
                                            acc[i][2 * JP - 2 + c][e]);
-    wait_vmcnt<0>();   // loads past the end write their zeros before LDS is given up
+    w4_wait<0>();   // loads past the end write their zeros before LDS is given up
   }
 #endif  // SG_DEVICE_PASS
 };

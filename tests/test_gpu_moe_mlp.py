@@ -182,3 +182,33 @@ def test_refusals():
                 dict(x=x.cpu())):
         with pytest.raises(sg.SgError):
             call(**bad)
+
+
+@pytest.mark.parametrize("T,k", [(1, 8), (3, 4), (4, 4), (7, 2), (16, 1), (12, 5), (100, 6)])
+def test_an_expert_twice_in_a_token(T, k):
+    """Slots of one token may name the same expert: each contributes."""
+    E, D, F, gc = 6, 128, 96, 32
+    g = np.random.default_rng(T)
+    ids = g.integers(-1, 3, (T, k)).astype(np.int32)
+    w = g.uniform(0.05, 1.0, (T, k)).astype(np.float32)
+    say(f"duplicates T{T} k{k}")
+    run_and_check(T, E, k, D, F, gc, F32, ids, w)
+
+
+@pytest.mark.parametrize("T", [2, 9, 60])
+def test_an_expert_of_infinities_stays_with_its_tokens(T):
+    """Scales of one expert's weights that are inf or NaN: tokens of others keep their bits."""
+    E, D, F, gc, k = 8, 128, 64, 64, 2
+    host, dev = layer(7, E, D, F, gc)
+    ids = np.stack([np.array([t % 4, 4 + t % 3]) for t in range(T)]).astype(np.int32)     # expert 7 unused
+    ids[0] = (7, 1)
+    w = np.full((T, k), 0.5, np.float32)
+    x = torch.randn((T, D), generator=torch.Generator().manual_seed(T)).to(BF16).to(DEV)
+    want = sg.w4a16_moe_mlp(x, up(ids), up(w), *dev, F, gc, out_dtype=F32)
+    for c, s in host:
+        s[7] = np.inf
+    host[2][1][7] = np.nan
+    bad = [sg.w4_pack(up(c), up(s), gc) for c, s in host]
+    got = sg.w4a16_moe_mlp(x, up(ids), up(w), *bad, F, gc, out_dtype=F32)
+    assert torch.isnan(got[0]).all()
+    assert torch.equal(got[1:], want[1:])
