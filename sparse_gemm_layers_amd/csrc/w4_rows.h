@@ -120,6 +120,11 @@ struct W4Rows {
       if (kb + (DW - 1) * step < s.KB) w4_wait<FLY>();
       else w4_wait<0>();
       compute(n % DW);
+      // finished here: the compiler would carry unscaled sums into the branches that follow, and spill them
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) asm volatile("" : "+v"(acc[rb][j]));
       if (kb + DX * step < s.KB) load_x(n % DX, kb + DX * step);
       if (n < DW - 1 && kb + DW * step < s.KB) load_w(n, kb + DW * step);
     }
