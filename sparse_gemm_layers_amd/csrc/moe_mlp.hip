@@ -8,8 +8,9 @@
 // products, one fp32 row per pair.  (4) Each token's k rows are weighted and
 // summed in fp32 in slot order, so results do not depend on the order of pairs
 // within an expert.
-// Few pairs: no sorting, the products' workgroups find their pairs; a handful of
-// pairs: no fourth launch either, the down kernel adds up each token's experts.
+// Few pairs per expert: no sorting, the products' workgroups find their pairs; a
+// handful of pairs: no fourth launch either, the down kernel adds up each token's
+// experts.
 #include "sg_moe.h"
 #include "w4_rows.h"
 #include "w4_tile.h"
@@ -18,6 +19,7 @@ namespace sg {
 
 constexpr int MOE_EMAX = 1024;
 constexpr int MOE_BM = 128;   // pairs per tile
+constexpr int MOE_FEW = 16;   // pairs of the shortest calls: a wave holds them all
 
 struct MoeArgs {
   int64_t T, P;           // tokens, pairs
@@ -108,13 +110,13 @@ __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g));
 __device__ __forceinline__ void wave_order() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // The pairs of expert e, in order: their number; the first one; list (this
-// wave's LDS) holds those of rank m0 .. m0 + n - 1.
-__device__ __forceinline__ int find_pairs(const int32_t* ids, int P, int e, int m0, int n, int* list, int l,
+// wave's LDS) holds those of rank m0 .. m0 + n - 1.  v: ids[l], -1 past the end.
+__device__ __forceinline__ int find_pairs(const int32_t* ids, int P, int v, int e, int m0, int n, int* list, int l,
                                           int& first) {
   int cnt = 0;
   first = P;
   for (int c = 0; c < P; c += 64) {
-    const bool hit = c + l < P && ids[c + l] == e;
+    const bool hit = c == 0 ? v == e : c + l < P && ids[c + l] == e;
     const uint64_t m = __ballot(hit);
     const int rank = cnt + __builtin_popcountll(m & ((1ull << l) - 1)) - m0;
     if (hit && rank >= 0 && rank < n) list[rank] = c + l;
@@ -127,8 +129,8 @@ __device__ __forceinline__ int find_pairs(const int32_t* ids, int P, int e, int 
 
 // The expert of workgroup row y: with fewer pairs than experts the one of pair
 // y, otherwise expert y; -1 where the pair is empty.
-__device__ __forceinline__ int row_expert(const MoeArgs& a, int y) {
-  const int e = a.P <= a.E ? a.ids[y] : y;
+__device__ __forceinline__ int row_expert(const MoeArgs& a, int v, int y) {
+  const int e = a.P > a.E ? y : y < 64 ? __builtin_amdgcn_readlane(v, y) : a.ids[y];
   return __builtin_amdgcn_readfirstlane(e >= 0 && e < a.E ? e : -1);
 }
 
@@ -148,9 +150,11 @@ __device__ __forceinline__ void give_tile(uint8_t* lds, int wave, int i, int l, 
 }
 #endif  // SG_DEVICE_PASS
 
-// Few pairs per expert: a workgroup takes one block of 16 rows of one expert's
-// gate and up weights, finds that expert's pairs by itself (no sorting launch
-// before it: 5 us) and takes 4 XI of them a pass; its waves split the K blocks.
+// A handful of pairs (P <= MOE_FEW): a workgroup takes one block of 16 rows of one
+// expert's gate and up weights, finds that expert's pairs by itself (no sorting
+// launch before it: 5 us) and takes 4 XI of them a pass; its waves split the K
+// blocks.  One token of 64 experts (4096, 1024, k 8): 12 us for 36 MB, of which
+// 2.5 are the launch and 1.5 the ids' way from memory; the down product 8.
 template <int GC, int XI>
 __global__ void __launch_bounds__(512) k_moe_gate_up_rows(MoeArgs a) {
 #if SG_DEVICE_PASS
@@ -159,7 +163,8 @@ __global__ void __launch_bounds__(512) k_moe_gate_up_rows(MoeArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6), P = (int)a.P;
-  const int e = row_expert(a, blockIdx.y);
+  const int v = l < P ? a.ids[l] : -1;
+  const int e = row_expert(a, v, blockIdx.y);
   if (e < 0) return;
   uint8_t* const mine = lds + wave * T::WAVE_LDS;
   int* const list = reinterpret_cast<int*>(mine);
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(512) k_moe_gate_up_rows(MoeArgs a) {
   s.w_bytes[0] = s.w_bytes[1] = (uint32_t)(s.KB * T::P::CHUNK);
   int first, cnt = 1;
   for (int m0 = 0; m0 < cnt; m0 += 4 * XI) {
-    cnt = find_pairs(a.ids, P, e, m0, 4 * XI, list, l, first);
+    cnt = find_pairs(a.ids, P, v, e, m0, 4 * XI, list, l, first);
     if (cnt == 0 || (a.P <= a.E && first != (int)blockIdx.y)) return;   // the same for every wave
     const int n = min(4 * XI, cnt - m0);
 #pragma unroll
@@ -204,48 +209,7 @@ __global__ void __launch_bounds__(512) k_moe_gate_up_rows(MoeArgs a) {
 #endif  // SG_DEVICE_PASS
 }
 
-template <int GC, int XI>
-__global__ void __launch_bounds__(512) k_moe_down_rows(MoeArgs a) {
-#if SG_DEVICE_PASS
-  using T = W4Rows<GC, 1, XI>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
-  const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6), P = (int)a.P;
-  const int e = row_expert(a, blockIdx.y);
-  if (e < 0) return;
-  uint8_t* const mine = lds + wave * T::WAVE_LDS;
-  int* const list = reinterpret_cast<int*>(mine);
-  typename T::Src s;
-  s.K = a.F;
-  s.KB = (a.F + 127) >> 7;
-  s.x = a.h;
-  s.x_bytes = (uint32_t)(a.P * a.F * 2);
-  s.w[0] = a.down + (int64_t)e * a.d_bytes + (int64_t)blockIdx.x * s.KB * T::P::CHUNK;
-  s.w_bytes[0] = (uint32_t)(s.KB * T::P::CHUNK);
-  int first, cnt = 1;
-  for (int m0 = 0; m0 < cnt; m0 += 4 * XI) {
-    cnt = find_pairs(a.ids, P, e, m0, 4 * XI, list, l, first);
-    if (cnt == 0 || (a.P <= a.E && first != (int)blockIdx.y)) return;
-    const int n = min(4 * XI, cnt - m0);
-#pragma unroll
-    for (int i = 0; i < XI; ++i) s.xoff[i] = 4 * i + g < n ? (uint32_t)list[4 * i + g] * (a.F * 2) : W4_OUT;
-    const int pair = lr < n ? list[lr] : -1;
-    wave_order();
-    v4f acc[1][1] = {{{0.f, 0.f, 0.f, 0.f}}};
-    T::multiply(mine, s, wave, W4_WAVES, l, acc);
-    __syncthreads();
-    give_tile<1>(lds, wave, 0, l, acc[0][0]);
-    __syncthreads();
-    const int d = blockIdx.x * 16 + 4 * g;
-    if (wave == 0 && pair >= 0 && d < a.D)
-      *reinterpret_cast<v4f*>(a.o + (int64_t)pair * a.D + d) = join_waves<1>(lds, 0, l) * W4_UNIT;
-    __syncthreads();
-  }
-#endif  // SG_DEVICE_PASS
-}
-
-// A handful of pairs (P <= 16): a workgroup takes 16 rows of every active
-// expert's down weight and adds up their weighted products itself.  X row t is
+// Its down product: a workgroup takes 16 rows of every active expert's down weight and adds up their weighted products itself.  X row t is
 // token t's; waves take whole experts, or parts of one's K blocks where there
 // are fewer than 8.  Duplicates of an expert in a token share a row: their
 // weights are added.
@@ -325,7 +289,8 @@ __global__ void __launch_bounds__(512) k_moe_stream(MoeArgs a, int R) {
   extern __shared__ __attribute__((aligned(1024))) uint8_t moe_lds[];
   const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6), P = (int)a.P;
-  const int e = row_expert(a, blockIdx.y);
+  const int v = l < P ? a.ids[l] : -1;
+  const int e = row_expert(a, v, blockIdx.y);
   if (e < 0) return;
   int* const list = reinterpret_cast<int*>(moe_lds) + 16 * wave;
   uint8_t* const xs = moe_lds + 512;
@@ -337,7 +302,7 @@ __global__ void __launch_bounds__(512) k_moe_stream(MoeArgs a, int R) {
   const uint8_t* const w1 = DOWN ? w0 : a.up + e * a.gu_bytes + rb0 * bytes;
   int first, cnt = 1;
   for (int m0 = 0; m0 < cnt; m0 += R) {
-    cnt = find_pairs(a.ids, P, e, m0, R, list, l, first);
+    cnt = find_pairs(a.ids, P, v, e, m0, R, list, l, first);
     if (cnt == 0 || (a.P <= a.E && first != (int)blockIdx.y)) return;   // the same for every wave
     const int n = min(R, cnt - m0);
     const int pair = lr < n ? list[lr] : -1;
@@ -511,11 +476,10 @@ struct MoeSpace {
 };
 
 template <int GC, int XI>
-static void launch_moe_rows(const MoeArgs& a, bool bf16, hipStream_t st) {
+static void launch_moe_few(const MoeArgs& a, bool bf16, hipStream_t st) {
   const unsigned gy = (unsigned)(a.P < a.E ? a.P : a.E);
   k_moe_gate_up_rows<GC, XI><<<dim3((unsigned)cdiv(a.F, 16), gy), 512, 0, st>>>(a);
-  if (a.P <= 16) k_moe_down_join<GC, XI><<<(unsigned)cdiv(a.D, 16), 512, 0, st>>>(a, bf16);
-  else k_moe_down_rows<GC, XI><<<dim3((unsigned)cdiv(a.D, 16), gy), 512, 0, st>>>(a);
+  k_moe_down_join<GC, XI><<<(unsigned)cdiv(a.D, 16), 512, 0, st>>>(a, bf16);
 }
 
 // One product by streaming: the most X rows of 16, 8, 4 that leave LDS to two
@@ -533,20 +497,25 @@ static void launch_moe_stream(const MoeArgs& a, hipStream_t st) {
   k_moe_stream<GC, DOWN><<<dim3((unsigned)gx, (unsigned)gy), 512, 512 + R * cdiv(K, 128) * 256, st>>>(a, R);
 }
 
+// Which way: us of 64 experts (4096, 1024), k 8 / 60 experts (2048, 1408), k 4.
+//   pairs      16         32          128          256        512
+//   few      27 / 28    68 / 51    163 / 114    205 / 155  301 / 218
+//   stream   43 / 29    54 / 43     83 /  76    155 /  84  212 / 154
+//   tiles    53 / 40    65 / 42    104 /  76    119 /  79  120 / 103
+// Streaming passes over an expert's weights once for every R of its pairs, so it
+// is taken while an expert has R / 4 on average (some have several times that).
 template <int GC>
 static void launch_moe(const MoeArgs& a, bool bf16, hipStream_t st) {
-  // few-rows kernels: every workgroup reads all ids, 32-bit offsets into h
-  if (a.P <= 16LL * a.E && a.P <= 2048 && a.P <= (1LL << 30) / a.F) {
-    const int64_t gy = a.P < a.E ? a.P : a.E;
-    if (gy * (a.F / 16) >= 2048 && gy * (a.D / 16) >= 2048 && moe_stream_rows(a.D) && moe_stream_rows(a.F)) {
-      launch_moe_stream<GC, false>(a, st);
-      launch_moe_stream<GC, true>(a, st);
-    } else {
-      if (a.T <= 4) launch_moe_rows<GC, 1>(a, bf16, st);
-      else if (a.T <= 8) launch_moe_rows<GC, 2>(a, bf16, st);
-      else launch_moe_rows<GC, 4>(a, bf16, st);
-      if (a.P <= 16) return;
-    }
+  if (a.P <= MOE_FEW) {
+    if (a.T <= 4) launch_moe_few<GC, 1>(a, bf16, st);
+    else if (a.T <= 8) launch_moe_few<GC, 2>(a, bf16, st);
+    else launch_moe_few<GC, 4>(a, bf16, st);
+    return;
+  }
+  const int rd = moe_stream_rows(a.D), rf = moe_stream_rows(a.F), R = rd < rf ? rd : rf;
+  if (4 * a.P <= (int64_t)R * a.E && a.P <= 2048) {   // every workgroup reads all ids
+    launch_moe_stream<GC, false>(a, st);
+    launch_moe_stream<GC, true>(a, st);
   } else {
     k_moe_plan<<<1, 1024, 0, st>>>(a);
     const int tm = (int)moe_tiles(a.P, a.E), ng = (int)cdiv(a.F, 128), nd = (int)cdiv(a.D, 256);
