@@ -184,7 +184,7 @@ static void launch_w4(const W4Args& a, bool b16, hipStream_t st) {
   int rb = 1, xi = a.M <= 4 ? 1 : a.M <= 8 ? 2 : 4;
   if (a.M > 8)
     for (int x = 4; x <= 16 && 4 * x < a.M + 16; x += 4)
-      for (int r = 1; r <= (x == 4 ? 2 : 4); r *= 2)
+      for (int r = x == 16 ? 2 : 1; r <= (x == 4 ? 2 : 4); r *= 2)   // 16, 1 costs more than 8, 2 everywhere
         if (w4_rows_cost(a.M, a.N, r, x) < w4_rows_cost(a.M, a.N, rb, xi)) rb = r, xi = x;
   if (cdiv(a.M, 4 * xi) > 65535 || w4_tile_cost(a.M, a.N) < w4_rows_cost(a.M, a.N, rb, xi)) {
     using T = W4Tile<GC>;
@@ -204,7 +204,6 @@ static void launch_w4(const W4Args& a, bool b16, hipStream_t st) {
     case 121: launch_w4_rows<GC, 1, 12>(a, b16, st); break;
     case 122: launch_w4_rows<GC, 2, 12>(a, b16, st); break;
     case 124: launch_w4_rows<GC, 4, 12>(a, b16, st); break;
-    case 161: launch_w4_rows<GC, 1, 16>(a, b16, st); break;
     case 162: launch_w4_rows<GC, 2, 16>(a, b16, st); break;
     default: launch_w4_rows<GC, 4, 16>(a, b16, st); break;
   }

@@ -106,7 +106,8 @@ sg_status sg_w4a16_gemm_groupwise_packed(int64_t M, int64_t N, int64_t K, const 
  *   y[t] = sum_j weights[t, j] * Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),  e = ids[t, j]
  * with silu(g) = g / (1 + exp(-g)).  Products and sums are fp32; the inner
  * activations are rounded to bf16 once, as the down product's operand.  The k
- * contributions are added in slot order: the same call gives the same bits.
+ * contributions are added in an order that the sizes and ids fix: the same call
+ * gives the same bits.  A token may name an expert more than once.
  * Slots whose id is outside [0, E) contribute nothing and their weight is not
  * read into the sum; a token without any gets zeros.
  *   x : bf16 [T, D], ld ldx;  ids: int32 [T, k], weights: fp32 [T, k], contiguous
