@@ -69,29 +69,33 @@ struct W4Rows {
       }
       w4_pin();
     };
+    // X operands are read once, a row block's codes widened and its scales read once.
     const auto compute = [&](int n) {
-      v4i aw[RB][4];
+      v4i bx[MT][4];
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) aw[rb][q] = w4_widen(cw[n][rb][q]);
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        v4i bx[4];
+      for (int j = 0; j < MT; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          bx[q] = *reinterpret_cast<const v4i*>(lds + (n % DX) * XI * 1024 + (16 * j + r0) * 256 +
-                                                (((4 * q + g) ^ r0) << 4));
+          bx[j][q] = *reinterpret_cast<const v4i*>(lds + (n % DX) * XI * 1024 + (16 * j + r0) * 256 +
+                                                   (((4 * q + g) ^ r0) << 4));
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
+      for (int rb = 0; rb < RB; ++rb) {
+        v4i aw[4];
+        v4f sw[P::NG];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) aw[q] = w4_widen(cw[n][rb][q]);
+#pragma unroll
+        for (int t = 0; t < P::NG; ++t)
+          sw[t] = *reinterpret_cast<const v4f*>(lds + S_OFF + (n * RB + rb) * 256 + t * 64 + 16 * g);
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
 #pragma unroll
           for (int t = 0; t < P::NG; ++t) {
-            const v4f sw = *reinterpret_cast<const v4f*>(lds + S_OFF + (n * RB + rb) * 256 + t * 64 + 16 * g);
             v4f p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int q = t * P::QPG; q < (t + 1) * P::QPG; ++q) p = w4_mfma(aw[rb][q], bx[q], p);
+            for (int q = t * P::QPG; q < (t + 1) * P::QPG; ++q) p = w4_mfma(aw[q], bx[j][q], p);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[rb][j][e] = fmaf(p[e], sw[e], acc[rb][j][e]);
+            for (int e = 0; e < 4; ++e) acc[rb][j][e] = fmaf(p[e], sw[t][e], acc[rb][j][e]);
           }
       }
     };
