@@ -124,12 +124,12 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, n_group: int = 
         raise SgError(f"group_score must be 'max' or 'top2', got {group_score!r}")
     pb = None if bias is None else _rows(bias, "bias", torch.float32, (E,), dev)
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        ids = logits.new_empty((T, k), dtype=torch.int32)
         pi = ids.data_ptr()
     else:
         pi = _rows(ids, "ids", torch.int32, (T, k), dev)
     if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        weights = logits.new_empty((T, k), dtype=torch.float32)
         pw = weights.data_ptr()
     else:
         pw = _rows(weights, "weights", torch.float32, (T, k), dev)
@@ -157,7 +157,7 @@ def moe_route_backward(grad, logits, ids, score: str = "softmax", renormalize: b
     pi = _rows(ids, "ids", torch.int32, (T, k), dev)
     pg = _rows(grad, "grad", torch.float32, (T, k), dev)
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        dlogits = logits.new_empty((T, E))
         ldd = E
     else:
         ldd = _result(dlogits, "dlogits", (logits.dtype,), (T, E), dev)
@@ -219,7 +219,7 @@ def w4a16_gemm_groupwise_packed(x, wpacked, n: int, gc: int = 128, out_dtype=tor
     if y is None:
         if out_dtype not in _CODE:
             raise SgError(f"out_dtype {out_dtype} not supported (float32 or bfloat16)")
-        y = torch.empty((M, n), dtype=out_dtype, device=dev)
+        y = x.new_empty((M, n), dtype=out_dtype)
         ldy = n
     else:
         ldy = _result(y, "y", _FB, (M, n), dev)
@@ -270,14 +270,14 @@ def w4a16_moe_mlp(x, ids, weights, gate, up, down, f: int, gc: int = 128, out_dt
     pd = _rows(down, "down", torch.uint8, (E, _packed_bytes(D, f, gc)), dev)
     need = _moe_need(T, k, E, D, f)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = ids.new_empty(need, dtype=torch.uint8)
     elif not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or not workspace.is_contiguous() \
             or workspace.numel() < need or workspace.device != dev:
         raise SgError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {dev}")
     if y is None:
         if out_dtype not in _CODE:
             raise SgError(f"out_dtype {out_dtype} not supported (float32 or bfloat16)")
-        y = torch.empty((T, D), dtype=out_dtype, device=dev)
+        y = x.new_empty((T, D), dtype=out_dtype)
         ldy = D
     else:
         ldy = _result(y, "y", _FB, (T, D), dev)

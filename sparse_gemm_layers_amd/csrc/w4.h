@@ -58,10 +58,12 @@ __device__ __forceinline__ float w4_code(uint32_t w) {
 // three significant bits), 13 instructions: 8 conversions that pick their byte,
 // one shift for the odd codes, 4 joins of two high halves.  w4_pair<B> is the
 // B-th pair.
+__device__ __forceinline__ int w4_join(float even, float odd) {
+  return (int)__builtin_amdgcn_perm(__float_as_uint(odd), __float_as_uint(even), 0x07060302u);
+}
 template <int B>
 __device__ __forceinline__ int w4_pair(int code) {
-  return (int)__builtin_amdgcn_perm(__float_as_uint(w4_code<B>((uint32_t)code >> 4)),
-                                    __float_as_uint(w4_code<B>((uint32_t)code)), 0x07060302u);
+  return w4_join(w4_code<B>((uint32_t)code), w4_code<B>((uint32_t)code >> 4));
 }
 __device__ __forceinline__ v4i w4_widen(int code) {
   return (v4i){w4_pair<0>(code), w4_pair<1>(code), w4_pair<2>(code), w4_pair<3>(code)};

@@ -58,8 +58,9 @@ struct W4Tile {
       for (int j = 0; j < 8; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
     int cur = 0, nxt = STAGE, far = 2 * STAGE;   // the stages of kb, kb + 1, kb + 2
 
-    // Loads past the last K block go through descriptors without records: they
-    // read zeros and touch no memory.  The columns past K of the last block are W4_OUT.
+    // Loads past the last K block read that block again, columns past K of it are
+    // W4_OUT: the same few scalar instructions for every block (a wave issues one
+    // instruction in 8 cycles, of whatever kind).
     const int c = 8 * ((l & 7) ^ swz8q(l >> 3));   // first column of this lane's piece; its rows mod 8 are l >> 3
     uint32_t xv[2][2], xlast[2][2];
 #pragma unroll
@@ -70,27 +71,25 @@ struct W4Tile {
         xlast[u][h] = (s.KB - 1) * 128 + 64 * h + c < s.K ? xv[u][h] : W4_OUT;
       }
     const uint32_t cv = 16 * l, sv = l < 16 * P::NG ? (uint32_t)(W4_CODES + 4 * l) : W4_OUT;
+    const __amdgpu_buffer_rsrc_t rx = w4_rsrc(s.x, s.x_bytes), rw0 = w4_rsrc(s.w[0], s.w_bytes[0]),
+                                 rw1 = w4_rsrc(s.w[1], s.w_bytes[1]);
     const auto load_codes = [&](int i, int stage, int kb) {
-      const bool in = kb < s.KB;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(w4_rsrc(s.w[i], in ? s.w_bytes[i] : 0u),
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(i ? rw1 : rw0,
                                                (w4_lds_t*)(lds + stage + W_OFF + (2 * wave + i) * W4_CODES), 16, cv,
-                                               in ? kb * P::CHUNK : 0, 0, 0);
+                                               min(kb, s.KB - 1) * P::CHUNK, 0, 0);
     };
     // load group b: codes of b + 1, scales and X of b, one at a time
     const auto load_one = [&](int n, int codes, int x, int b) {
-      const bool in = b < s.KB;
       if (n < 2) {
         load_codes(n, codes, b + 1);
       } else if (n < 4) {
-        const int i = n - 2;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            w4_rsrc(s.w[i], in ? s.w_bytes[i] : 0u),
-            (w4_lds_t*)(lds + S_OFF + (b & 3) * S_STAGE + (2 * wave + i) * 256), 4, sv, in ? b * P::CHUNK : 0, 0, 0);
+            n == 3 ? rw1 : rw0, (w4_lds_t*)(lds + S_OFF + (b & 3) * S_STAGE + (2 * wave + n - 2) * 256), 4, sv,
+            min(b, s.KB - 1) * P::CHUNK, 0, 0);
       } else {
         const int u = (n - 4) >> 1, h = n & 1;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            w4_rsrc(s.x, in ? s.x_bytes : 0u), (w4_lds_t*)(lds + x + h * (BM * 128) + (8 * u + wave) * 1024), 16,
-            b == s.KB - 1 ? xlast[u][h] : xv[u][h], in ? b * 256 : 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (w4_lds_t*)(lds + x + h * (BM * 128) + (8 * u + wave) * 1024), 16,
+                                                 b >= s.KB - 1 ? xlast[u][h] : xv[u][h], min(b, s.KB - 1) * 256, 0, 0);
       }
     };
     const auto load = [&](int codes, int x, int b) {
@@ -112,14 +111,20 @@ struct W4Tile {
     };
 
     v4i aw[2][2][4], bx[2][4], cw[2];
-    v4f p[2][2][2], sw[2][2];   // sums of the group in work and of the one before, and their scales
+    // Sums of the group in work and of the one before; the scales of the block's
+    // groups, each read anew for the next block once its last sums are scaled.
+    v4f p[2][2][2], sw[P::NG][2];
+    const v4f zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int i = 0; i < 2; ++i) {
+      p[0][i][0] = p[0][i][1] = p[1][i][0] = p[1][i][1] = zero;
+      sw[P::NG - 1][i] = zero;   // of the group before the first
+    }
+    const auto read_scales = [&](int u, int kb) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        sw[t][i] = (v4f){0.f, 0.f, 0.f, 0.f};
-        p[t][i][0] = p[t][i][1] = sw[t][i];
-      }
+      for (int i = 0; i < 2; ++i)
+        sw[u][i] = *reinterpret_cast<const v4f*>(lds + so + (kb & 3) * S_STAGE + i * 256 + u * 64);
+    };
     w4_wait<2 * LOADS>();
 #pragma unroll
     for (int i = 0; i < 2; ++i) cw[i] = *reinterpret_cast<const v4i*>(lds + cur + wo + i * W4_CODES);
@@ -134,6 +139,8 @@ struct W4Tile {
 #pragma unroll
     for (int q = 0; q < 4; ++q) read_x(bx, cur, 0, q);
 #pragma unroll
+    for (int u = 0; u < P::NG - 1; ++u) read_scales(u, 0);
+#pragma unroll
     for (int i = 0; i < 2; ++i) cw[i] = *reinterpret_cast<const v4i*>(lds + nxt + wo + i * W4_CODES);
 
     // One K block: JP pairs of sub-tile columns, 16 matrix instructions each.
@@ -147,8 +154,8 @@ struct W4Tile {
     const auto block = [&](int kb, auto pa, auto pu) {
       constexpr int PA = decltype(pa)::value, PU = decltype(pu)::value;
       constexpr int L = 4 * P::QPG;   // matrix instructions per group
-      const uint8_t* const sp = lds + so + (kb & 3) * S_STAGE;
       v4i ahead[2];   // codes of kb + 2
+      float half0 = 0.f, half1 = 0.f;
 #pragma unroll
       for (int jj = 0; jj < JP; ++jj) {
 #pragma unroll
@@ -156,27 +163,26 @@ struct W4Tile {
           const int q = t >> 2, i = (t >> 1) & 1, c = t & 1;
           const int u = jj * P::NG + t / L, in = t % L;   // group of the block, instruction of the group
           const int now = (PU + u) & 1, old = now ^ 1;
-          const int oj = u == 0 ? JP - 1 : (u - 1) / P::NG;   // pair of the group before
-          if (in == 0) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              sw[now][k] = *reinterpret_cast<const v4f*>(sp + k * 256 + (t / L) * 64);
-          }
+          const int oj = u == 0 ? JP - 1 : (u - 1) / P::NG;        // pair of the group before,
+          const int og = (u + P::NG - 1) % P::NG;                  // its place among the block's groups
+          // both X operands of these 32 columns: six reads at least were asked for after them
+          if ((t & 3) == 0) __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (7 << 4) | (6 << 8));
           p[now][i][c] = w4_mfma(aw[PA][i][q], bx[c][q], in < 4 ? (v4f){0.f, 0.f, 0.f, 0.f} : p[now][i][c]);
           if (in % P::QPG == P::QPG / 2) {
             const int k = in / P::QPG, ki = k >> 1, kc = k & 1;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              acc[ki][2 * oj + kc][e] = fmaf(p[old][ki][kc][e], sw[old][ki][e], acc[ki][2 * oj + kc][e]);
+              acc[ki][2 * oj + kc][e] = fmaf(p[old][ki][kc][e], sw[og][ki][e], acc[ki][2 * oj + kc][e]);
           }
+          if (in == L - 1 && oj == JP - 1) read_scales(og, u == 0 ? kb : kb + 1);
 #pragma unroll
           for (int d = (jj * 16 + t) * 2 / JP; d < (jj * 16 + t + 1) * 2 / JP; ++d) {
-            const int wi = (d >> 2) & 1, wq = d >> 3;
-            const int w = cw[wi][wq];
-            aw[PA ^ 1][wi][wq][d & 3] = (d & 3) == 0   ? w4_pair<0>(w)
-                                        : (d & 3) == 1 ? w4_pair<1>(w)
-                                        : (d & 3) == 2 ? w4_pair<2>(w)
-                                                       : w4_pair<3>(w);
+            // a pair's halves are joined a step later: right after the conversions a wait would come between
+            if (d > 0) aw[PA ^ 1][((d - 1) >> 2) & 1][(d - 1) >> 3][(d - 1) & 3] = w4_join(half0, half1);
+            const int w = cw[(d >> 2) & 1][d >> 3];
+            half0 = (d & 3) == 0 ? w4_code<0>(w) : (d & 3) == 1 ? w4_code<1>(w) : (d & 3) == 2 ? w4_code<2>(w) : w4_code<3>(w);
+            const uint32_t h = (uint32_t)w >> 4;
+            half1 = (d & 3) == 0 ? w4_code<0>(h) : (d & 3) == 1 ? w4_code<1>(h) : (d & 3) == 2 ? w4_code<2>(h) : w4_code<3>(h);
           }
           if (jj == JP - 1) {
             if (t == 2) {
@@ -197,6 +203,7 @@ struct W4Tile {
           __builtin_amdgcn_sched_barrier(0);
         }
       }
+      aw[PA ^ 1][1][3][3] = w4_join(half0, half1);
 #pragma unroll
       for (int i = 0; i < 2; ++i) cw[i] = ahead[i];
       const int was = cur;
@@ -221,7 +228,7 @@ struct W4Tile {
       for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          acc[i][2 * JP - 2 + c][e] = fmaf(odd ? p[0][i][c][e] : p[1][i][c][e], odd ? sw[0][i][e] : sw[1][i][e],
+          acc[i][2 * JP - 2 + c][e] = fmaf(odd ? p[0][i][c][e] : p[1][i][c][e], sw[P::NG - 1][i][e],
                                            acc[i][2 * JP - 2 + c][e]);
     w4_wait<0>();   // loads past the end write their zeros before LDS is given up
   }
