@@ -119,11 +119,11 @@ __global__ void __launch_bounds__(512) k_w4_rows(W4Args a, int out_bf16) {
 #endif  // SG_DEVICE_PASS
 }
 
-// Many rows: tiles of 256 W rows x 128 X rows (w4_tile.h).
-template <int GC, bool OUT_BF16>
-__global__ void __launch_bounds__(512) k_w4_gemm(W4Args a, int tiles_m, int tiles_n) {
+// Many rows: tiles of 128 IW W rows x 128 X rows (w4_tile.h).
+template <int GC, int IW>
+__global__ void __launch_bounds__(512) k_w4_gemm(W4Args a, int tiles_m, int tiles_n, int out_bf16) {
 #if SG_DEVICE_PASS
-  using T = W4Tile<GC>;
+  using T = W4Tile<GC, IW>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   int tn, tm;
   tile_coords(tiles_m, tiles_n, tn, tm);
@@ -136,19 +136,22 @@ __global__ void __launch_bounds__(512) k_w4_gemm(W4Args a, int tiles_m, int tile
   s.x = a.x + m0 * a.ldx;
   s.x_bytes = (uint32_t)(((xrows - 1) * a.ldx + a.K) * 2);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t rb = (n0 >> 4) + 2 * wave + i;
+  for (int i = 0; i < IW; ++i) {
+    const int64_t rb = (n0 >> 4) + IW * wave + i;
     s.w[i] = a.w + rb * s.KB * T::P::CHUNK;
     s.w_bytes[i] = rb * 16 < a.N ? (uint32_t)(s.KB * T::P::CHUNK) : 0u;
-    const int r = T::x_row(i, wave, l);
-    s.xoff[i] = r < xrows ? (uint32_t)(r * a.ldx * 2) : W4_OUT;
   }
-  v4f acc[2][8];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = T::x_row(u, wave, l);
+    s.xoff[u] = r < xrows ? (uint32_t)(r * a.ldx * 2) : W4_OUT;
+  }
+  v4f acc[IW][8];
   T::template multiply<4>(lds, s, wave, l, acc);
   const int g = l >> 4, lr = l & 15;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t n = n0 + (2 * wave + i) * 16 + 4 * g;
+  for (int i = 0; i < IW; ++i) {
+    const int64_t n = n0 + (IW * wave + i) * 16 + 4 * g;
     float b[4] = {0.f, 0.f, 0.f, 0.f};
     if (a.bias) {
 #pragma unroll
@@ -159,7 +162,8 @@ __global__ void __launch_bounds__(512) k_w4_gemm(W4Args a, int tiles_m, int tile
       v4f v;
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = fmaf(acc[i][j][e], W4_UNIT, b[e]);
-      store_quad<OUT_BF16, false>(a, m0 + j * 16 + lr, n, v);
+      if (out_bf16) store_quad<true, false>(a, m0 + j * 16 + lr, n, v);
+      else store_quad<false, false>(a, m0 + j * 16 + lr, n, v);
     }
   }
 #endif  // SG_DEVICE_PASS
@@ -170,14 +174,21 @@ static void launch_w4_rows(const W4Args& a, bool b16, hipStream_t st) {
   k_w4_rows<GC, RB, XI><<<dim3((unsigned)cdiv(a.N, 16 * RB), (unsigned)cdiv(a.M, 4 * XI)), 512, 0, st>>>(a, b16);
 }
 
-// Time of the busiest compute unit per K block of 128, in units that make one
-// wave of workgroups comparable: rb blocks of W rows and 4 xi X rows each
-// (w4_rows.h), or one 256 x 128 tile.  4096 x 4096 at 64 rows: xi 8, rb 2 (308)
-// 7.8 us, 12, 2 (372) 9.0, 16, 2 (436) 10.1, 16, 4 (616) 14.0; tiles 50.5.
+// Time of the busiest compute unit per K block of 128, in units of 0.02 us at K =
+// 4096: rb blocks of W rows and 4 xi X rows each (w4_rows.h), or tiles (w4_tile.h).
+// 4096 x 4096, us: 64 rows: xi 8, rb 2 (308) 7.3; 12, 2 (372) 8.3; 16, 2 (436) 9.9;
+// 16, 4 (616) 13.6.  16, 4 / tiles: 256 rows 15.8 / 30.6, 512 30.1 / 32.7, 600 40.4 /
+// 32.7, 1024 53.7 / 38.4.
 static int64_t w4_rows_cost(int64_t M, int64_t N, int rb, int xi) {
   return cdiv(cdiv(N, 16 * rb) * cdiv(M, 4 * xi), 256) * (16 * xi + 90 * rb);
 }
-static int64_t w4_tile_cost(int64_t M, int64_t N) { return cdiv(cdiv(N, 256) * cdiv(M, 128), 256) * 2400; }
+// Half tiles (128 W rows) where they do not fill the card: 1024 rows 38.4 us for 56.
+static bool w4_half_tiles(int64_t M, int64_t N) { return cdiv(N, 128) * cdiv(M, 128) <= 256; }
+static int64_t w4_tile_cost(int64_t M, int64_t N) {
+  if (w4_half_tiles(M, N)) return 1300 + cdiv(N, 128) * cdiv(M, 128) * 8 / 5;
+  const int64_t tiles = cdiv(N, 256) * cdiv(M, 128);
+  return tiles < 256 ? 1600 + tiles * 32 / 5 : cdiv(tiles, 256) * 3240;
+}
 
 template <int GC>
 static void launch_w4(const W4Args& a, bool b16, hipStream_t st) {
@@ -187,10 +198,9 @@ static void launch_w4(const W4Args& a, bool b16, hipStream_t st) {
       for (int r = x == 16 ? 2 : 1; r <= (x == 4 ? 2 : 4); r *= 2)   // 16, 1 costs more than 8, 2 everywhere
         if (w4_rows_cost(a.M, a.N, r, x) < w4_rows_cost(a.M, a.N, rb, xi)) rb = r, xi = x;
   if (cdiv(a.M, 4 * xi) > 65535 || w4_tile_cost(a.M, a.N) < w4_rows_cost(a.M, a.N, rb, xi)) {
-    using T = W4Tile<GC>;
-    const int64_t tm = cdiv(a.M, T::BM), tn = cdiv(a.N, T::BN);
-    if (b16) k_w4_gemm<GC, true><<<(unsigned)(tm * tn), 512, 0, st>>>(a, (int)tm, (int)tn);
-    else k_w4_gemm<GC, false><<<(unsigned)(tm * tn), 512, 0, st>>>(a, (int)tm, (int)tn);
+    const int64_t tm = cdiv(a.M, 128), tn = cdiv(a.N, 256), tn1 = cdiv(a.N, 128);
+    if (w4_half_tiles(a.M, a.N)) k_w4_gemm<GC, 1><<<(unsigned)(tm * tn1), 512, 0, st>>>(a, (int)tm, (int)tn1, b16);
+    else k_w4_gemm<GC, 2><<<(unsigned)(tm * tn), 512, 0, st>>>(a, (int)tm, (int)tn, b16);
     return;
   }
   switch (10 * xi + rb) {

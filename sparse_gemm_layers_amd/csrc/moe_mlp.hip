@@ -342,10 +342,10 @@ __global__ void __launch_bounds__(512) k_moe_stream(MoeArgs a, int R) {
 
 #if SG_DEVICE_PASS
 // The tile's product over its first `rows` pairs, in steps of 32.
-template <int GC>
-__device__ __forceinline__ void multiply_rows(uint8_t* lds, const typename W4Tile<GC>::Src& s, int rows, int wave,
-                                              int l, v4f (&acc)[2][8]) {
-  using T = W4Tile<GC>;
+template <int GC, int IW>
+__device__ __forceinline__ void multiply_rows(uint8_t* lds, const typename W4Tile<GC, IW>::Src& s, int rows, int wave,
+                                              int l, v4f (&acc)[IW][8]) {
+  using T = W4Tile<GC, IW>;
   if (rows > 96) T::template multiply<4>(lds, s, wave, l, acc);
   else if (rows > 64) T::template multiply<3>(lds, s, wave, l, acc);
   else if (rows > 32) T::template multiply<2>(lds, s, wave, l, acc);
@@ -353,12 +353,14 @@ __device__ __forceinline__ void multiply_rows(uint8_t* lds, const typename W4Til
 }
 #endif  // SG_DEVICE_PASS
 
-// Many pairs per expert: tiles of MOE_BM pairs of one expert.  Gate and up: 128
-// rows of each, a wave's first slot is gate's row block, its second the same of up's.
-template <int GC>
+// Many pairs per expert: tiles of MOE_BM pairs of one expert.  Gate and up, 64 IW
+// rows of each.  IW = 2: a wave's first slot is gate's row block, its second the
+// same of up's; IW = 1: waves 0 .. 3 have gate's row blocks, 4 .. 7 up's, and
+// hand their sums over in LDS.
+template <int GC, int IW>
 __global__ void __launch_bounds__(512) k_moe_gate_up(MoeArgs a, int tiles_n) {
 #if SG_DEVICE_PASS
-  using T = W4Tile<GC>;
+  using T = W4Tile<GC, IW>;
   static_assert(T::BM == MOE_BM, "tile");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   const int tile = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
@@ -368,11 +370,13 @@ __global__ void __launch_bounds__(512) k_moe_gate_up(MoeArgs a, int tiles_n) {
   typename T::Src s;
   s.K = a.D;
   s.KB = (a.D + 127) >> 7;
-  const int fb = tn * 8 + wave;
+  const int fb = tn * 4 * IW + (IW == 2 ? wave : wave & 3);
   const int64_t at = (int64_t)e * a.gu_bytes + (int64_t)fb * s.KB * T::P::CHUNK;
-  s.w[0] = a.gate + at;
-  s.w[1] = a.up + at;
-  s.w_bytes[0] = s.w_bytes[1] = fb * 16 < a.F ? (uint32_t)(s.KB * T::P::CHUNK) : 0u;
+#pragma unroll
+  for (int i = 0; i < IW; ++i) {
+    s.w[i] = ((IW == 2 ? i : wave >> 2) ? a.up : a.gate) + at;
+    s.w_bytes[i] = fb * 16 < a.F ? (uint32_t)(s.KB * T::P::CHUNK) : 0u;
+  }
   s.x = a.x;
   s.x_bytes = (uint32_t)(((a.T - 1) * a.ldx + a.D) * 2);
 #pragma unroll
@@ -380,26 +384,36 @@ __global__ void __launch_bounds__(512) k_moe_gate_up(MoeArgs a, int tiles_n) {
     const int r = T::x_row(u, wave, l);
     s.xoff[u] = r < rows ? (uint32_t)((int64_t)(a.list[m0 + r] / a.k) * a.ldx * 2) : W4_OUT;
   }
-  v4f acc[2][8];
-  multiply_rows<GC>(lds, s, rows, wave, l, acc);
+  v4f acc[IW][8];
+  multiply_rows<GC, IW>(lds, s, rows, wave, l, acc);
+  if (IW == 1) {
+    lds_barrier();   // every wave is done with the stages
+    if (wave >= 4) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) *reinterpret_cast<v4f*>(lds + ((wave - 4) * 8 + j) * 1024 + 16 * l) = acc[0][j];
+    }
+    __syncthreads();
+    if (wave >= 4) return;
+  }
   const int f = fb * 16 + 4 * (l >> 4), lr = l & 15;
   if (f >= a.F) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     if (16 * j + lr >= rows) continue;
+    const v4f up = IW == 2 ? acc[IW - 1][j] : *reinterpret_cast<const v4f*>(lds + (wave * 8 + j) * 1024 + 16 * l);
     float h[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) h[q] = silu(acc[0][j][q] * W4_UNIT) * (acc[1][j][q] * W4_UNIT);
+    for (int q = 0; q < 4; ++q) h[q] = silu(acc[0][j][q] * W4_UNIT) * (up[q] * W4_UNIT);
     *reinterpret_cast<uint2*>(a.h + (int64_t)(m0 + 16 * j + lr) * a.F + f) =
         make_uint2(f32x2_to_bf16x2(h[0], h[1]), f32x2_to_bf16x2(h[2], h[3]));
   }
 #endif  // SG_DEVICE_PASS
 }
 
-template <int GC>
+template <int GC, int IW>
 __global__ void __launch_bounds__(512) k_moe_down(MoeArgs a, int tiles_n) {
 #if SG_DEVICE_PASS
-  using T = W4Tile<GC>;
+  using T = W4Tile<GC, IW>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   const int tile = blockIdx.x / tiles_n, tn = blockIdx.x % tiles_n;
   if (tile >= a.tile[0]) return;
@@ -410,23 +424,26 @@ __global__ void __launch_bounds__(512) k_moe_down(MoeArgs a, int tiles_n) {
   s.KB = (a.F + 127) >> 7;
   s.x = a.h + (int64_t)m0 * a.F;
   s.x_bytes = (uint32_t)(rows * a.F * 2);
-  const int rb0 = tn * 16 + 2 * wave;
+  const int rb0 = (tn * 8 + wave) * IW;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < IW; ++i) {
     s.w[i] = a.down + (int64_t)e * a.d_bytes + (int64_t)(rb0 + i) * s.KB * T::P::CHUNK;
     s.w_bytes[i] = (rb0 + i) * 16 < a.D ? (uint32_t)(s.KB * T::P::CHUNK) : 0u;
-    const int r = T::x_row(i, wave, l);
-    s.xoff[i] = r < rows ? (uint32_t)(r * a.F * 2) : W4_OUT;
   }
-  v4f acc[2][8];
-  multiply_rows<GC>(lds, s, rows, wave, l, acc);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = T::x_row(u, wave, l);
+    s.xoff[u] = r < rows ? (uint32_t)(r * a.F * 2) : W4_OUT;
+  }
+  v4f acc[IW][8];
+  multiply_rows<GC, IW>(lds, s, rows, wave, l, acc);
   const int g = l >> 4, lr = l & 15;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     if (16 * j + lr >= rows) continue;
     float* const row = a.o + (int64_t)a.list[m0 + 16 * j + lr] * a.D;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < IW; ++i) {
       const int n = (rb0 + i) * 16 + 4 * g;
       if (n < a.D) *reinterpret_cast<v4f*>(row + n) = acc[i][j] * W4_UNIT;
     }
@@ -497,11 +514,14 @@ static void launch_moe_stream(const MoeArgs& a, hipStream_t st) {
   k_moe_stream<GC, DOWN><<<dim3((unsigned)gx, (unsigned)gy), 512, 512 + R * cdiv(K, 128) * 256, st>>>(a, R);
 }
 
-// Which way: us of 64 experts (4096, 1024), k 8 / 60 experts (2048, 1408), k 4.
-//   pairs      16         32          128          256        512
-//   few      27 / 28    68 / 51    163 / 114    205 / 155  301 / 218
-//   stream   43 / 29    54 / 43     83 /  76    155 /  84  212 / 154
-//   tiles    53 / 40    65 / 42    104 /  76    119 /  79  120 / 103
+// Which way: us of 64 experts (4096, 1024), k 8 / 60 experts (2048, 1408), k 4 / 9
+// experts (2016, 1216), k 2.
+//   pairs         few        stream       tiles
+//   16          27 / 28     43 / 29      53 / 40
+//   32          68 / 51     54 / 43      65 / 57 / 31
+//   128        163 / 114    85 / 73      99 / 73 / 33
+//   256        205 / 155   137 / 93     109 / 90
+//   512        301 / 218   253 / 160    120 / 95
 // Streaming passes over an expert's weights once for every R of its pairs, so it
 // is taken while an expert has R / 4 on average (some have several times that).
 template <int GC>
@@ -518,9 +538,13 @@ static void launch_moe(const MoeArgs& a, bool bf16, hipStream_t st) {
     launch_moe_stream<GC, true>(a, st);
   } else {
     k_moe_plan<<<1, 1024, 0, st>>>(a);
-    const int tm = (int)moe_tiles(a.P, a.E), ng = (int)cdiv(a.F, 128), nd = (int)cdiv(a.D, 256);
-    k_moe_gate_up<GC><<<(unsigned)(tm * ng), 512, 0, st>>>(a, ng);
-    k_moe_down<GC><<<(unsigned)(tm * nd), 512, 0, st>>>(a, nd);
+    // tiles there may be, and about as many as there are: half an expert's last one is empty
+    const int64_t tm = moe_tiles(a.P, a.E), about = cdiv(a.P, MOE_BM) + (a.P < a.E ? a.P : a.E) / 2;
+    const int64_t ng = cdiv(a.F, 128), nd = cdiv(a.D, 256);
+    if (about * ng <= 256) k_moe_gate_up<GC, 1><<<(unsigned)(tm * cdiv(a.F, 64)), 512, 0, st>>>(a, (int)cdiv(a.F, 64));
+    else k_moe_gate_up<GC, 2><<<(unsigned)(tm * ng), 512, 0, st>>>(a, (int)ng);
+    if (about * nd <= 256) k_moe_down<GC, 1><<<(unsigned)(tm * cdiv(a.D, 128)), 512, 0, st>>>(a, (int)cdiv(a.D, 128));
+    else k_moe_down<GC, 2><<<(unsigned)(tm * nd), 512, 0, st>>>(a, (int)nd);
   }
   const unsigned grid = grid_for(a.T * (a.D / 4), 256, 8192);
   if (bf16) k_moe_combine<true><<<grid, 256, 0, st>>>(a);
