@@ -78,10 +78,8 @@ __global__ void __launch_bounds__(512) k_w4_rows(W4Args a, int out_bf16) {
   s.x = a.x + m0 * a.ldx;
   s.x_bytes = (uint32_t)(((xrows - 1) * a.ldx + a.K) * 2);
 #pragma unroll
-  for (int rb = 0; rb < RB; ++rb) {
-    s.w[rb] = a.w + (rb0 + rb) * s.KB * T::P::CHUNK;
-    s.w_bytes[rb] = (rb0 + rb) * 16 < a.N ? (uint32_t)(s.KB * T::P::CHUNK) : 0u;
-  }
+  for (int rb = 0; rb < RB; ++rb)   // past N the last one again: nothing of it is stored
+    s.w[rb] = a.w + min(rb0 + rb, (a.N - 1) >> 4) * s.KB * T::P::CHUNK;
 #pragma unroll
   for (int i = 0; i < XI; ++i) {
     const int r = 4 * i + (l >> 4);
@@ -136,11 +134,8 @@ __global__ void __launch_bounds__(512) k_w4_gemm(W4Args a, int tiles_m, int tile
   s.x = a.x + m0 * a.ldx;
   s.x_bytes = (uint32_t)(((xrows - 1) * a.ldx + a.K) * 2);
 #pragma unroll
-  for (int i = 0; i < IW; ++i) {
-    const int64_t rb = (n0 >> 4) + IW * wave + i;
-    s.w[i] = a.w + rb * s.KB * T::P::CHUNK;
-    s.w_bytes[i] = rb * 16 < a.N ? (uint32_t)(s.KB * T::P::CHUNK) : 0u;
-  }
+  for (int i = 0; i < IW; ++i)   // past N the last row block again: nothing of it is stored
+    s.w[i] = a.w + min((n0 >> 4) + IW * wave + i, (a.N - 1) >> 4) * s.KB * T::P::CHUNK;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int r = T::x_row(u, wave, l);

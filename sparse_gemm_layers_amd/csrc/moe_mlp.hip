@@ -42,7 +42,7 @@ struct MoeArgs {
 
 // One workgroup counts, sums and places the pairs.  Up to 16 pairs a thread stay
 // in registers between counting and placing, each with its rank in its expert.
-// (16384 pairs: 18 us when the ids were read and counted twice, @@ so.)
+// (16384 pairs: 18 us when the ids were read and counted twice, 12 so.)
 constexpr int PLAN_KEEP = 16;
 __global__ void __launch_bounds__(1024) k_moe_plan(MoeArgs a) {
   __shared__ int cnt[MOE_EMAX], wsum[16], wtiles[16];
@@ -115,13 +115,22 @@ __device__ __forceinline__ int find_pairs(const int32_t* ids, int P, int v, int 
                                           int& first) {
   int cnt = 0;
   first = P;
-  for (int c = 0; c < P; c += 64) {
-    const bool hit = c == 0 ? v == e : c + l < P && ids[c + l] == e;
-    const uint64_t m = __ballot(hit);
-    const int rank = cnt + __builtin_popcountll(m & ((1ull << l) - 1)) - m0;
-    if (hit && rank >= 0 && rank < n) list[rank] = c + l;
-    if (cnt == 0 && m) first = c + __builtin_ctzll(m);
-    cnt += __builtin_popcountll(m);
+  for (int c0 = 0; c0 < P; c0 += 512) {
+    int id[8];   // all on their way before the first is looked at
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int p = c0 + 64 * i + l;
+      id[i] = p == l ? v : p < P ? ids[p] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool hit = id[i] == e;
+      const uint64_t m = __ballot(hit);
+      const int rank = cnt + __builtin_popcountll(m & ((1ull << l) - 1)) - m0;
+      if (hit && rank >= 0 && rank < n) list[rank] = c0 + 64 * i + l;
+      if (cnt == 0 && m) first = c0 + 64 * i + __builtin_ctzll(m);
+      cnt += __builtin_popcountll(m);
+    }
   }
   wave_order();
   return cnt;
@@ -176,7 +185,6 @@ __global__ void __launch_bounds__(512) k_moe_gate_up_rows(MoeArgs a) {
   const int64_t at = (int64_t)e * a.gu_bytes + (int64_t)blockIdx.x * s.KB * T::P::CHUNK;
   s.w[0] = a.gate + at;
   s.w[1] = a.up + at;
-  s.w_bytes[0] = s.w_bytes[1] = (uint32_t)(s.KB * T::P::CHUNK);
   int first, cnt = 1;
   for (int m0 = 0; m0 < cnt; m0 += 4 * XI) {
     cnt = find_pairs(a.ids, P, v, e, m0, 4 * XI, list, l, first);
@@ -232,7 +240,6 @@ __global__ void __launch_bounds__(512) k_moe_down_join(MoeArgs a, int out_bf16) 
   s.KB = (a.F + 127) >> 7;
   s.x = a.h;
   s.x_bytes = (uint32_t)(a.P * a.F * 2);
-  s.w_bytes[0] = (uint32_t)(s.KB * T::P::CHUNK);
   v4f sum = {0.f, 0.f, 0.f, 0.f};
   int at = 0;   // rank of the expert in hand
   for (; lead; lead &= lead - 1, ++at) {
@@ -371,12 +378,10 @@ __global__ void __launch_bounds__(512) k_moe_gate_up(MoeArgs a, int tiles_n) {
   s.K = a.D;
   s.KB = (a.D + 127) >> 7;
   const int fb = tn * 4 * IW + (IW == 2 ? wave : wave & 3);
-  const int64_t at = (int64_t)e * a.gu_bytes + (int64_t)fb * s.KB * T::P::CHUNK;
+  // past F the last row block again: nothing of it is stored
+  const int64_t at = (int64_t)e * a.gu_bytes + (int64_t)min(fb, (a.F - 1) >> 4) * s.KB * T::P::CHUNK;
 #pragma unroll
-  for (int i = 0; i < IW; ++i) {
-    s.w[i] = ((IW == 2 ? i : wave >> 2) ? a.up : a.gate) + at;
-    s.w_bytes[i] = fb * 16 < a.F ? (uint32_t)(s.KB * T::P::CHUNK) : 0u;
-  }
+  for (int i = 0; i < IW; ++i) s.w[i] = ((IW == 2 ? i : wave >> 2) ? a.up : a.gate) + at;
   s.x = a.x;
   s.x_bytes = (uint32_t)(((a.T - 1) * a.ldx + a.D) * 2);
 #pragma unroll
@@ -426,10 +431,8 @@ __global__ void __launch_bounds__(512) k_moe_down(MoeArgs a, int tiles_n) {
   s.x_bytes = (uint32_t)(rows * a.F * 2);
   const int rb0 = (tn * 8 + wave) * IW;
 #pragma unroll
-  for (int i = 0; i < IW; ++i) {
-    s.w[i] = a.down + (int64_t)e * a.d_bytes + (int64_t)(rb0 + i) * s.KB * T::P::CHUNK;
-    s.w_bytes[i] = (rb0 + i) * 16 < a.D ? (uint32_t)(s.KB * T::P::CHUNK) : 0u;
-  }
+  for (int i = 0; i < IW; ++i)
+    s.w[i] = a.down + (int64_t)e * a.d_bytes + (int64_t)min(rb0 + i, (a.D - 1) >> 4) * s.KB * T::P::CHUNK;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int r = T::x_row(u, wave, l);

@@ -6,10 +6,10 @@
 // the matrix core wants it (lane 16 g + r: row r) takes 64, since neighbouring
 // lanes then read different rows; so X rows come whole, four per load, into
 // this wave's part of LDS and are read from there: 37 x 4096 x 14336 took 46 us
-// with operands loaded directly and takes @@.  Scales take one load of 4 bytes a
+// with operands loaded directly and takes 18.  Scales take one load of 4 bytes a
 // lane per row block (7 cycles), codes one of 16 (a packed chunk's 1 KB).
-// Codes, which come from HBM, are loaded four K blocks ahead, X rows, which L2
-// holds, two (few rows: four).
+// Codes, which come from HBM, are loaded DW K blocks ahead, X rows, which L2
+// holds, DX.
 #pragma once
 
 #include "w4.h"
@@ -29,8 +29,8 @@ struct W4Rows {
   static_assert(LDS <= 160 * 1024, "LDS");
 #if SG_DEVICE_PASS
   struct Src {
-    const void *x, *w[RB];             // w: each row block from its first chunk
-    uint32_t x_bytes, w_bytes[RB];     // at most 2^31; 0: the row block is not there
+    const void *x, *w[RB];             // w: each row block from its first chunk, KB chunks
+    uint32_t x_bytes;                  // at most 2^31
     uint32_t xoff[XI];                 // byte offset in x of row 4 i + l / 16, W4_OUT: not there
     int K, KB;
   };
@@ -62,7 +62,7 @@ struct W4Rows {
     const auto load_w = [&](int slot, int kb) {
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
-        const __amdgpu_buffer_rsrc_t rw = w4_rsrc(s.w[rb], s.w_bytes[rb]);
+        const __amdgpu_buffer_rsrc_t rw = w4_rsrc(s.w[rb], (uint32_t)(s.KB * P::CHUNK));
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (w4_lds_t*)(lds + S_OFF + (slot * RB + rb) * 256), 4, sv,
                                                  kb * P::CHUNK, 0, 0);
         cw[slot][rb] = w4_ld16(rw, (uint32_t)(16 * l), kb * P::CHUNK);

@@ -40,8 +40,8 @@ struct W4Tile {
 
 #if SG_DEVICE_PASS
   struct Src {
-    const void *x, *w[IW];            // w: this wave's row blocks, each from its first chunk
-    uint32_t x_bytes, w_bytes[IW];    // at most 2^31; 0: the row block is not there
+    const void *x, *w[IW];            // w: this wave's row blocks, each from its first chunk, KB chunks
+    uint32_t x_bytes;                 // at most 2^31
     uint32_t xoff[2];                 // byte offset in x of this lane's rows, W4_OUT: not there
     int K, KB;
   };
@@ -73,8 +73,9 @@ struct W4Tile {
         xlast[u][h] = (s.KB - 1) * 128 + 64 * h + c < s.K ? xv[u][h] : W4_OUT;
       }
     const uint32_t cv = 16 * l, sv = l < 16 * P::NG ? (uint32_t)(W4_CODES + 4 * l) : W4_OUT;
-    const __amdgpu_buffer_rsrc_t rx = w4_rsrc(s.x, s.x_bytes), rw0 = w4_rsrc(s.w[0], s.w_bytes[0]),
-                                 rw1 = w4_rsrc(s.w[IW - 1], s.w_bytes[IW - 1]);
+    const uint32_t w_bytes = (uint32_t)(s.KB * P::CHUNK);
+    const __amdgpu_buffer_rsrc_t rx = w4_rsrc(s.x, s.x_bytes), rw0 = w4_rsrc(s.w[0], w_bytes),
+                                 rw1 = w4_rsrc(s.w[IW - 1], w_bytes);
     const auto load_codes = [&](int i, int stage, int kb) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(i ? rw1 : rw0,
                                                (w4_lds_t*)(lds + stage + W_OFF + (IW * wave + i) * W4_CODES), 16, cv,
