@@ -384,14 +384,15 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {   // Batcher's odd
 // fp64 scores of every expert were most of them (16384 tokens of 256 experts in 8
 // groups: 32.6 us, 22.8 this way); here scores are fp32 and keys are whole numbers of 24 bits with
 // the expert in the low byte (255 - e, so that the lowest wins among equals), one
-// 32-bit maximum finding both.  A key is off by `err` units at most; where two
-// that the choice hangs on lie within 2 err, the token is done again by
-// route_token, which decides in fp64.  bf16 logits without a bias are exact keys.
+// 32-bit maximum finding both.  A key is off by `err` units at most; candidates
+// within 2 err of each other are put in order by their fp64 keys, and where a
+// group, or an expert that is no candidate, lies as near to those that stay, the
+// token is done again by route_token, which decides in fp64.  bf16 logits without a bias are exact keys.
 //   err, with a bias: scores are off by 2^-22 (sigmoid: exponential and reciprocal
 //   of one step each, s (1 - s) |x| <= 0.23 of the argument's rounding) or 2^-19
 //   (softmax: 3 steps of 2^-24 a term, 28 on the sum), taken twice as large; the
 //   sum s + b by half a step of |lo| + R; three roundings more of one unit at most.
-// KL: entries kept per lane (a lane gives at most k).
+// KL: entries kept per lane (a lane gives at most k + 2).
 template <int VPL, int KL, bool SCORES, bool BF16>
 __global__ void __launch_bounds__(64 * RT_WAVES) k_moe_route_rows(RouteArgs a, int vec) {
 #if SG_DEVICE_PASS
@@ -578,24 +579,45 @@ __global__ void __launch_bounds__(64 * RT_WAVES) k_moe_route_rows(RouteArgs a, i
       key[v] = key[v] ? (key[v] << 8) | (uint32_t)(255 - (64 * (v >> 2) + 4 * j + (v & 3))) : 0u;
     sort_down<VPL>(key);
 
-    // k rounds for the experts, one more for the distance to the next
-    uint32_t my = 0, before = 0;
-    for (int r = 0; r <= a.k; ++r) {
+    // k rounds for the experts, one for a candidate more, one for the distance to the next
+    const int c = min(a.k + 1, 16);
+    uint32_t my = 0, before = 0, kth = 0;
+    bool close = false;   // two candidates whose order these keys do not tell
+    for (int r = 0; r <= c; ++r) {
       const uint32_t m = row_max(key[0]);
       const uint32_t won = key[0] == m ? ~0u : 0u;   // keys differ in their expert, unless all are gone
 #pragma unroll
       for (int v = 0; v < KL; ++v) key[v] = (won & (v + 1 < KL ? key[v + 1] : 0u)) | (~won & key[v]);
-      unsure = unsure || (r > 0 && m && (int)((before >> 8) - (m >> 8)) <= th);
+      close = close || (r > 0 && r < c && m && (int)((before >> 8) - (m >> 8)) <= th);
       before = m;
-      if (j == r && r < a.k) my = m;
+      if (r == a.k - 1) kth = m;
+      if (j == r && r < c) my = m;
     }
+    // one that is no candidate may belong among the k
+    unsure = unsure || (before && (int)((kth >> 8) - (before >> 8)) <= th);
 
-    const int id = my ? 255 - (int)(my & 255) : -1;
-    double w = 0.0;
+    int id = my ? 255 - (int)(my & 255) : -1;
+    double w = 0.0, xc = 0.0;
     if (id >= 0) {
-      const double xc = (double)fminf(rt_load(a.logits, t * a.ldl + id, BF16), 3.402823466e38f);
+      xc = (double)fminf(rt_load(a.logits, t * a.ldl + id, BF16), 3.402823466e38f);
       w = a.sigmoid ? 1.0 / (1.0 + exp(-xc)) : exp(xc - (double)top) / (double)sum;
     }
+    if (a.bias && !a.sigmoid) {
+      unsure = unsure || close;   // these scores' sum is fp32
+    } else if (__ballot(close)) {
+      // the candidates anew by their fp64 keys, as route_token orders them
+      const double k64 = id < 0 ? 0.0 : a.bias ? w + (double)fminf(a.bias[id], 3.402823466e38f) : xc;
+      int rank = id < 0 ? j : 0, from = 0;
+      for (int i = 0; i < c; ++i) {
+        const double o = __shfl(k64, i, 16);
+        const int oid = __shfl(id, i, 16);
+        rank += id >= 0 && oid >= 0 && (o > k64 || (o == k64 && oid < id)) ? 1 : 0;
+      }
+      for (int i = 0; i < 16; ++i) from = __shfl(rank, i, 16) == j ? i : from;
+      id = __shfl(id, from, 16);
+      w = __shfl(w, from, 16);
+    }
+    if (j >= a.k) w = 0.0;
     if (a.renorm) w = w / fmax(row_sum(w), 1e-300);
     const uint64_t again = __ballot(unsure);
     if (here && j < a.k && ((again >> (16 * tok)) & 0xffff) == 0) {
@@ -769,7 +791,7 @@ static void launch_route_rows(const RouteArgs& a, hipStream_t st) {
   const unsigned grid = grid_for(a.T, tokens, 1024);
   const size_t lds = a.n_group > 1 ? (size_t)RT_WAVES * VPL * 36 * sizeof(double) : 0;
   const int vec = a.E % 4 == 0 && a.ldl % 4 == 0 && aligned(a.logits, BF16 ? 8 : 16);
-  if (a.k <= 8) k_moe_route_rows<VPL, VPL < 8 ? VPL : 8, F64, BF16><<<grid, 64 * RT_WAVES, lds, st>>>(a, vec);
+  if (a.k <= 10) k_moe_route_rows<VPL, VPL < 12 ? VPL : 12, F64, BF16><<<grid, 64 * RT_WAVES, lds, st>>>(a, vec);
   else k_moe_route_rows<VPL, VPL, F64, BF16><<<grid, 64 * RT_WAVES, lds, st>>>(a, vec);
 }
 
