@@ -173,7 +173,9 @@ static void launch_w4_rows(const W4Args& a, bool b16, hipStream_t st) {
 // 4096: rb blocks of W rows and 4 xi X rows each (w4_rows.h), or tiles (w4_tile.h).
 // 4096 x 4096, us: 64 rows: xi 8, rb 2 (308) 7.3; 12, 2 (372) 8.3; 16, 2 (436) 9.9;
 // 16, 4 (616) 13.6.  16, 4 / tiles: 256 rows 15.8 / 30.6, 512 30.1 / 32.7, 600 40.4 /
-// 32.7, 1024 53.7 / 38.4.
+// 32.7, 1024 53.7 / 38.4.  xi 6 and 10, for 8 and 12: 17 rows 5.6 / 6.0, 33 rows 6.9 /
+// 7.3.  Left out, since they give 2 % at most: 10, 4 (40 x 14336 x 4096 14.0 for 12, 4's
+// 14.1) and 14, 4 (56 x 14336 x 4096 16.2 for 16, 4's 16.5).
 static int64_t w4_rows_cost(int64_t M, int64_t N, int rb, int xi) {
   return cdiv(cdiv(N, 16 * rb) * cdiv(M, 4 * xi), 256) * (16 * xi + 90 * rb);
 }
@@ -189,8 +191,9 @@ template <int GC>
 static void launch_w4(const W4Args& a, bool b16, hipStream_t st) {
   int rb = 1, xi = a.M <= 4 ? 1 : a.M <= 8 ? 2 : 4;
   if (a.M > 8)
-    for (int x = 4; x <= 16 && 4 * x < a.M + 16; x += 4)
-      for (int r = x == 16 ? 2 : 1; r <= (x == 4 ? 2 : 4); r *= 2)   // 16, 1 costs more than 8, 2 everywhere
+    for (int x = 4; x <= 16 && 4 * x < a.M + 16; x += x == 12 ? 4 : 2)
+      // 16, 1 costs more than 8, 2 everywhere; 6, 4 more than 12, 2
+      for (int r = x == 16 ? 2 : 1; r <= (x <= 6 || x == 10 ? 2 : 4); r *= 2)
         if (w4_rows_cost(a.M, a.N, r, x) < w4_rows_cost(a.M, a.N, rb, xi)) rb = r, xi = x;
   if (cdiv(a.M, 4 * xi) > 65535 || w4_tile_cost(a.M, a.N) < w4_rows_cost(a.M, a.N, rb, xi)) {
     const int64_t tm = cdiv(a.M, 128), tn = cdiv(a.N, 256), tn1 = cdiv(a.N, 128);
@@ -203,9 +206,13 @@ static void launch_w4(const W4Args& a, bool b16, hipStream_t st) {
     case 21: launch_w4_rows<GC, 1, 2>(a, b16, st); break;
     case 41: launch_w4_rows<GC, 1, 4>(a, b16, st); break;
     case 42: launch_w4_rows<GC, 2, 4>(a, b16, st); break;
+    case 61: launch_w4_rows<GC, 1, 6>(a, b16, st); break;
+    case 62: launch_w4_rows<GC, 2, 6>(a, b16, st); break;
     case 81: launch_w4_rows<GC, 1, 8>(a, b16, st); break;
     case 82: launch_w4_rows<GC, 2, 8>(a, b16, st); break;
     case 84: launch_w4_rows<GC, 4, 8>(a, b16, st); break;
+    case 101: launch_w4_rows<GC, 1, 10>(a, b16, st); break;
+    case 102: launch_w4_rows<GC, 2, 10>(a, b16, st); break;
     case 121: launch_w4_rows<GC, 1, 12>(a, b16, st); break;
     case 122: launch_w4_rows<GC, 2, 12>(a, b16, st); break;
     case 124: launch_w4_rows<GC, 4, 12>(a, b16, st); break;

@@ -40,7 +40,7 @@ struct W4Rows {
   // not there hold anything.  lds: this wave's WAVE_LDS bytes.
   __device__ static __forceinline__ void multiply(uint8_t* lds, const Src& s, int first, int step, int l,
                                                   v4f (&acc)[RB][MT]) {
-    const int g = l >> 4, lr = l & 15, r0 = lr & (4 * XI - 1);   // few rows: the lanes past them repeat these
+    const int g = l >> 4, lr = l & 15;
     v4i cw[DW][RB];
     uint32_t xv[XI], xlast[XI];
     // row r's 16-byte piece c lies at c ^ (r & 15)
@@ -75,9 +75,12 @@ struct W4Rows {
 #pragma unroll
       for (int j = 0; j < MT; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          bx[j][q] = *reinterpret_cast<const v4i*>(lds + (n % DX) * XI * 1024 + (16 * j + r0) * 256 +
-                                                   (((4 * q + g) ^ r0) << 4));
+        for (int q = 0; q < 4; ++q) {
+          // lanes past the last row that is kept read rows that are
+          const int r = XI < 4 ? lr & (4 * XI - 1) : min(16 * j + lr, 4 * XI - 1);
+          bx[j][q] = *reinterpret_cast<const v4i*>(lds + (n % DX) * XI * 1024 + r * 256 +
+                                                   (((4 * q + g) ^ (r & 15)) << 4));
+        }
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
         v4i aw[4];

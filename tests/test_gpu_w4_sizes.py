@@ -13,8 +13,9 @@ from test_gpu_w4 import BF16, F32, up, weight
 pytestmark = pytest.mark.gpu
 
 # (M, N): one per split, the last three in tiles
-SIZES = [(1, 40), (7, 40), (12, 40), (12, 4100), (130, 500), (30, 4100), (30, 9000), (130, 1000), (40, 4100), (40, 9000),
-         (60, 4100), (60, 9000), (190, 16400), (1100, 3300), (2049, 1700)]
+SIZES = [(1, 40), (7, 40), (12, 40), (12, 4100), (130, 500), (17, 4136), (25, 2076), (30, 4100), (30, 9000), (130, 1000),
+         (40, 4100), (40, 9000), (2108, 65), (41, 4143), (41, 8218), (50, 4138), (49, 8444), (60, 4100), (60, 9000),
+         (190, 16400), (1100, 3300), (2049, 1700)]
 COLS = [(32, 32), (160, 32), (128, 128), (320, 64), (384, 128), (1056, 32), (2240, 64), (2048, 128)]
 
 
