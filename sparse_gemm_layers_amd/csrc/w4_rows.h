@@ -35,6 +35,16 @@ struct W4Rows {
     int K, KB;
   };
 
+  // Loads into LDS are not ordered against this wave's LDS reads: a slot is refilled
+  // once its reads are done (reads_done).  EARLY: right after the X operands have come,
+  // the first row block's codes being widened meanwhile, and the multiplication follows;
+  // otherwise after it.  Early / late, us: 24 x 4096 x 4096, groups of 32, 5.9 / 6.3; 33 x
+  // 4096 x 4096 6.6 / 7.1; 41 x 4143 x 4096, groups of 32, 9.0 / 11.9 (late spills); but 4 x
+  // 4096 x 14336 8.7 / 8.5, one token of the routed MLP 22.4 / 18.6, and with RB 4, XI 16,
+  // which spills early, 256 x 4096 x 4096 18.2 / 15.6.
+  static constexpr bool EARLY = XI >= 4 && !(RB == 4 && XI == 16);
+  __device__ static __forceinline__ void reads_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
   // acc[rb][j] += rows of block rb times X rows 16 j + l % 16 (in units of
   // W4_UNIT) over K blocks first, first + step, ...  Columns of X rows that are
   // not there hold anything.  lds: this wave's WAVE_LDS bytes.
@@ -70,7 +80,8 @@ struct W4Rows {
       w4_pin();
     };
     // X operands are read once, a row block's codes widened and its scales read once.
-    const auto compute = [&](int n) {
+    // refill: the loads into this X slot, once it has been read.
+    const auto compute = [&](int n, auto refill) {
       v4i bx[MT][4];
 #pragma unroll
       for (int j = 0; j < MT; ++j)
@@ -81,12 +92,21 @@ struct W4Rows {
           bx[j][q] = *reinterpret_cast<const v4i*>(lds + (n % DX) * XI * 1024 + r * 256 +
                                                    (((4 * q + g) ^ (r & 15)) << 4));
         }
+      v4i aw[4];
+      if (EARLY) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) aw[q] = w4_widen(cw[n][0][q]);
+        __builtin_amdgcn_sched_barrier(0);
+        reads_done();
+        refill();
+      }
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb) {
-        v4i aw[4];
         v4f sw[P::NG];
+        if (rb > 0 || !EARLY) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) aw[q] = w4_widen(cw[n][rb][q]);
+          for (int q = 0; q < 4; ++q) aw[q] = w4_widen(cw[n][rb][q]);
+        }
 #pragma unroll
         for (int t = 0; t < P::NG; ++t)
           sw[t] = *reinterpret_cast<const v4f*>(lds + S_OFF + (n * RB + rb) * 256 + t * 64 + 16 * g);
@@ -115,8 +135,10 @@ struct W4Rows {
 #pragma unroll
       for (int n = 0; n < DW; ++n) {
         w4_wait<FLY>();
-        compute(n);
-        load_x(n % DX, kb + (n + DX) * step);   // DX divides DW
+        const auto refill = [&] { load_x(n % DX, kb + (n + DX) * step); };   // DX divides DW
+        compute(n, refill);
+        reads_done();
+        if (!EARLY) refill();
         load_w(n, kb + (n + DW) * step);
       }
     }
@@ -126,13 +148,17 @@ struct W4Rows {
       if (kb >= s.KB) break;
       if (kb + (DW - 1) * step < s.KB) w4_wait<FLY>();
       else w4_wait<0>();
-      compute(n % DW);
+      const auto refill = [&] {
+        if (kb + DX * step < s.KB) load_x(n % DX, kb + DX * step);
+      };
+      compute(n % DW, refill);
       // finished here: the compiler would carry unscaled sums into the branches that follow, and spill them
 #pragma unroll
       for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
         for (int j = 0; j < MT; ++j) asm volatile("" : "+v"(acc[rb][j]));
-      if (kb + DX * step < s.KB) load_x(n % DX, kb + DX * step);
+      reads_done();
+      if (!EARLY) refill();
       if (n < DW - 1 && kb + DW * step < s.KB) load_w(n, kb + DW * step);
     }
     w4_wait<0>();
