@@ -122,7 +122,6 @@ inline void clear_hip_error() { (void)hipGetLastError(); }
 
 inline sg_status launch_status() { return hipGetLastError() == hipSuccess ? SG_OK : SG_ERR_HIP; }
 
-// Workgroup count for grid-stride loops: enough to fill 256 CUs several times.
 // Compute units of the current device (queried once per device).
 inline int cu_count() {
   static std::atomic<int> cache[64];
@@ -136,6 +135,11 @@ inline int cu_count() {
   return n;
 }
 
+// Threads of a launch are counted in 32 bits along x: of a larger grid only the
+// remainder runs, without an error.
+inline bool launch_fits(int64_t groups, int threads) { return groups < (1LL << 32) / threads; }
+
+// Workgroup count for grid-stride loops: enough to fill 256 CUs several times.
 inline unsigned grid_for(int64_t items, int per_group, unsigned cap = 4096) {
   const int64_t g = cdiv(items, per_group);
   return (unsigned)(g < 1 ? 1 : (g > cap ? cap : g));

@@ -24,28 +24,29 @@ struct W4PackArgs {
   uint8_t* out;
 };
 
-// One wave per chunk.
+// One wave per chunk, grid-striding: a launch has threads for 2^26 of them.
 __global__ void __launch_bounds__(256) k_w4_pack(W4PackArgs a) {
   const int l = threadIdx.x & 63, g = l >> 4, r = l & 15;
-  const int64_t c = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (c >= a.chunks) return;
-  const int64_t one = a.RB * a.KB, e = c / one, rest = c - e * one;
-  const int64_t R = rest / a.KB;
-  const int kb = (int)(rest - R * a.KB);
-  const int64_t n = R * 16 + r;
-  uint8_t* const out = a.out + e * a.per + rest * a.chunk;
-  uint32_t d[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t k = (int64_t)kb * 128 + 32 * q + 8 * g;
-    d[q] = n < a.N && k < a.K ? *reinterpret_cast<const uint32_t*>(a.wq + e * a.w_bs + n * a.ldw + k / 2) : 0u;
-  }
-  *reinterpret_cast<uint4*>(out + 16 * l) = make_uint4(d[0], d[1], d[2], d[3]);
   const int ng = 128 / a.gc;
-  for (int i = l; i < 16 * ng; i += 64) {   // [group][row]
-    const int64_t nr = R * 16 + (i & 15), k = (int64_t)kb * 128 + (int64_t)(i >> 4) * a.gc;
-    reinterpret_cast<float*>(out + W4_CODES)[i] =
-        nr < a.N && k < a.K ? a.s[e * a.s_bs + nr * a.s_sn + k / a.gc * a.s_sk] : 0.0f;
+  const int64_t one = a.RB * a.KB;
+  for (int64_t c = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); c < a.chunks; c += (int64_t)gridDim.x * 4) {
+    const int64_t e = c / one, rest = c - e * one;
+    const int64_t R = rest / a.KB;
+    const int kb = (int)(rest - R * a.KB);
+    const int64_t n = R * 16 + r;
+    uint8_t* const out = a.out + e * a.per + rest * a.chunk;
+    uint32_t d[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t k = (int64_t)kb * 128 + 32 * q + 8 * g;
+      d[q] = n < a.N && k < a.K ? *reinterpret_cast<const uint32_t*>(a.wq + e * a.w_bs + n * a.ldw + k / 2) : 0u;
+    }
+    *reinterpret_cast<uint4*>(out + 16 * l) = make_uint4(d[0], d[1], d[2], d[3]);
+    for (int i = l; i < 16 * ng; i += 64) {   // [group][row]
+      const int64_t nr = R * 16 + (i & 15), k = (int64_t)kb * 128 + (int64_t)(i >> 4) * a.gc;
+      reinterpret_cast<float*>(out + W4_CODES)[i] =
+          nr < a.N && k < a.K ? a.s[e * a.s_bs + nr * a.s_sn + k / a.gc * a.s_sk] : 0.0f;
+    }
   }
 }
 
@@ -241,12 +242,12 @@ extern "C" sg_status sg_w4_pack(int64_t L, const uint8_t* wq, int64_t ldw, int64
   W4PackArgs a;
   a.KB = (int)cdiv(K, 128);
   a.RB = cdiv(N, 16);
-  if (L > (1LL << 33) / (a.RB * a.KB)) return SG_ERR_SHAPE;   // workgroups: a quarter of the chunks
+  if (L > (1LL << 40) / (a.RB * a.KB)) return SG_ERR_SHAPE;   // 64-bit sizes
   if (!aligned(wq, 4) || ldw % 4 || w_bs % 4 || !aligned(s, 4) || !aligned(packed, 16)) return SG_ERR_ALIGN;
   a.wq = wq; a.ldw = ldw; a.w_bs = w_bs; a.s = s; a.s_sn = s_sn; a.s_sk = s_sk; a.s_bs = s_bs;
   a.N = N; a.K = K; a.gc = gc; a.chunk = w4_chunk(gc); a.per = per; a.chunks = L * a.RB * a.KB; a.out = packed;
   clear_hip_error();
-  k_w4_pack<<<(unsigned)cdiv(a.chunks, 4), 256, 0, stream>>>(a);
+  k_w4_pack<<<grid_for(a.chunks, 4, 1 << 20), 256, 0, stream>>>(a);
   return launch_status();
 }
 
@@ -257,9 +258,10 @@ extern "C" sg_status sg_w4a16_gemm_groupwise_packed(int64_t M, int64_t N, int64_
   if (gc != 32 && gc != 64 && gc != 128) return SG_ERR_UNSUPPORTED;
   if (y_dt != SG_F32 && y_dt != SG_BF16) return SG_ERR_UNSUPPORTED;
   if (M <= 0 || sg_w4_packed_bytes(N, K, gc) < 0 || ldx < K || ldy < N) return SG_ERR_SHAPE;
-  // 32-bit buffer offsets: 256 X rows, and a tile's 8 row blocks of chunks; a 32-bit tile count
+  // 32-bit buffer offsets: 256 X rows, and a tile's 8 row blocks of chunks; a launch's threads
   if (ldx >= (1LL << 22) || cdiv(K, 128) * 8 * w4_chunk(gc) >= (1LL << 31)) return SG_ERR_SHAPE;
-  if (M >= (1LL << 31) || cdiv(M, 128) * cdiv(N, 256) > 0x7fffffffLL) return SG_ERR_SHAPE;
+  if (M >= (1LL << 31) || !launch_fits(cdiv(N, 16), 512) || !launch_fits(cdiv(M, 128) * cdiv(N, 256), 512))
+    return SG_ERR_SHAPE;
   if (!aligned(x, 16) || (ldx * 2) % 16 || !aligned(wpacked, 16) || !aligned(bias, 4) || !aligned(y, dtype_size(y_dt)))
     return SG_ERR_ALIGN;
   W4Args a;

@@ -558,7 +558,9 @@ static void launch_moe(const MoeArgs& a, bool bf16, hipStream_t st) {
 static bool moe_shape_ok(int64_t T, int k, int64_t E, int64_t D, int64_t F) {
   if (T < 1 || k < 1 || E < 1 || E > MOE_EMAX || D < 32 || F < 32 || D % 32 || F % 32) return false;
   if (D >= (1LL << 22) || F >= (1LL << 22) || T > (1LL << 30) / k) return false;
-  return (moe_tiles(T * k, E) + 1) * cdiv(D > F ? D : F, 64) < (1LL << 31);
+  // the tiles' launches (the half tiles are of a few hundred workgroups)
+  const int64_t nf = cdiv(F, 128), nd = cdiv(D, 256);
+  return launch_fits(moe_tiles(T * k, E) * (nf > nd ? nf : nd), 512);
 }
 
 }  // namespace sg

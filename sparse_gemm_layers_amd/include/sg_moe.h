@@ -94,8 +94,9 @@ sg_status sg_w4_pack(int64_t L, const uint8_t* wq, int64_t ldw, int64_t w_bs, co
  *   y[m, n] = bias[n] + sum_c s[n, c] sum_{k in group c} x[m, k] code[n, k]
  * in fp32 (the codes are exact in bf16, scales stay fp32), rounded once to y_dt.
  *   x : bf16 [M, K], leading dim ldx;  bias: fp32 [N] or NULL;  y: SG_F32 or SG_BF16
- * Requires ldx >= K, ldx < 2^22, ldy >= N, M < 2^31, ceil(K/128) * 8 chunks under
- * 2^31 bytes; x 16-byte aligned, ldx a multiple of 8, y aligned to its element.
+ * Requires ldx >= K, ldx < 2^22, ldy >= N, M < 2^31, N <= 2^27 - 16, ceil(M/128) *
+ * ceil(N/256) < 2^23 (a launch's workgroups), ceil(K/128) * 8 chunks under 2^31
+ * bytes; x 16-byte aligned, ldx a multiple of 8, y aligned to its element.
  */
 sg_status sg_w4a16_gemm_groupwise_packed(int64_t M, int64_t N, int64_t K, const uint16_t* x, int64_t ldx,
                                          const uint8_t* wpacked, int gc, const float* bias, void* y, sg_dtype y_dt,
@@ -116,9 +117,9 @@ sg_status sg_w4a16_gemm_groupwise_packed(int64_t M, int64_t N, int64_t K, const 
  *   workspace: at least sg_w4a16_moe_mlp_workspace(T, k, E, D, F) bytes, 256-byte
  *              aligned, in use until the work on `stream` is done
  * Requires E <= 1024, D and F multiples of gc and under 2^22, T * k <= 2^30, T *
- * ldx <= 2^30 (-1 from the size query, SG_ERR_SHAPE from the call), ldx >= D and a
- * multiple of 8, ldy >= D and a multiple of 4; x, packed weights 16-byte aligned, y
- * aligned to 4 elements.
+ * ldx <= 2^30, (ceil(T k/128) + min(T k, E)) * max(ceil(F/128), ceil(D/256)) < 2^23 (-1
+ * from the size query, SG_ERR_SHAPE from the call), ldx >= D and a multiple of 8, ldy
+ * >= D and a multiple of 4; x, packed weights 16-byte aligned, y aligned to 4 elements.
  */
 int64_t sg_w4a16_moe_mlp_workspace(int64_t T, int k, int64_t E, int64_t D, int64_t F);
 
