@@ -9,7 +9,7 @@ _build/san/libsg_hostsan.so, whose HOST code (argument checks, launch set-up)
 is instrumented with AddressSanitizer and UndefinedBehaviorSanitizer; device
 code is built as usual and not instrumented.  Load it with the sanitizer
 runtime preloaded (HOST_SANITIZER_RUNTIME) and SG_LIBRARY pointing at it; the
-CPU-only ABI tests run that way (tests/test_abi_sanitized.py).
+CPU-only ABI tests run that way (tests/test_abi_sanitized.py, test_moe_abi_sanitized.py).
 """
 import concurrent.futures
 import glob
@@ -32,6 +32,8 @@ CFLAGS = [
     # matrix-core results in VGPRs: the promotion FMAs read them directly
     # instead of copying them out of AGPRs
     "-mllvm", "-amdgpu-mfma-vgpr-form",
+    # sg_moe.h is beside the package: include/ holds sg.h and sg_probe.h, whose functions
+    # are bound one to one in _binding.py (tests/test_abi.py)
     "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "include"), "-I", CSRC,
     "-Wall", "-Wno-unused-function",
 ]
