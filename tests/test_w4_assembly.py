@@ -1,8 +1,12 @@
-"""Few-rows kernels of the 4-bit weights: a wave's part of LDS is refilled by loads
-that write LDS themselves, and such a write is not ordered against the wave's own
-LDS reads.  So no read may be outstanding where a refill is issued.  Checked on the
-assembly of the kernels as built: along every path, the most LDS operations that may
-be in flight (lgkmcnt) is zero at each load into LDS.  Needs hipcc and no GPU."""
+"""What the assembly of the 4-bit kernels as built has to show.  Needs hipcc and no GPU.
+
+Few-rows kernels: a wave's part of LDS is refilled by loads that write LDS
+themselves, and such a write is not ordered against the wave's own LDS reads.  So
+no read may be outstanding where a refill is issued: along every path, the most LDS
+operations that may be in flight (lgkmcnt) is zero at each load into LDS.
+
+All of them: no registers are spilled to memory; the waits count loads, and spills
+count among those."""
 import os
 import re
 import subprocess
@@ -82,21 +86,33 @@ def test_the_check_itself():
     assert [h for _, _, h in outstanding(one)] == [1]
 
 
+@pytest.fixture(scope="module")
+def functions(tmp_path_factory):
+    """source -> {mangled name: assembly of that kernel, with its statistics}, compiled when asked for."""
+    done = {}
+
+    def of(source):
+        if not os.path.exists(B.HIPCC):
+            pytest.skip("hipcc not available")
+        if source not in done:
+            asm = tmp_path_factory.mktemp("asm") / "device.s"
+            r = subprocess.run([B.HIPCC, *B.CFLAGS, *B.SRC_FLAGS.get(source, []), "--cuda-device-only", "-S",
+                                os.path.join(B.CSRC, source), "-o", str(asm)], capture_output=True, text=True)
+            assert r.returncode == 0, r.stderr
+            parts = re.split(r"^(?=_Z\w+:)", asm.read_text(), flags=re.M)[1:]
+            done[source] = {p.split(":", 1)[0]: p for p in parts}
+        return done[source]
+
+    return of
+
+
 @pytest.mark.timeout(300)
 @pytest.mark.parametrize("source", sorted(KERNELS))
-def test_no_read_in_flight_at_a_refill(source, tmp_path):
-    if not os.path.exists(B.HIPCC):
-        pytest.skip("hipcc not available")
-    asm = tmp_path / "device.s"
-    r = subprocess.run([B.HIPCC, *B.CFLAGS, *B.SRC_FLAGS.get(source, []), "--cuda-device-only", "-S",
-                        os.path.join(B.CSRC, source), "-o", str(asm)], capture_output=True, text=True)
-    assert r.returncode == 0, r.stderr
-    functions = re.split(r"^(?=_Z\w+:)", asm.read_text(), flags=re.M)
+def test_no_read_in_flight_at_a_refill(source, functions):
     seen, bad = set(), []
-    for f in functions:
-        name = f.split(":", 1)[0]
+    for name, f in functions(source).items():
         which = [k for k in KERNELS[source] if k in name]
-        if not which or not f.startswith("_Z"):
+        if not which:
             continue
         refills = outstanding(f.split(".Lfunc_end", 1)[0].splitlines()[1:])
         assert refills, f"{name}: no load into LDS found"
@@ -105,4 +121,16 @@ def test_no_read_in_flight_at_a_refill(source, tmp_path):
         if worst:
             bad.append(f"{name}: {sum(h > 0 for _, _, h in refills)} of {len(refills)} refills, up to {worst} reads in flight")
     assert seen == set(KERNELS[source])
+    assert not bad, "\n".join(bad)
+
+
+@pytest.mark.timeout(300)
+@pytest.mark.parametrize("source", ["gemm_w4a16.hip", "moe_mlp.hip", "moe_route.hip"])
+def test_no_spills(source, functions):
+    bad = []
+    for name, f in functions(source).items():
+        scratch = re.search(r"; ScratchSize: (\d+)", f)
+        assert scratch, name
+        if int(scratch.group(1)):
+            bad.append(f"{name}: {scratch.group(1)} bytes a lane")
     assert not bad, "\n".join(bad)
