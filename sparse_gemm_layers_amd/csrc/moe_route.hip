@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(64 * RT_WAVES) k_moe_route_rows(RouteArgs a, i
   if (hi < lo) hi = lo = 0.0f;   // nothing usable
   // Finite masks (-1e4, -1e9) would leave the others too few units: keys below hi - 64
   // are all 1 then, equal to each other.  Decisions among those are made in fp64 as
-  // between any keys this near; the sum of a group's two largest is unknown with one.
+  // between any keys this near; a group's value by its two largest is unknown with one.
   const bool floor = hi - lo > 1024.0f;
   if (floor) lo = hi - 64.0f;
   const float R = 1.0f + (hi - lo);
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(64 * RT_WAVES) k_moe_route_rows(RouteArgs a, i
       }
       const bool stays = grp < a.n_group && perhaps < a.topk_group;
       unsure = unsure || (grp < a.n_group && V != none && !stays && surely < a.topk_group);
-      unsure = unsure || (floor && a.top2 && b1 == 1);
+      unsure = unsure || (floor && a.top2 && (b1 ? b1 : b0) == 1);
       const uint32_t kept = (uint32_t)(__ballot(stays) >> (16 * tok));
 #pragma unroll
       for (int v = 0; v < VPL; ++v)

@@ -55,5 +55,19 @@ def test_whole_groups_and_steps_of_masks(gs, score):
     compare(l, 8, score=score, bias=b, n_group=12, topk_group=5, group_score=gs)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_group_of_one_masked_expert(score):
+    """Its value is the one key, -1e4; groups of two keys each 60 below the best sum up to about -120."""
+    E = 48
+    b = torch.full((E,), -60.0)
+    b[:12] = -float("inf")
+    b[3] = -1e4
+    b[12:24] = -float("inf")
+    b[14] = b[20] = 0.0                  # two of the four that are chosen
+    say(f"one masked expert {score}")
+    for tg in (1, 2, 3, 4):
+        compare(logits(2, E, F32, False), 4, score=score, bias=b, n_group=4, topk_group=tg, group_score="top2")
+
+
 def test_tokens():
     assert T >= 8192      # from where many tokens have their own kernel
