@@ -113,8 +113,9 @@ def moe_route(logits, k: int, score: str = "softmax", bias=None, n_group: int = 
     bias; with n_group > 1 only the topk_group groups of E / n_group experts with
     the largest value (the group's largest key, "max", or the sum of its two
     largest score + bias, "top2") stay.  Weights are the scores of the chosen,
-    divided by their sum if `renormalize`, times `scale`.  Ties go to the lowest
-    index; -inf or NaN takes an expert out."""
+    divided by their sum if `renormalize`, times `scale`; softmax weights are within
+    32 steps of 2^-24, and may differ by that between calls of few and of many
+    tokens.  Ties go to the lowest index; -inf or NaN takes an expert out."""
     T, E, ld = _matrix(logits, "logits", _FB)
     dev = logits.device
     if k < 1:
@@ -249,7 +250,8 @@ def w4a16_moe_mlp(x, ids, weights, gate, up, down, f: int, gc: int = 128, out_dt
 
     x bfloat16 [T, D]; ids int32 and weights float32 [T, k] as moe_route gives
     them (an id outside [0, E) contributes nothing); gate, up uint8 [E, bytes] from
-    w4_pack of E weights [f, D], down of E weights [D, f].  workspace: uint8, at least
+    w4_pack of E weights [f, D], down of E weights [D, f].  fp32 sums; silu(..) * (..)
+    is rounded to bf16 once, also for out_dtype float32.  workspace: uint8, at least
     w4a16_moe_mlp_workspace(T, k, E, D, f) bytes (allocated if not given; keep it
     to one stream)."""
     T, D, ldx = _matrix(x, "x", _BF)

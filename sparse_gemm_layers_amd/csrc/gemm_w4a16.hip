@@ -172,11 +172,16 @@ static void launch_w4_rows(const W4Args& a, bool b16, hipStream_t st) {
 
 // Time of the busiest compute unit per K block of 128, in units of 0.02 us at K =
 // 4096: rb blocks of W rows and 4 xi X rows each (w4_rows.h), or tiles (w4_tile.h).
-// 4096 x 4096, us: 64 rows: xi 8, rb 2 (308) 7.3; 12, 2 (372) 8.3; 16, 2 (436) 9.9;
-// 16, 4 (616) 13.6.  16, 4 / tiles: 256 rows 15.8 / 30.6, 512 30.1 / 32.7, 600 40.4 /
-// 32.7, 1024 53.7 / 38.4.  xi 6 and 10, for 8 and 12: 17 rows 5.6 / 6.0, 33 rows 6.9 /
-// 7.3.  Left out, since they give 2 % at most: 10, 4 (40 x 14336 x 4096 14.0 for 12, 4's
-// 14.1) and 14, 4 (56 x 14336 x 4096 16.2 for 16, 4's 16.5).
+// 4096 x 4096, us: 64 rows: xi 8, rb 2 (308) 7.0; 12, 2 (372) 7.9; 16, 2 (436) 9.1;
+// 16, 4 (616) 13.2.  16, 4 / tiles: 256 rows 14.2 / 29.3, 512 26.7 / 30.2, 600 37.7 /
+// 30.7, 1024 50.9 / 37.4.  xi 6 and 10, for 8 and 12: 17 rows 5.3 / 5.4, 33 rows 6.8 /
+// 6.9.  Left out, since they gave 2 % at most when they were tried: 10, 4 (40 x 14336 x
+// 4096 14.0 for 12, 4's 14.1) and 14, 4 (56 x 14336 x 4096 16.2 for 16, 4's 16.5).
+// The costs are those of groups of 128 (32: 64 rows 7.6, 256 rows 16.8 / 37.6), and K
+// is left out of them: neither way splits it over workgroups, so sizes that fill few
+// compute units are far from what memory allows (682 x 1621 x 12224 63 us, 262 x 5090 x
+// 5632 30), and so is a size just past a full round of tiles (2048 x 4096 x 4096 61 us,
+// 2049 rows 111).
 static int64_t w4_rows_cost(int64_t M, int64_t N, int rb, int xi) {
   return cdiv(cdiv(N, 16 * rb) * cdiv(M, 4 * xi), 256) * (16 * xi + 90 * rb);
 }

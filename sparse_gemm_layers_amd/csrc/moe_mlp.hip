@@ -42,7 +42,7 @@ struct MoeArgs {
 
 // One workgroup counts, sums and places the pairs.  Up to 16 pairs a thread stay
 // in registers between counting and placing, each with its rank in its expert.
-// (16384 pairs: 18 us when the ids were read and counted twice, 12 so.)
+// (16384 pairs: 18 us when the ids were read and counted twice, 12 so; beyond, they are.)
 constexpr int PLAN_KEEP = 16;
 __global__ void __launch_bounds__(1024) k_moe_plan(MoeArgs a) {
   __shared__ int cnt[MOE_EMAX], wsum[16], wtiles[16];
@@ -518,15 +518,18 @@ static void launch_moe_stream(const MoeArgs& a, hipStream_t st) {
 }
 
 // Which way: us of 64 experts (4096, 1024), k 8 / 60 experts (2048, 1408), k 4 / 9
-// experts (2016, 1216), k 2.
-//   pairs         few        stream       tiles
-//   16          27 / 28     43 / 29      53 / 40
-//   32          68 / 51     54 / 43      65 / 57 / 31
-//   128        163 / 114    85 / 73      99 / 73 / 33
-//   256        205 / 155   137 / 93     109 / 90
-//   512        301 / 218   253 / 160    120 / 95
-// Streaming passes over an expert's weights once for every R of its pairs, so it
-// is taken while an expert has R / 4 on average (some have several times that).
+// experts (2016, 1216), k 2, the same four routings in turn for each way.
+//   pairs       few            stream            tiles
+//   16      34 / 38 / 24     49 /  34 / 35     48 / 38 / 32
+//   32                       58 /  53 / 37     72 / 54 / 32
+//   64                       80 /  61 / 53     83 / 67 / 32
+//   128                     104 /  68 / 77    101 / 70 / 36
+//   256                     131 /  94         109 / 77
+//   512                     216 / 135         123 / 92
+// Streaming passes over an expert's weights once for every R of its pairs (R is 8, 16
+// and 16 here), so it is taken while an expert has R / 4 on average (some have several
+// times that).  With as few experts as 9 its workgroups are too few: the tiles are
+// faster by a seventh from 17 to 36 pairs, where the rule still streams.
 template <int GC>
 static void launch_moe(const MoeArgs& a, bool bf16, hipStream_t st) {
   if (a.P <= MOE_FEW) {

@@ -39,8 +39,10 @@ struct RouteGradArgs {
 
 constexpr int RT_WAVES = 4, RT_EMAX = 1024, RT_KMAX = 64, RT_GMAX = 64;
 
-// Tokens from which k_moe_route_rows is the faster (256 experts, 4 of 8 groups, bias: 4096 tokens 13.5 us for
-// 11.0, 16384 tokens 22.8 for 32.6; 128 experts without: 6.9 for 5.3, 9.9 for 13.1).
+// Tokens from which k_moe_route_rows is taken; us, it / k_moe_route, at 4096, 6144, 8192, 16384 tokens: 256 experts,
+// 4 of 8 groups, bias 10.4 / 10.9, 13.6 / 15.3, 14.0 / 19.0, 23.2 / 34.2; 256 without either 7.7 / 6.4, 9.1 / 8.1,
+// 9.5 / 10.4, 15.0 / 17.4; 128 without 5.5 / 5.4, 6.4 / 6.6, 6.4 / 8.0, 8.8 / 13.3; 60 without 4.2 / 4.1, 4.8 / 5.0,
+// 4.7 / 5.9, 6.3 / 9.1.
 constexpr int64_t RT_ROWS_MIN = 8192;
 
 #if SG_DEVICE_PASS
@@ -382,9 +384,10 @@ __device__ __forceinline__ void sort_down(uint32_t (&v)[N]) {   // Batcher's odd
 // Many tokens: 16 lanes a token, four tokens a wave, VPL experts a lane (lane j:
 // 64 i + 4 j .. + 3).  What bounds routing is the instructions per token, and the
 // fp64 scores of every expert were most of them (16384 tokens of 256 experts in 8
-// groups: 32.6 us, 22.8 this way); here scores are fp32 and keys are whole numbers of 24 bits with
-// the expert in the low byte (255 - e, so that the lowest wins among equals), one
-// 32-bit maximum finding both.  A key is off by `err` units at most; candidates
+// groups: 34.2 us, 23.2 this way, of which the experts' preparation, done once a wave
+// and at this size for four tokens only, is 44% of the instructions); here scores are
+// fp32 and keys are whole numbers of 24 bits with the expert in the low byte (255 - e,
+// so that the lowest wins among equals), one 32-bit maximum finding both.  A key is off by `err` units at most; candidates
 // within 2 err of each other are put in order by their fp64 keys, and where a
 // group, or an expert that is no candidate, lies as near to those that stay, the
 // token is done again by route_token, which decides in fp64.  bf16 logits without a bias are exact keys.

@@ -6,7 +6,7 @@
 // the matrix core wants it (lane 16 g + r: row r) takes 64, since neighbouring
 // lanes then read different rows; so X rows come whole, four per load, into
 // this wave's part of LDS and are read from there: 37 x 4096 x 14336 took 46 us
-// with operands loaded directly and takes 18.  Scales take one load of 4 bytes a
+// with operands loaded directly and takes 16.  Scales take one load of 4 bytes a
 // lane per row block (7 cycles), codes one of 16 (a packed chunk's 1 KB).
 // Codes, which come from HBM, are loaded DW K blocks ahead, X rows, which L2
 // holds, DX.

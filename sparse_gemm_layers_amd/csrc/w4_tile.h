@@ -2,11 +2,11 @@
 // 128 X rows per workgroup of 8 waves.  A wave owns IW row blocks of 16 W rows
 // ("slots" IW w ..) and every X row, so each code is widened by one wave alone:
 // widening (13 instructions per 8 codes) is much of what a wave issues, one
-// instruction in 8 cycles with two waves a SIMD.  2048 x 4096 x 4096 with groups
-// of 128: 70 us (61 with a quantised normal weight), 980 TFLOP/s at the 1.8 GHz
-// that the card holds under this load; 600 rows of it, at 2.4 GHz, 43 us.  A 2 x 4
-// grid of waves, which widens each code four times, took 83 us.  The price is that
-// every wave reads every X row from LDS.
+// instruction in 8 cycles with two waves a SIMD.  2048 x 4096 x 4096: 59 to 61 us
+// with groups of 128, 1.13 PFLOP/s at the 1.8 to 2.1 GHz that the card holds under this
+// load, 66 with groups of 64, 76 of 32 (four sums to scale a block for one).  A 2 x 4
+// grid of waves, which widens each code four times, took 83 us where this took 70.
+// The price is that every wave reads every X row from LDS.
 // IW = 1 is for products that leave compute units empty otherwise.
 //
 // A K block is one stage of a ring of three.  A wave's own codes and scales are
@@ -234,7 +234,7 @@ struct W4Tile {
         for (int e = 0; e < 4; ++e)
           acc[i][2 * JP - 2 + c][e] = fmaf(odd ? p[0][i][c][e] : p[1][i][c][e], sw[P::NG - 1][i][e],
                                            acc[i][2 * JP - 2 + c][e]);
-    w4_wait<0>();   // loads past the end write their zeros before LDS is given up
+    w4_wait<0>();   // loads past the end, of the last block again, have landed before LDS is given up
   }
 #endif  // SG_DEVICE_PASS
 };

@@ -37,7 +37,10 @@ enum { SG_GROUP_MAX = 0, SG_GROUP_TOP2 = 1 };
  *   ids      = the k largest keys that stay, largest first; w = s of those,
  *              divided by their sum if renormalize, times scale.
  * Equal keys (and groups) go to the lower index.  Keys are compared as if
- * computed in 64 bits, so the choice does not depend on fp32 rounding.
+ * computed in 64 bits, so the choice does not depend on fp32 rounding.  Weights are
+ * rounded once from 64 bits, except that a softmax's sum may be taken in fp32, which
+ * depends on the call's sizes and options: those weights are within 32 steps of 2^-24
+ * of their value, and may differ by that between calls of few tokens and of many.
  * A logit of -inf or NaN, or a bias of -inf or NaN, takes its expert out
  * (+inf counts as the largest finite value); where fewer than k experts are
  * left the remaining slots hold id -1 and weight 0.
@@ -106,7 +109,8 @@ sg_status sg_w4a16_gemm_groupwise_packed(int64_t M, int64_t N, int64_t K, const 
  * sg_w4a16_moe_mlp -- the routed gated MLP on packed 4-bit experts:
  *   y[t] = sum_j weights[t, j] * Wd_e (silu(Wg_e x_t) * (Wu_e x_t)),  e = ids[t, j]
  * with silu(g) = g / (1 + exp(-g)).  Products and sums are fp32; the inner
- * activations are rounded to bf16 once, as the down product's operand.  The k
+ * activations are rounded to bf16 once, as the down product's operand: SG_F32 results
+ * carry that rounding (half a step, 2^-8 of an activation at most).  The k
  * contributions are added in an order that the sizes and ids fix: the same call
  * gives the same bits.  A token may name an expert more than once.
  * Slots whose id is outside [0, E) contribute nothing and their weight is not
