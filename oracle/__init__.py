@@ -20,7 +20,8 @@ of the source pages it follows; the pages are
 ``pack.py`` additionally defines the library's own gfx950 packed weight layouts (the
 FP8 / int8 one and the int4 blocked one: byte permutations of the compressed
 values and metadata).  ``moe.py`` holds the mixture-of-experts operators
-(routing, its gradient, 4-bit linear layers, the routed MLP).
+(routing, its gradient, 4-bit linear layers, the routed MLP), ``adapt.py`` the gated
+projections and the low-rank adapters with their gradients.
 
 Parity status: every public function here is pinned by a ``-m "not gpu"`` test
 against something other than itself (an independent codec, closed forms,
@@ -49,7 +50,7 @@ from .gemm import (
     mixed_gemm_add,
     within_tolerance,
 )
-from . import moe
+from . import adapt, moe
 
 __all__ = [
     "E4M3_MAX", "e4m3_decode", "e4m3_encode", "bf16_decode",
@@ -60,5 +61,5 @@ __all__ = [
     "expand_scales", "fp8_gemm_groupwise", "fp8_sparse24_gemm_groupwise",
     "int8_gemm_groupwise", "int8_sparse24_gemm_groupwise", "fp8_gemm_rowwise",
     "fp8_sparse24_gemm_rowwise", "int8_sparse24_gemm_rowwise", "add_bias", "w8a16_sparse24_gemm_groupwise",
-    "w4a16_sparse24_gemm_groupwise", "mixed_gemm_add", "within_tolerance", "moe",
+    "w4a16_sparse24_gemm_groupwise", "mixed_gemm_add", "within_tolerance", "moe", "adapt",
 ]

@@ -3,7 +3,8 @@ linear-layer GEMMs for AMD Instinct MI355X (gfx950).
 
 A thin Python binding over the C ABI of ``libsg.so`` (declared in
 ``include/sg.h``; the measurement helpers in ``include/sg_probe.h``; the
-mixture-of-experts operators in ``sparse_gemm_layers_amd/include/sg_moe.h``).  The functions only marshal arguments: PyTorch supplies
+mixture-of-experts operators in ``sparse_gemm_layers_amd/include/sg_moe.h``, the
+gated projections in ``sg_gated.h`` beside it, the low-rank adapters in ``sg_lora.h``).  The functions only marshal arguments: PyTorch supplies
 device memory and the current HIP stream; every step runs in the library's
 HIP kernels.  There is no CPU fallback: if ``libsg.so`` is missing or the
 tensors are not on a GPU, the call raises.
@@ -49,6 +50,17 @@ from ._moe import (
     w4a16_moe_mlp_workspace,
     w4a16_moe_mlp,
 )
+from ._gated import (
+    gated_gemm,
+    gated_gemm_backward_workspace,
+    gated_gemm_backward,
+)
+from ._lora import (
+    lora_gemm_workspace,
+    lora_gemm,
+    lora_gemm_backward_workspace,
+    lora_gemm_backward,
+)
 
 __all__ = [
     "SgError", "lib", "fp8_quant_groupwise", "int4_quant_groupwise",
@@ -63,4 +75,6 @@ __all__ = [
     "w4a16_sparse24_gemm_groupwise_packed", "sparse24_w4_packed_bytes", "sparse24_pack_w4",
     "moe_route", "moe_route_backward", "w4_packed_bytes", "w4_pack", "w4a16_gemm_groupwise_packed",
     "w4a16_moe_mlp_workspace", "w4a16_moe_mlp",
+    "gated_gemm", "gated_gemm_backward_workspace", "gated_gemm_backward",
+    "lora_gemm_workspace", "lora_gemm", "lora_gemm_backward_workspace", "lora_gemm_backward",
 ]

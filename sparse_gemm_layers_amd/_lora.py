@@ -1,0 +1,150 @@
+"""ctypes binding of the low-rank adapters' entry points of libsg.so
+(``sparse_gemm_layers_amd/include/sg_lora.h``).  Argument marshalling only."""
+
+import functools
+
+import torch
+
+from ._binding import SgError, _FB, _check, _i64, _int, _ptr, lib
+from ._moe import _BF, _CODE, _current_stream, _matrix, _refuse, _result, _rows
+
+_SIGS = {
+    "sg_lora_gemm_workspace": ([_i64, _i64, _i64, _int, _i64], _i64),
+    "sg_lora_gemm": ([_i64, _i64, _i64, _int, _i64, _ptr, _i64, _ptr, _ptr, _ptr, _ptr, _ptr, _int, _i64, _ptr, _int,
+                      _i64, _ptr, _i64, _ptr], _int),
+    "sg_lora_gemm_backward_workspace": ([_i64, _i64, _i64, _int, _i64], _i64),
+    "sg_lora_gemm_backward": ([_i64, _i64, _i64, _int, _i64, _ptr, _i64, _ptr, _i64, _ptr, _ptr, _ptr, _ptr, _ptr, _i64,
+                               _ptr, _i64, _ptr, _ptr, _int, _ptr, _i64, _ptr], _int),
+}
+
+_typed = None
+
+
+def _lib():
+    """libsg.so with this module's entry points typed too."""
+    global _typed
+    h = lib()
+    if _typed is not h:
+        for name, (args, res) in _SIGS.items():
+            fn = getattr(h, name)
+            fn.argtypes = args
+            fn.restype = res
+        _typed = h
+    return h
+
+
+def lora_gemm_workspace(t: int, k: int, n: int, r: int, l: int) -> int:
+    """Bytes of workspace of a lora_gemm call (-1: sizes out of range)."""
+    return int(_lib().sg_lora_gemm_workspace(t, k, n, r, l))
+
+
+def lora_gemm_backward_workspace(t: int, k: int, n: int, r: int, l: int) -> int:
+    """Bytes of workspace of a lora_gemm_backward call (-1: sizes out of range)."""
+    return int(_lib().sg_lora_gemm_backward_workspace(t, k, n, r, l))
+
+
+@functools.lru_cache(maxsize=1024)
+def _need(back, t, k, n, r, l):
+    need = (lora_gemm_backward_workspace if back else lora_gemm_workspace)(t, k, n, r, l)
+    if need < 0:
+        raise SgError(f"low-rank adapters: sizes out of range (T = {t}, K = {k}, N = {n}, r = {r}, L = {l}; K, N and r "
+                      "multiples of 8, r at most 256)")
+    return need
+
+
+def _adapters(x, ids, a, b, scale):
+    """(T, K, N, r, L, row stride of x, addresses of ids, a, b and scale)."""
+    T, K, ldx = _matrix(x, "x", _BF)
+    dev = x.device
+    if not isinstance(a, torch.Tensor) or a.dim() != 3 or not isinstance(b, torch.Tensor) or b.dim() != 3:
+        raise SgError("a and b must be GPU tensors [L, r, K] and [L, N, r]")
+    L, r = a.shape[0], a.shape[1]
+    N = b.shape[1]
+    if min(L, r, N) < 1:
+        raise SgError(f"L, r and N must be at least 1, got {L}, {r} and {N}")
+    pa = _rows(a, "a", torch.bfloat16, (L, r, K), dev)
+    pb = _rows(b, "b", torch.bfloat16, (L, N, r), dev)
+    pi = None if ids is None else _rows(ids, "ids", torch.int32, (T,), dev)
+    ps = None if scale is None else _rows(scale, "scale", torch.float32, (L,), dev)
+    return T, K, N, r, L, ldx, pi, pa, pb, ps
+
+
+def _space(workspace, need, x):
+    if workspace is None:
+        return x.new_empty(need, dtype=torch.uint8)
+    if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or not workspace.is_contiguous() \
+            or workspace.numel() < need or workspace.device != x.device:
+        raise SgError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {x.device}")
+    return workspace
+
+
+def lora_gemm(x, ids, a, b, scale=None, base=None, out_dtype=torch.bfloat16, y=None, workspace=None):
+    """y[t] = base[t] + scale[e] (x[t] . a[e]^T) . b[e]^T, e = ids[t].
+
+    x bfloat16 [T, K]; ids int32 [T] (outside [0, L): no adapter, y is base or 0; None:
+    adapter 0 for every token); a bfloat16 [L, r, K], b bfloat16 [L, N, r] (a smaller
+    rank is padded with zeros); scale float32 [L] or None for 1; base [T, N] float32 or
+    bfloat16: the shared projection's output, from any of the library's products, or
+    None for 0.  y may be base: then the adapters are added in place.  fp32 sums, the
+    inner product included; y is rounded once.  workspace: uint8, at least
+    lora_gemm_workspace(T, K, N, r, L) bytes (allocated if not given; keep it to one
+    stream)."""
+    T, K, N, r, L, ldx, pi, pa, pb, ps = _adapters(x, ids, a, b, scale)
+    dev = x.device
+    ldb = 0 if base is None else _result(base, "base", _FB, (T, N), dev)
+    if y is None:
+        if out_dtype not in _CODE:
+            raise SgError(f"out_dtype {out_dtype} not supported (float32 or bfloat16)")
+        y = x.new_empty((T, N), dtype=out_dtype)
+        ldy = N
+    else:
+        ldy = _result(y, "y", _FB, (T, N), dev)
+    workspace = _space(workspace, _need(False, T, K, N, r, L), x)
+    st = _lib().sg_lora_gemm(T, K, N, r, L, x.data_ptr(), ldx, pi, pa, pb, ps,
+                             None if base is None else base.data_ptr(), 0 if base is None else _CODE[base.dtype], ldb,
+                             y.data_ptr(), _CODE[y.dtype], ldy, workspace.data_ptr(), workspace.numel(),
+                             _current_stream(x))
+    if st:
+        _check(st, "sg_lora_gemm")
+    return y
+
+
+def lora_gemm_backward(dy, x, ids, a, b, scale=None, base=None, need_dx: bool = True, need_dab: bool = True,
+                       grad_dtype=torch.bfloat16, dx=None, da=None, db=None, workspace=None):
+    """Gradients of lora_gemm for dy bfloat16 [T, N], the gradient of y (and so of its
+    base): (dx bfloat16 [T, K], da [L, r, K], db [L, N, r]); None where not needed.
+
+    dx[t] = base[t] + scale[e] (dy[t] . b[e]) . a[e], with base bfloat16 [T, K] what else
+    contributes to the gradient of x (None: 0; it may be dx itself); da and db, of
+    grad_dtype, are sums over the adapter's own tokens, zeros where it has none.
+    workspace: uint8, at least lora_gemm_backward_workspace(T, K, N, r, L) bytes
+    (allocated if not given; keep it to one stream)."""
+    T, K, N, r, L, ldx, pi, pa, pb, ps = _adapters(x, ids, a, b, scale)
+    dev = x.device
+    ld_dy = _result(dy, "dy", _BF, (T, N), dev)
+    ldb = 0 if base is None else _result(base, "base", _BF, (T, K), dev)
+    if grad_dtype not in _CODE:
+        raise SgError(f"grad_dtype {grad_dtype} not supported (float32 or bfloat16)")
+    if need_dx and dx is None:
+        dx = x.new_empty((T, K))
+    if need_dab and da is None and db is None:
+        da, db = x.new_empty((L, r, K), dtype=grad_dtype), x.new_empty((L, N, r), dtype=grad_dtype)
+    pdx, ldd = (None, 0) if dx is None else (dx.data_ptr(), _result(dx, "dx", _BF, (T, K), dev))
+    pda = pdb = None
+    if da is not None or db is not None:
+        if da is None or db is None:
+            raise SgError("da and db go together")
+        if da.dtype not in _CODE:
+            _refuse(da, "da", _FB, (L, r, K), dev)
+        pda = _rows(da, "da", da.dtype, (L, r, K), dev)
+        pdb = _rows(db, "db", da.dtype, (L, N, r), dev)
+    if pdx is None and pda is None:
+        return None, None, None
+    workspace = _space(workspace, _need(True, T, K, N, r, L), x)
+    st = _lib().sg_lora_gemm_backward(T, K, N, r, L, dy.data_ptr(), ld_dy, x.data_ptr(), ldx, pi, pa, pb, ps,
+                                      None if base is None else base.data_ptr(), ldb, pdx, ldd, pda, pdb,
+                                      0 if pda is None else _CODE[da.dtype], workspace.data_ptr(), workspace.numel(),
+                                      _current_stream(x))
+    if st:
+        _check(st, "sg_lora_gemm_backward")
+    return dx, da, db

@@ -1,0 +1,692 @@
+// Low-rank adapters of many requests, with e = ids[t]:
+//   y[t] = base[t] + s_e (x[t] . A_e^T) . B_e^T
+// and the backward pass
+//   u = x . A_e^T, v = s_e dy . B_e, dx = base + v . A_e,
+//   dA_e = sum_t v[t]^T x[t], dB_e = s_e sum_t dy[t]^T u[t].
+// Three kinds of kernel, all bound by memory: "down" products [T, C] -> [T, r], the
+// long side summed in parts over workgroups; "up" products [T, r] -> [T, C], which add up
+// those parts as they read them; and the sums over an adapter's tokens [T, r]^T [T, C].
+//
+// The [T, r] values between two products stay fp32 in memory and enter the matrix
+// core as a sum of NP bf16 parts (each the rounding of what the ones before leave):
+// with so few ranks that costs matrix instructions only, which nothing waits for.
+//
+// Down and up go by blocks of 16 TM consecutive tokens and, within one, by the adapters
+// that appear in it: one for a prompt, up to 16 in a decoding batch, where the
+// third dimension of the grid shares them out.  A token's row of a product is kept from the
+// pass of its own adapter alone.  The sums gather the rows of one adapter.
+#include "bf16_tile.h"
+#include "sg_lora.h"
+
+namespace sg {
+
+#if SG_DEVICE_PASS
+// The adapter of token t, -1: none.
+__device__ __forceinline__ int lora_id(const int32_t* ids, int64_t t, int64_t T, int L) {
+  if (t >= T) return -1;
+  const int e = ids ? ids[t] : 0;
+  return e >= 0 && e < L ? e : -1;
+}
+
+// The next adapter among those of this block's tokens (id[j]: token 16 j + l % 16) that are not
+// done, which it marks; -1: no more.
+template <int TM>
+__device__ __forceinline__ int lora_next(const int (&id)[TM], bool (&done)[TM]) {
+  int e = -1;
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const uint64_t m = __ballot(id[j] >= 0 && !done[j]);
+    if (e < 0 && m) e = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(m));
+  }
+#pragma unroll
+  for (int j = 0; j < TM; ++j) done[j] = done[j] || id[j] == e;
+  return e;
+}
+
+// NP bf16 parts of eight fp32 values.  What an infinite part or a NaN leaves is nothing,
+// not the NaN that subtracting it gives.
+template <int NP>
+__device__ __forceinline__ void lora_parts(float (&v)[8], v4i (&p)[NP]) {
+#pragma unroll
+  for (int n = 0; n < NP; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = f32x2_to_bf16x2(v[2 * i], v[2 * i + 1]);
+      p[n][i] = (int)w;
+      if (n + 1 == NP) continue;
+      v[2 * i] = (w & 0x7f80u) == 0x7f80u ? 0.0f : v[2 * i] - __uint_as_float(w << 16);
+      v[2 * i + 1] = (w & 0x7f800000u) == 0x7f800000u ? 0.0f : v[2 * i + 1] - __uint_as_float(w & 0xffff0000u);
+    }
+}
+#endif
+
+// ------------------------------------------------------------------ down
+
+struct LoraDown {
+  int64_t T;
+  int C, r, L, splits;     // the sum runs over C, in `splits` parts
+  const uint16_t *z, *w;   // z [T, C]; w [L][r][C], or KS: [L][C][r]
+  int64_t ldz;
+  const int32_t* ids;
+  float* part;             // [splits][T][r]
+};
+
+template <bool KS, int TM, int RM>
+__global__ void __launch_bounds__(256) k_lora_down(LoraDown a) {
+#if SG_DEVICE_PASS
+  constexpr int PITCH = 32 * RM + 16;   // KS: one row's ranks in LDS
+  constexpr int RED = 4 * RM * TM * 1024, STG = KS ? 4 * 64 * PITCH : 0;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[RED > STG ? RED : STG];
+  const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int64_t t0 = (int64_t)blockIdx.x * (16 * TM);
+  const int split = blockIdx.y % a.splits, rho0 = (int)(blockIdx.y / a.splits) * 16 * RM;
+  const int rows = (int)min((int64_t)(16 * TM), a.T - t0);
+  const int units = (a.C + 63) >> 6;   // of 64 columns
+  const int u0 = (int)((int64_t)units * split / a.splits), u1 = (int)((int64_t)units * (split + 1) / a.splits);
+  int id[TM];
+  bool done[TM];
+  uint32_t zo[TM];
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    id[j] = lora_id(a.ids, t0 + 16 * j + lr, a.T, a.L);
+    done[j] = false;
+    zo[j] = 16 * j + lr < rows ? (uint32_t)(((16 * j + lr) * a.ldz + 8 * g) * 2) : W4_OUT;
+  }
+  const __amdgpu_buffer_rsrc_t rz = w4_rsrc(a.z + t0 * a.ldz, (uint32_t)(((rows - 1) * a.ldz + a.C) * 2));
+  for (int d = 0;; ++d) {
+    const int e = lora_next<TM>(id, done);
+    if (e < 0) break;
+    if (d % gridDim.z != blockIdx.z) continue;
+    const uint16_t* const w = a.w + (int64_t)e * a.r * a.C;
+    const __amdgpu_buffer_rsrc_t rw = KS ? w4_rsrc(w, 0) : w4_rsrc(w + (int64_t)rho0 * a.C, (uint32_t)(min(a.r - rho0, 16 * RM) * a.C * 2));
+    v4f acc[RM][TM];
+#pragma unroll
+    for (int m = 0; m < RM; ++m)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[m][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+    for (int u = u0 + wave; u < u1; u += 4) {
+      v4i zf[TM][2], wf[RM][2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const bool in = 64 * u + 32 * q + 8 * g < a.C;
+#pragma unroll
+        for (int j = 0; j < TM; ++j) zf[j][q] = w4_ld16(rz, in ? zo[j] + 64 * q : W4_OUT, u * 128);
+        if (!KS) {
+#pragma unroll
+          for (int m = 0; m < RM; ++m) {
+            const int rho = 16 * m + lr;
+            wf[m][q] = w4_ld16(rw, in && rho0 + rho < a.r ? (uint32_t)((rho * a.C + 8 * g + 32 * q) * 2) : W4_OUT, u * 128);
+          }
+        }
+      }
+      if (KS) {   // 64 rows of 16 RM ranks through this wave's part of LDS
+        uint8_t* const st = lds + wave * 64 * PITCH;
+        uint4 v[2 * RM];
+#pragma unroll
+        for (int i = 0; i < 2 * RM; ++i) {
+          const int k = (i * 64 + l) / (2 * RM), c = (i * 64 + l) % (2 * RM);
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (64 * u + k < a.C && rho0 + 8 * c < a.r)
+            v[i] = *reinterpret_cast<const uint4*>(w + (int64_t)(64 * u + k) * a.r + rho0 + 8 * c);
+        }
+#pragma unroll
+        for (int i = 0; i < 2 * RM; ++i) {
+          const int k = (i * 64 + l) / (2 * RM), c = (i * 64 + l) % (2 * RM);
+          *reinterpret_cast<uint4*>(st + k * PITCH + 16 * c) = v[i];
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int m = 0; m < RM; ++m) {
+            const uint8_t* const at = st + (32 * q + 8 * g + (lr >> 2)) * PITCH + 32 * m + 8 * (lr & 3);
+            const uint2 x = lds_tr4(at), y = lds_tr4(at + 4 * PITCH);
+            wf[m][q] = (v4i){(int)x.x, (int)x.y, (int)y.x, (int)y.y};
+          }
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int m = 0; m < RM; ++m)
+#pragma unroll
+          for (int j = 0; j < TM; ++j) acc[m][j] = w4_mfma(wf[m][q], zf[j][q], acc[m][j]);
+    }
+    float(*const red)[RM * TM][64][4] = reinterpret_cast<float(*)[RM * TM][64][4]>(lds);
+    if (KS) __syncthreads();
+#pragma unroll
+    for (int m = 0; m < RM; ++m)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) *reinterpret_cast<v4f*>(&red[wave][m * TM + j][l][0]) = acc[m][j];
+    __syncthreads();
+    for (int q = wave; q < RM * TM; q += 4) {
+      const int m = q / TM, j = q % TM;
+      v4f s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s += *reinterpret_cast<const v4f*>(&red[k][q][l][0]);
+      int mine = -1;   // the id of token 16 j + lr
+#pragma unroll
+      for (int i = 0; i < TM; ++i) mine = i == j ? id[i] : mine;
+      const int rho = rho0 + 16 * m + 4 * g;
+      if (mine == e && rho < a.r)
+        *reinterpret_cast<float4*>(a.part + ((int64_t)split * a.T + t0 + 16 * j + lr) * a.r + rho) =
+            make_float4(s[0], s[1], s[2], s[3]);
+    }
+    __syncthreads();
+  }
+#endif  // SG_DEVICE_PASS
+}
+
+// ------------------------------------------------------------------ up
+
+struct LoraUp {
+  int64_t T;
+  int C, r, L, splits;     // parts of p
+  const float* part;       // [splits][T][r]
+  const float* scale;
+  const int32_t* ids;
+  const uint16_t* w;       // [L][C][r], or KS: [L][r][C]
+  const void* base;
+  int64_t ld_base;
+  int base_f32;
+  void* y;
+  int64_t ldy;
+  int y_f32;
+};
+
+#if SG_DEVICE_PASS
+// Ranks rho .. rho + 7 of token t's [T, r] value: its parts added in order, scaled.
+__device__ __forceinline__ void lora_value(const float* part, int splits, int64_t T, int r, int64_t t, int rho,
+                                           float scale, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  for (int s = 0; s < splits; ++s) {
+    float x[8];
+    load4(part + ((int64_t)s * T + t) * r + rho, x);
+    load4(part + ((int64_t)s * T + t) * r + rho + 4, x + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += x[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= scale;
+}
+
+// Columns n .. n + 7 of row t: base plus v.
+__device__ __forceinline__ void lora_store(const LoraUp& a, int64_t t, int n, float (&v)[8]) {
+  if (a.base) {
+    float x[8];
+    if (a.base_f32) {
+      const float* const p = reinterpret_cast<const float*>(a.base) + t * a.ld_base + n;
+      load4(p, x);
+      load4(p + 4, x + 4);
+    } else {
+      const uint16_t* const p = reinterpret_cast<const uint16_t*>(a.base) + t * a.ld_base + n;
+      load4(p, x);
+      load4(p + 4, x + 4);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += x[i];
+  }
+  if (a.y_f32) {
+    float* const o = reinterpret_cast<float*>(a.y) + t * a.ldy + n;
+    *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.y) + t * a.ldy + n) =
+        make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
+                   f32x2_to_bf16x2(v[6], v[7]));
+  }
+}
+#endif
+
+// A workgroup's four waves take 64 columns each.
+template <bool KS, int TM, int NP>
+__global__ void __launch_bounds__(256) k_lora_up(LoraUp a) {
+#if SG_DEVICE_PASS
+  constexpr int PITCH = 128 + 16;   // KS: 64 columns of one rank in LDS
+  __shared__ __attribute__((aligned(16))) uint8_t lds[KS ? 4 * 32 * PITCH : 16];
+  const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int64_t t0 = (int64_t)blockIdx.x * (16 * TM);
+  const int n0 = (blockIdx.y * 4 + wave) * 64;
+  if (n0 >= a.C) return;   // no barrier follows
+  int id[TM];
+  bool done[TM];
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    id[j] = lora_id(a.ids, t0 + 16 * j + lr, a.T, a.L);
+    done[j] = false;
+  }
+  for (int d = 0;; ++d) {
+    const int e = lora_next<TM>(id, done);
+    if (e < 0) break;
+    if (d % gridDim.z != blockIdx.z) continue;
+    const float scale = a.scale ? a.scale[e] : 1.0f;
+    const uint16_t* const w = a.w + (int64_t)e * a.r * a.C;
+    v4f acc[4][TM];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
+    for (int rho0 = 0; rho0 < a.r; rho0 += 32) {
+      const int rho = rho0 + 8 * g;
+      v4i wf[4];
+      if (!KS) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = n0 + tile_n(i, lr);
+          wf[i] = (v4i){0, 0, 0, 0};
+          if (n < a.C && rho < a.r) wf[i] = *reinterpret_cast<const v4i*>(w + (int64_t)n * a.r + rho);
+        }
+      } else {
+        uint8_t* const st = lds + wave * 32 * PITCH;
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = 8 * i + (l >> 3), c = 8 * (l & 7);
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (rho0 + k < a.r && n0 + c < a.C)
+            v[i] = *reinterpret_cast<const uint4*>(w + (int64_t)(rho0 + k) * a.C + n0 + c);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(st + (8 * i + (l >> 3)) * PITCH + 16 * (l & 7)) = v[i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t* const at = st + (8 * g + (lr >> 2)) * PITCH + 64 * (i >> 1) + 16 * (lr & 3) + 8 * (i & 1);
+          const uint2 x = lds_tr4(at), y = lds_tr4(at + 4 * PITCH);
+          wf[i] = (v4i){(int)x.x, (int)x.y, (int)y.x, (int)y.y};
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (id[j] == e && rho < a.r) lora_value(a.part, a.splits, a.T, a.r, t0 + 16 * j + lr, rho, scale, v);
+        v4i p[NP];
+        lora_parts<NP>(v, p);
+#pragma unroll
+        for (int n = NP - 1; n >= 0; --n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i][j] = w4_mfma(wf[i], p[n], acc[i][j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int n = n0 + 32 * q + 8 * g;
+        if (id[j] == e && n < a.C) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = acc[2 * q + (i >> 2)][j][i & 3];
+          lora_store(a, t0 + 16 * j + lr, n, v);
+        }
+      }
+  }
+  if (blockIdx.z == 0 && a.y != a.base) {   // tokens without an adapter
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int n = n0 + 32 * q + 8 * g;
+        if (id[j] < 0 && t0 + 16 * j + lr < a.T && n < a.C) {
+          float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          lora_store(a, t0 + 16 * j + lr, n, v);
+        }
+      }
+  }
+#endif  // SG_DEVICE_PASS
+}
+
+// ------------------------------------------------------------------ sums over tokens
+
+[[maybe_unused]] constexpr int LORA_LIST = 1024;   // tokens looked through at a time
+
+struct LoraSum {
+  int64_t T;
+  int C, r, L, splits;     // parts of p
+  const uint16_t* z;       // [T, C]
+  int64_t ldz;
+  const float* part;       // [splits][T][r]
+  const float* scale;
+  const int32_t* ids;
+  int tsplits;             // parts of the tokens
+  float* sums;             // [tsplits][L][r][C], or RC: [tsplits][L][C][r]; tsplits 1: NULL
+  void* out;               // the same without the parts
+  int out_f32;
+};
+
+// Adapter blockIdx.y's sum over its tokens in range blockIdx.z, columns of 64 a wave.  CR:
+// results are [C][r] (dB), else [r][C] (dA).
+template <bool CR, int RM, int NP>
+__global__ void __launch_bounds__(256) k_lora_sum(LoraSum a) {
+#if SG_DEVICE_PASS
+  constexpr int PP = 32 * RM + 16, ZP = 128 + 16;   // pitches of one token's ranks and columns
+  __shared__ __attribute__((aligned(16))) uint8_t pl[NP * 32 * PP], zl[4 * 32 * ZP];
+  __shared__ int list[LORA_LIST], count[4];
+  const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int chunks = (a.r + 16 * RM - 1) / (16 * RM);
+  const int e = blockIdx.y / chunks, rho0 = (int)(blockIdx.y % chunks) * 16 * RM;
+  const int n0 = (blockIdx.x * 4 + wave) * 64;
+  const int64_t b0 = a.T * blockIdx.z / a.tsplits, b1 = a.T * (blockIdx.z + 1) / a.tsplits;
+  const float scale = a.scale ? a.scale[e] : 1.0f;
+  v4f acc[4][RM];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int m = 0; m < RM; ++m) acc[i][m] = (v4f){0.f, 0.f, 0.f, 0.f};
+  for (int64_t c0 = b0; c0 < b1; c0 += LORA_LIST) {
+    // this adapter's tokens among LORA_LIST, in order: each wave looks through a quarter
+    __syncthreads();
+    int n = 0;
+    uint64_t hit[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      hit[i] = __ballot(lora_id(a.ids, c0 + wave * 256 + 64 * i + l, b1, a.L) == e);
+      n += __builtin_popcountll(hit[i]);
+    }
+    if (l == 0) count[wave] = n;
+    __syncthreads();
+    int at = 0, total = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (k < wave) at += count[k];
+      total += count[k];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if ((hit[i] >> l) & 1) list[at + __builtin_popcountll(hit[i] & ((1ull << l) - 1))] = wave * 256 + 64 * i + l;
+      at += __builtin_popcountll(hit[i]);
+    }
+    __syncthreads();
+    uint4 zv[4];
+    const auto load_z = [&](int k0) {   // 32 tokens x 64 columns of this wave
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = k0 + 8 * i + (l >> 3), c = n0 + 8 * (l & 7);
+        zv[i] = make_uint4(0, 0, 0, 0);
+        if (k < total && c < a.C) zv[i] = *reinterpret_cast<const uint4*>(a.z + (c0 + list[k]) * a.ldz + c);
+      }
+    };
+    load_z(0);
+    for (int k0 = 0; k0 < total; k0 += 32) {
+      for (int o = t; o < 64 * RM; o += 256) {   // eight ranks of one token each
+        const int k = o / (2 * RM), rho = rho0 + 8 * (o % (2 * RM));
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (k0 + k < total && rho < a.r) lora_value(a.part, a.splits, a.T, a.r, c0 + list[k0 + k], rho, scale, v);
+        v4i p[NP];
+        lora_parts<NP>(v, p);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) *reinterpret_cast<v4i*>(pl + (q * 32 + k) * PP + 16 * (o % (2 * RM))) = p[q];
+      }
+      uint8_t* const st = zl + wave * 32 * ZP;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(st + (8 * i + (l >> 3)) * ZP + 16 * (l & 7)) = zv[i];
+      __syncthreads();
+      load_z(k0 + 32);
+      v4i zf[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // CR: columns as they are; else dealt so that a lane's results are 8 neighbours
+        const int col = CR ? 32 * i + 8 * (lr & 3) : 64 * (i >> 1) + 16 * (lr & 3) + 8 * (i & 1);
+        const uint8_t* const from = st + (8 * g + (lr >> 2)) * ZP + col;
+        const uint2 x = lds_tr4(from), y = lds_tr4(from + 4 * ZP);
+        zf[i] = (v4i){(int)x.x, (int)x.y, (int)y.x, (int)y.y};
+      }
+#pragma unroll
+      for (int m = 0; m < RM; ++m)
+#pragma unroll
+        for (int q = NP - 1; q >= 0; --q) {
+          const uint8_t* const from = pl + (q * 32 + 8 * g + (lr >> 2)) * PP + 32 * m + 8 * (lr & 3);
+          const uint2 x = lds_tr4(from), y = lds_tr4(from + 4 * PP);
+          const v4i pf = {(int)x.x, (int)x.y, (int)y.x, (int)y.y};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i][m] = CR ? w4_mfma(pf, zf[i], acc[i][m]) : w4_mfma(zf[i], pf, acc[i][m]);
+        }
+      __syncthreads();
+    }
+  }
+  const int64_t one = (int64_t)a.r * a.C;
+  const bool f32 = a.tsplits > 1 || a.out_f32;
+  float* const of = (a.tsplits > 1 ? a.sums + (int64_t)blockIdx.z * a.L * one : reinterpret_cast<float*>(a.out)) + e * one;
+  uint16_t* const ob = reinterpret_cast<uint16_t*>(a.out) + e * one;
+  if (CR) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < RM; ++m) {
+        const int n = n0 + 16 * i + lr, rho = rho0 + 16 * m + 4 * g;
+        if (n >= a.C || rho >= a.r) continue;
+        const v4f v = acc[i][m];
+        if (f32) *reinterpret_cast<float4*>(of + (int64_t)n * a.r + rho) = make_float4(v[0], v[1], v[2], v[3]);
+        else *reinterpret_cast<uint2*>(ob + (int64_t)n * a.r + rho) =
+            make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
+      }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int m = 0; m < RM; ++m) {
+        const int n = n0 + 32 * q + 8 * g, rho = rho0 + 16 * m + lr;
+        if (n >= a.C || rho >= a.r) continue;
+        const v4f v = acc[2 * q][m], w = acc[2 * q + 1][m];
+        if (f32) {
+          float* const o = of + (int64_t)rho * a.C + n;
+          *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(o + 4) = make_float4(w[0], w[1], w[2], w[3]);
+        } else {
+          *reinterpret_cast<uint4*>(ob + (int64_t)rho * a.C + n) =
+              make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(w[0], w[1]),
+                         f32x2_to_bf16x2(w[2], w[3]));
+        }
+      }
+  }
+#endif  // SG_DEVICE_PASS
+}
+
+// The parts of both gradients, added in order.  n: values of one part, of dA then dB.
+struct LoraJoin {
+  const float* sums[2];
+  void* out[2];
+  int64_t n[2];
+  int parts, out_f32;
+};
+__global__ void __launch_bounds__(256) k_lora_join(LoraJoin a) {
+#if SG_DEVICE_PASS
+  const int64_t step = (int64_t)gridDim.x * 1024;
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < a.n[0] + a.n[1]; i += step) {
+    const int h = i >= a.n[0];
+    const int64_t at = h ? i - a.n[0] : i, n = h ? a.n[1] : a.n[0];
+    const float* const p = (h ? a.sums[1] : a.sums[0]) + at;
+    void* const o = h ? a.out[1] : a.out[0];
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < a.parts; ++s) {
+      float x[4];
+      load4(p + s * n, x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] += x[k];
+    }
+    if (a.out_f32) *reinterpret_cast<float4*>(reinterpret_cast<float*>(o) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    else *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(o) + at) =
+        make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
+  }
+#endif
+}
+
+// ------------------------------------------------------------------ sizes
+
+// Workgroups' share of the adapters in a block of 16 tokens: all of one block where
+// there are few blocks.
+static int lora_slots(int64_t T, int64_t L, int64_t groups) {
+  const int64_t most = L < 16 ? L : 16, n = T < most ? T : most;
+  int64_t s = 1024 / (groups < 1 ? 1 : groups);
+  return (int)(s < 1 ? 1 : s > n ? n : s);
+}
+
+// Parts of a down product's sum: enough workgroups, and at least 256 columns each.
+static int lora_splits(int64_t T, int64_t C) {
+  int64_t s = 512 / cdiv(T, 16);
+  const int64_t most = cdiv(C, 256);
+  s = s > most ? most : s;
+  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+}
+
+static int lora_tsplits(int64_t T, int64_t C, int64_t L) {
+  int64_t s = 256 / (cdiv(C, 256) * L);
+  const int64_t most = cdiv(T, 128);
+  s = s > most ? most : s;
+  return (int)(s < 1 ? 1 : s > 32 ? 32 : s);
+}
+
+struct LoraSpace {
+  int64_t u, v, sa, sb, bytes;
+  int su, sv, ts;
+  LoraSpace(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L, bool back) {
+    int64_t at = 0;
+    const auto part = [&](int64_t n) { const int64_t was = at; at += cdiv(n, 256) * 256; return was; };
+    su = lora_splits(T, K);
+    sv = lora_splits(T, N);
+    ts = lora_tsplits(T, K > N ? K : N, L);
+    u = part(4 * su * T * r);
+    v = sa = sb = 0;
+    if (back) {
+      v = part(4 * sv * T * r);
+      if (ts > 1) {
+        sa = part(4 * ts * L * r * K);
+        sb = part(4 * ts * L * r * N);
+      }
+    }
+    bytes = at;
+  }
+};
+
+template <bool KS, int TM>
+static void launch_down_rm(const LoraDown& a, hipStream_t st) {
+  const unsigned gx = (unsigned)cdiv(a.T, 16 * TM);
+  const auto grid = [&](int rm) {
+    const int64_t gy = a.splits * cdiv(a.r, 16 * rm);
+    return dim3(gx, (unsigned)gy, (unsigned)lora_slots(a.T, a.L, gx * gy));
+  };
+  if (a.r <= 16) k_lora_down<KS, TM, 1><<<grid(1), 256, 0, st>>>(a);
+  else if (a.r <= 32) k_lora_down<KS, TM, 2><<<grid(2), 256, 0, st>>>(a);
+  else k_lora_down<KS, TM, 4><<<grid(4), 256, 0, st>>>(a);
+}
+template <bool KS>
+static void launch_down(const LoraDown& a, hipStream_t st) { launch_down_rm<KS, 1>(a, st); }
+
+template <bool KS>
+static void launch_up(const LoraUp& a, hipStream_t st) {
+  const unsigned gx = (unsigned)cdiv(a.T, 16), gy = (unsigned)cdiv(a.C, 256);
+  const dim3 grid(gx, gy, (unsigned)lora_slots(a.T, a.L, (int64_t)gx * gy));
+  if (a.y_f32) k_lora_up<KS, 1, 3><<<grid, 256, 0, st>>>(a);
+  else k_lora_up<KS, 1, 2><<<grid, 256, 0, st>>>(a);
+}
+
+template <bool CR, int NP>
+static void launch_sum_np(const LoraSum& a, hipStream_t st) {
+  const auto grid = [&](int rm) {
+    return dim3((unsigned)cdiv(a.C, 256), (unsigned)(a.L * cdiv(a.r, 16 * rm)), (unsigned)a.tsplits);
+  };
+  if (a.r <= 16) k_lora_sum<CR, 1, NP><<<grid(1), 256, 0, st>>>(a);
+  else if (a.r <= 32) k_lora_sum<CR, 2, NP><<<grid(2), 256, 0, st>>>(a);
+  else k_lora_sum<CR, 4, NP><<<grid(4), 256, 0, st>>>(a);
+}
+template <bool CR>
+static void launch_sum(const LoraSum& a, hipStream_t st) {
+  if (a.out_f32) launch_sum_np<CR, 3>(a, st);
+  else launch_sum_np<CR, 2>(a, st);
+}
+
+static bool lora_shape_ok(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
+  if (T < 1 || K < 8 || N < 8 || r < 8 || L < 1 || K % 8 || N % 8 || r % 8) return false;
+  // grids: ranks in chunks of 64 by adapters
+  return T < (1LL << 22) && K < (1LL << 22) && N < (1LL << 22) && r <= 256 && L * cdiv(r, 64) <= 65535;
+}
+static bool lora_ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld < (1LL << 22); }
+
+}  // namespace sg
+
+using namespace sg;
+
+extern "C" int64_t sg_lora_gemm_workspace(int64_t T, int64_t K, int64_t N, int r, int64_t L) {
+  if (!lora_shape_ok(T, K, N, r, L)) return -1;
+  return LoraSpace(T, K, N, r, L, false).bytes;
+}
+
+extern "C" int64_t sg_lora_gemm_backward_workspace(int64_t T, int64_t K, int64_t N, int r, int64_t L) {
+  if (!lora_shape_ok(T, K, N, r, L)) return -1;
+  return LoraSpace(T, K, N, r, L, true).bytes;
+}
+
+extern "C" sg_status sg_lora_gemm(int64_t T, int64_t K, int64_t N, int r, int64_t L, const uint16_t* x, int64_t ldx,
+                                  const int32_t* ids, const uint16_t* a, const uint16_t* b, const float* scale,
+                                  const void* base, sg_dtype base_dt, int64_t ld_base, void* y, sg_dtype y_dt,
+                                  int64_t ldy, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
+  if (!x || !a || !b || !y || !workspace) return SG_ERR_NULL;
+  if ((y_dt != SG_F32 && y_dt != SG_BF16) || (base && base_dt != SG_F32 && base_dt != SG_BF16))
+    return SG_ERR_UNSUPPORTED;
+  if (!lora_shape_ok(T, K, N, r, L) || !lora_ld_ok(ldx, K) || !lora_ld_ok(ldy, N) ||
+      (base && !lora_ld_ok(ld_base, N)) || (base == y && (base_dt != y_dt || ld_base != ldy)))
+    return SG_ERR_SHAPE;
+  const LoraSpace ws(T, K, N, r, L, false);
+  if (workspace_bytes < ws.bytes) return SG_ERR_SHAPE;
+  if (ldx % 8 || ldy % 8 || (base && ld_base % 8) || !aligned(x, 16) || !aligned(ids, 4) || !aligned(a, 16) ||
+      !aligned(b, 16) || !aligned(scale, 4) || !aligned(base, 16) || !aligned(y, 16) || !aligned(workspace, 256))
+    return SG_ERR_ALIGN;
+  clear_hip_error();
+  float* const part = reinterpret_cast<float*>(workspace);
+  launch_down<false>(LoraDown{T, (int)K, r, (int)L, ws.su, x, a, ldx, ids, part}, stream);
+  LoraUp p = {};
+  p.T = T; p.C = (int)N; p.r = r; p.L = (int)L; p.splits = ws.su; p.part = part; p.scale = scale; p.ids = ids; p.w = b;
+  p.base = base; p.ld_base = ld_base; p.base_f32 = base_dt == SG_F32; p.y = y; p.ldy = ldy; p.y_f32 = y_dt == SG_F32;
+  launch_up<false>(p, stream);
+  return launch_status();
+}
+
+extern "C" sg_status sg_lora_gemm_backward(int64_t T, int64_t K, int64_t N, int r, int64_t L, const uint16_t* dy,
+                                           int64_t ld_dy, const uint16_t* x, int64_t ldx, const int32_t* ids,
+                                           const uint16_t* a, const uint16_t* b, const float* scale,
+                                           const uint16_t* base, int64_t ld_base, uint16_t* dx, int64_t ld_dx,
+                                           void* da, void* db, sg_dtype grad_dt, void* workspace,
+                                           int64_t workspace_bytes, hipStream_t stream) {
+  if (!dy || !x || !a || !b || !workspace || (!dx && !da) || !da != !db) return SG_ERR_NULL;
+  if (da && grad_dt != SG_F32 && grad_dt != SG_BF16) return SG_ERR_UNSUPPORTED;
+  if (!lora_shape_ok(T, K, N, r, L) || !lora_ld_ok(ldx, K) || !lora_ld_ok(ld_dy, N) || (dx && !lora_ld_ok(ld_dx, K)) ||
+      (dx && base && !lora_ld_ok(ld_base, K)) || (dx && base == dx && ld_base != ld_dx))
+    return SG_ERR_SHAPE;
+  const LoraSpace ws(T, K, N, r, L, true);
+  if (workspace_bytes < ws.bytes) return SG_ERR_SHAPE;
+  if (ldx % 8 || ld_dy % 8 || (dx && ld_dx % 8) || (dx && base && ld_base % 8) || !aligned(dy, 16) || !aligned(x, 16) ||
+      !aligned(ids, 4) || !aligned(a, 16) || !aligned(b, 16) || !aligned(scale, 4) || !aligned(base, 16) ||
+      !aligned(dx, 16) || !aligned(da, 16) || !aligned(db, 16) || !aligned(workspace, 256))
+    return SG_ERR_ALIGN;
+  clear_hip_error();
+  uint8_t* const w = reinterpret_cast<uint8_t*>(workspace);
+  float *const u = reinterpret_cast<float*>(w + ws.u), *const v = reinterpret_cast<float*>(w + ws.v);
+  launch_down<true>(LoraDown{T, (int)N, r, (int)L, ws.sv, dy, b, ld_dy, ids, v}, stream);
+  if (da) launch_down<false>(LoraDown{T, (int)K, r, (int)L, ws.su, x, a, ldx, ids, u}, stream);
+  if (dx) {
+    LoraUp p = {};
+    p.T = T; p.C = (int)K; p.r = r; p.L = (int)L; p.splits = ws.sv; p.part = v; p.scale = scale; p.ids = ids; p.w = a;
+    p.base = base; p.ld_base = ld_base; p.y = dx; p.ldy = ld_dx;
+    launch_up<true>(p, stream);
+  }
+  if (da) {
+    LoraSum s = {};
+    s.T = T; s.C = (int)K; s.r = r; s.L = (int)L; s.splits = ws.sv; s.z = x; s.ldz = ldx; s.part = v; s.scale = scale;
+    s.ids = ids; s.tsplits = ws.ts; s.sums = reinterpret_cast<float*>(w + ws.sa); s.out = da;
+    s.out_f32 = grad_dt == SG_F32;
+    launch_sum<false>(s, stream);
+    s.C = (int)N; s.splits = ws.su; s.z = dy; s.ldz = ld_dy; s.part = u; s.sums = reinterpret_cast<float*>(w + ws.sb);
+    s.out = db;
+    launch_sum<true>(s, stream);
+    if (ws.ts > 1) {
+      LoraJoin j = {};
+      j.sums[0] = reinterpret_cast<float*>(w + ws.sa); j.sums[1] = reinterpret_cast<float*>(w + ws.sb);
+      j.out[0] = da; j.out[1] = db; j.n[0] = L * r * K; j.n[1] = L * r * N; j.parts = ws.ts;
+      j.out_f32 = grad_dt == SG_F32;
+      k_lora_join<<<grid_for((j.n[0] + j.n[1]) / 4, 256, 4096), 256, 0, stream>>>(j);
+    }
+  }
+  return launch_status();
+}
