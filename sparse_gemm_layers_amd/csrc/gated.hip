@@ -121,6 +121,20 @@ __device__ __forceinline__ void gated_finish(const GatedArgs& a, int64_t m, int 
 }
 #endif  // SG_DEVICE_PASS
 
+// Left rows of a tile: a wave's first NI / 2 sub-tiles are gate rows, the others up rows
+// of the same f.
+template <int NI>
+struct GatedRow {
+#if SG_DEVICE_PASS
+  static constexpr int HALF = NI / 2;
+  __device__ static __forceinline__ int row(int u, int wave, int l) {
+    const int s = (8 * u + wave) >> 1, r = 8 * (wave & 1) + (l >> 3);
+    return s / NI * (16 * HALF) + tile_n(s % HALF, r);
+  }
+  __device__ static __forceinline__ int sel(int u, int wave) { return ((8 * u + wave) >> 1) / HALF & 1; }
+#endif
+};
+
 // Many rows: tiles of BN / 2 rows of each weight x BM tokens (bf16_tile.h).
 template <typename T, bool BACK>
 __global__ void __launch_bounds__(512) k_gated_tile(GatedArgs a, int tiles_m, int tiles_n) {
@@ -132,29 +146,19 @@ __global__ void __launch_bounds__(512) k_gated_tile(GatedArgs a, int tiles_m, in
   const int f0 = tn * (T::BN / 2);
   const int64_t m0 = (int64_t)tm * T::BM;
   const int rows = (int)min((int64_t)T::BM, a.T - m0), wrows = min(T::BN / 2, a.F - f0);
-  const int KB = (a.D + 31) >> 5;
+  const int KB = (a.D + 63) >> 6;
   typename T::L lo;
   typename T::R ro;
   lo.p[0] = a.gate + f0 * a.ldg;
   lo.p[1] = a.up + f0 * a.ldu;
   lo.bytes[0] = (uint32_t)(((wrows - 1) * a.ldg + a.D) * 2);
   lo.bytes[1] = (uint32_t)(((wrows - 1) * a.ldu + a.D) * 2);
-#pragma unroll
-  for (int u = 0; u < T::LU; ++u) {
-    // a wave's first NI / 2 sub-tiles are gate rows, the others up rows of the same f
-    const int s = 8 * u + wave, wn = s / T::NI, i = s % T::NI, half = T::NI / 2;
-    const int f = wn * (16 * half) + tile_n(i % half, l >> 2);
-    lo.sel[u] = i / half;
-    lo.set(u, f < wrows, f * (lo.sel[u] ? a.ldu : a.ldg), a.D, l);
-  }
+  lo.ld[0] = a.ldg;
+  lo.ld[1] = a.ldu;
+  lo.K = ro.K = a.D;
   ro.p[0] = ro.p[1] = a.x + m0 * a.ldx;
+  ro.ld[0] = ro.ld[1] = a.ldx;
   ro.bytes[0] = ro.bytes[1] = (uint32_t)(((rows - 1) * a.ldx + a.D) * 2);
-#pragma unroll
-  for (int u = 0; u < T::RU; ++u) {
-    const int m = 16 * (8 * u + wave) + (l >> 2);
-    ro.sel[u] = 0;
-    ro.set(u, m < rows, m * a.ldx, a.D, l);
-  }
   v4f acc[T::NI][T::MJ];
   T::run(lds, lo, ro, 0, KB, KB, wave, l, acc);
   const int g = l >> 4, lr = l & 15, wn = wave / T::WM, wm = wave % T::WM, half = T::NI / 2;
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(512) k_gated_dx(GatedGradArgs a, int tiles_m, 
   const int n0 = tn * T::BN;
   const int64_t m0 = (int64_t)tm * T::BM;
   const int rows = (int)min((int64_t)T::BM, a.T - m0), cols = min(T::BN, a.D - n0);
-  const int KB = (a.F + 31) >> 5;
+  const int KB = (a.F + 63) >> 6;
   const int kb0 = (int)((int64_t)2 * KB * split / a.splits), kb1 = (int)((int64_t)2 * KB * (split + 1) / a.splits);
   typename T::L lo;
   typename T::R ro;
@@ -328,17 +332,11 @@ __global__ void __launch_bounds__(512) k_gated_dx(GatedGradArgs a, int tiles_m, 
   lo.ld[0] = a.ldg;
   lo.ld[1] = a.ldu;
   lo.width = (uint32_t)((a.D - n0) * 2);
-  lo.K = a.F;
-  lo.set(wave, l);
+  lo.K = ro.K = a.F;
   ro.p[0] = a.dg + m0 * a.ld_dgu;
   ro.p[1] = a.du + m0 * a.ld_dgu;
+  ro.ld[0] = ro.ld[1] = a.ld_dgu;
   ro.bytes[0] = ro.bytes[1] = (uint32_t)(((rows - 1) * a.ld_dgu + a.F) * 2);
-#pragma unroll
-  for (int u = 0; u < T::RU; ++u) {
-    const int m = 16 * (8 * u + wave) + (l >> 2);
-    ro.sel[u] = 0;
-    ro.set(u, m < rows, m * a.ld_dgu, a.F, l);
-  }
   v4f acc[T::NI][T::MJ];
   T::run(lds, lo, ro, kb0, kb1, KB, wave, l, acc);
   const int g = l >> 4, lr = l & 15, wn = wave / T::WM, wm = wave % T::WM;
@@ -397,19 +395,16 @@ __global__ void __launch_bounds__(512) k_gated_dw(GatedGradArgs a, int tiles_m, 
   const bool up = 2 * tm >= tiles_m;
   const int n0 = tn * T::BN, m0 = (up ? tm - tiles_m / 2 : tm) * T::BM;
   const int rows = min(T::BM, a.F - m0), cols = min(T::BN, a.D - n0);
-  const int K = (int)a.T, KB = (K + 31) >> 5;
+  const int K = (int)a.T, KB = (K + 63) >> 6;
   typename T::L lo;
   typename T::R ro;
   lo.p[0] = lo.p[1] = a.x + n0;
   lo.ld[0] = lo.ld[1] = a.ldx;
   lo.width = (uint32_t)((a.D - n0) * 2);
-  lo.K = K;
-  lo.set(wave, l);
+  lo.K = ro.K = K;
   ro.p[0] = ro.p[1] = (up ? a.du : a.dg) + m0;
   ro.ld[0] = ro.ld[1] = a.ld_dgu;
   ro.width = (uint32_t)((a.F - m0) * 2);
-  ro.K = K;
-  ro.set(wave, l);
   v4f acc[T::NI][T::MJ];
   T::run(lds, lo, ro, 0, KB, KB, wave, l, acc);
   uint16_t* const out = up ? a.dup : a.dgate;
@@ -430,8 +425,8 @@ __global__ void __launch_bounds__(512) k_gated_dw(GatedGradArgs a, int tiles_m, 
 #endif  // SG_DEVICE_PASS
 }
 
-template <bool L, bool R> using TileA = Bf16Tile<L, R, 2, 4, 8, 4>;   // 256 x 256
-template <bool L, bool R> using TileB = Bf16Tile<L, R, 2, 4, 4, 2>;   // 128 x 128
+template <bool L, bool R, typename Row = PlainRow> using TileA = Bf16Tile<L, R, 2, 4, 8, 4, Row>;   // 256 x 256
+template <bool L, bool R, typename Row = PlainRow> using TileB = Bf16Tile<L, R, 2, 4, 4, 2, Row>;   // 128 x 128
 
 template <bool BACK, int MT>
 static void launch_gated_rows(const GatedArgs& a, hipStream_t st) {
@@ -450,11 +445,11 @@ static void launch_gated(const GatedArgs& a, hipStream_t st) {
     return;
   }
   if (cdiv(a.T, 256) * cdiv(a.F, 128) >= 256) {
-    using T = TileA<false, false>;
+    using T = TileA<false, false, GatedRow<8>>;
     const int tm = (int)cdiv(a.T, 256), tn = (int)cdiv(a.F, 128);
     k_gated_tile<T, BACK><<<(unsigned)tm * tn, 512, 0, st>>>(a, tm, tn);
   } else {
-    using T = TileB<false, false>;
+    using T = TileB<false, false, GatedRow<4>>;
     const int tm = (int)cdiv(a.T, 128), tn = (int)cdiv(a.F, 64);
     k_gated_tile<T, BACK><<<(unsigned)tm * tn, 512, 0, st>>>(a, tm, tn);
   }
@@ -465,11 +460,11 @@ struct DxPlan {
   bool big;
   int splits;
   DxPlan(int64_t T, int64_t F, int64_t D) {
-    const int64_t steps = 2 * cdiv(F, 32);
+    const int64_t steps = 2 * cdiv(F, 64);
     big = cdiv(T, 256) * cdiv(D, 256) >= 64;
     const int64_t tiles = big ? cdiv(T, 256) * cdiv(D, 256) : cdiv(T, 128) * cdiv(D, 128);
     int64_t s = (big ? 256 : 512) / tiles;
-    if (s > steps / 16) s = steps / 16;
+    if (s > steps / 8) s = steps / 8;
     splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
   }
   int64_t bytes(int64_t T, int64_t D) const { return splits == 1 ? 0 : 4 * splits * T * D; }
