@@ -4,15 +4,22 @@
 // a row holds one k), so that a forward product, the gradient of its input and
 // that of its weight all read the matrices as the caller has them.
 //
-// k goes by blocks of 64, two in LDS at a time, which buffer loads fill directly;
-// a block is two steps of 32, one 16x16x32 matrix instruction per pair of sub-tiles.
-// A KC block holds 128-byte rows (16-byte piece c of row r at c ^ swz8q(r)), read 16
-// bytes a lane: with 64-byte rows every line came from L2 twice.  A KS block holds
-// 64 rows of one k each (64-byte piece c of row k at c ^ swz(k)), read with
-// ds_read_b64_tr_b16, which hands each lane four k of one column.  What a wave reads of
-// the next step replaces what the matrix core has taken of this one in registers; so
-// the block's single barrier, in its second step, both opens the next block and frees
-// this one for the loads of the one after.
+// k goes by blocks of 64 (two steps of 32: one 16x16x32 matrix instruction per pair of
+// sub-tiles), which buffer loads bring to LDS directly, three of the left operand and
+// two of the right at a time.  A KC block holds 128-byte rows (16-byte piece c of row r
+// at c ^ swz8q(r)), read 16 bytes a lane: with 64-byte rows every line came from L2
+// twice.  A KS block holds 64 rows of one k each (64-byte piece c of row k at c ^ swz(k)),
+// read with ds_read_b64_tr_b16, which hands each lane four k of one column.
+//
+// A wave first takes a step's operands from LDS and asks for what comes blocks later,
+// then multiplies.  With 8 waves those of the second half, one to a SIMD as those of the
+// first, go one phase behind: while one wave of a SIMD multiplies the other reads.
+// Both kept going at once, with operands read ahead, is no faster (2048 x 14336 x 4096
+// forward 400 us for 383), and one wave a SIMD with 128 x 128 results of its own, which
+// reads a third less from LDS, has its sums moved about by the compiler (690).
+// What is left: the card's power.  It holds 1.75 to 1.9 GHz under this load, with the
+// matrix cores busy in 70% of the cycles of a full round; without the loads it is 80% at
+// 2.05 GHz, and a product of the library's with nothing fused runs at 1.78 GHz.
 //
 // Left rows are dealt to sub-tiles so that a lane's results of two neighbouring
 // sub-tiles are 8 consecutive n: row i of sub-tile 2 p + b is
@@ -27,10 +34,12 @@
 namespace sg {
 
 // Rows in order, one matrix a segment.
+template <int NW>
 struct PlainRow {
+  static constexpr int MATS = 1;
 #if SG_DEVICE_PASS
-  __device__ static __forceinline__ int row(int u, int wave, int l) { return 8 * (8 * u + wave) + (l >> 3); }
-  __device__ static __forceinline__ int sel(int, int) { return 0; }
+  __device__ static __forceinline__ int row(int u, int wave, int l) { return 8 * (NW * u + wave) + (l >> 3); }
+  __device__ static constexpr int sel(int) { return 0; }
 #endif
 };
 
@@ -62,19 +71,19 @@ __device__ __forceinline__ v4i tile_rsrc(const void* p, uint32_t bytes) {
 // n of row r of sub-tile s, relative to the wave's first.
 __device__ __forceinline__ int tile_n(int s, int r) { return 32 * (s >> 1) + 8 * (r >> 2) + 4 * (s & 1) + (r & 3); }
 
-// One wave's loads of a KC operand: U instructions of 8 rows a block.  The sum over k
+// One wave's loads of a KC operand: U instructions of 8 rows a block, NW waves.  The sum over k
 // has one segment or two of KB blocks, each with a matrix of its own; p[seg] is the
 // first column of row 0.  Row::row(u, wave, l) is the row that lane l of instruction u
 // loads; Row::sel(u, wave) which of the two matrices it is of, where it is not the
 // segment that says so.  Rows past the last lie outside of the descriptor (it ends
 // with the last row) and read as zero.
-template <int U, typename Row>
+template <int U, int NW, typename Row>
 struct KcOp {
   const uint16_t* p[2];
   int64_t ld[2];
   uint32_t bytes[2];
   int K, wave, l;
-  v4i r[U];             // where the next block's loads are
+  v4i r[Row::MATS];     // where the next block's loads are
   uint32_t cur[U];
   int soff;
   // Block k of segment seg is next; none: nothing but zeros is.
@@ -83,20 +92,24 @@ struct KcOp {
     const int c = 8 * ((l & 7) ^ swz8q(l >> 3));   // k of this lane's piece of 16 bytes
     const bool out = k * 64 + c >= K;
 #pragma unroll
+    for (int m = 0; m < Row::MATS; ++m) {
+      const int s = m ^ seg;
+      r[m] = tile_rsrc(s ? p[1] : p[0], none ? 0u : s ? bytes[1] : bytes[0]);
+    }
+#pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int s = Row::sel(u, wave) ^ seg;
-      r[u] = tile_rsrc(s ? p[1] : p[0], none ? 0u : s ? bytes[1] : bytes[0]);
+      const int s = Row::sel(u) ^ seg;
       cur[u] = out ? W4_OUT : (uint32_t)((Row::row(u, wave, l) * (s ? ld[1] : ld[0]) + c) * 2);
     }
   }
-  template <int AT>
-  __device__ __forceinline__ void load(int u, uint32_t base) const { lds_dma16<AT>(r[u], cur[u], soff, base); }
+  template <int N, int AT>
+  __device__ __forceinline__ void load(uint32_t base) const { lds_dma16<AT>(r[Row::sel(N)], cur[N], soff, base); }
   __device__ __forceinline__ void next() { soff += 128; }
 };
 
 // One wave's loads of a KS operand of B columns.  p[seg], ld[seg]: row k = 0, the
 // tile's first column.  Rows past K are outside of the descriptor and read as zero.
-template <int U, int B>
+template <int U, int NW, int B>
 struct KsOp {
   const uint16_t* p[2];
   int64_t ld[2];
@@ -114,12 +127,12 @@ struct KsOp {
                   none ? 0u : (uint32_t)((min(K - 64 * k, 64) - 1) * d * 2) + width);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int row = RPI * (8 * u + wave) + l / (B / 8);   // 16-byte piece l % (B / 8) of this row
+      const int row = RPI * (NW * u + wave) + l / (B / 8);   // 16-byte piece l % (B / 8) of this row
       cur[u] = (uint32_t)(row * d * 2) + 16 * ((l % (B / 8)) ^ (swz(row) << 2));
     }
   }
-  template <int AT>
-  __device__ __forceinline__ void load(int u, uint32_t base) const { lds_dma16<AT>(r, cur[u], 0, base); }
+  template <int N, int AT>
+  __device__ __forceinline__ void load(uint32_t base) const { lds_dma16<AT>(r, cur[N], 0, base); }
   __device__ __forceinline__ void next() {
     const uint64_t at = (((uint64_t)(uint32_t)r[1] << 32) | (uint32_t)r[0]) + step;
     r[0] = (int)at;
@@ -132,17 +145,39 @@ struct KsOp {
 template <bool LKS_, bool RKS_, int WN_, int WM_, int NI_, int MJ_, typename LRow = void>
 struct Bf16Tile {
   static constexpr bool LKS = LKS_, RKS = RKS_;
-  static constexpr int WN = WN_, WM = WM_, NI = NI_, MJ = MJ_;
-  static_assert(WN * WM == 8 && NI % 2 == 0 && MJ % 2 == 0, "waves");
+  static constexpr int WN = WN_, WM = WM_, NI = NI_, MJ = MJ_, NW = WN * WM;
+  static constexpr bool LAG = NW == 8;
+  static_assert(NI % 2 == 0 && MJ % 2 == 0, "pairs of sub-tiles");
   static constexpr int BN = WN * NI * 16, BM = WM * MJ * 16;
-  static constexpr int L_BYTES = BN * 128, BLOCK = (BN + BM) * 128, LDS = 2 * BLOCK;
-  static constexpr int LU = BN / 64, RU = BM / 64, LOADS = LU + RU;
+  static constexpr int L_BLOCK = BN * 128, R_BLOCK = BM * 128, R_OFF = 3 * L_BLOCK, LDS = R_OFF + 2 * R_BLOCK;
+  static constexpr int LU = BN / 8 / NW, RU = BM / 8 / NW;   // loads of one wave and block
   static_assert(LDS <= 160 * 1024, "LDS");
 #if SG_DEVICE_PASS
   template <bool C, typename A, typename B> struct pick { using type = A; };
   template <typename A, typename B> struct pick<false, A, B> { using type = B; };
-  using L = typename pick<LKS, KsOp<LU, BN>, KcOp<LU, LRow>>::type;
-  using R = typename pick<RKS, KsOp<RU, BM>, KcOp<RU, PlainRow>>::type;
+  using L = typename pick<LKS, KsOp<LU, NW, BN>, KcOp<LU, NW, LRow>>::type;
+  using R = typename pick<RKS, KsOp<RU, NW, BM>, KcOp<RU, NW, PlainRow<NW>>>::type;
+
+  // The block of one operand that is loaded next, and the one at which more than its place
+  // changes: a segment's last (k may end within it), its end, the end of all (from there on zeros).
+  template <typename Op>
+  struct Feed {
+    Op& op;
+    int at, event, kb1, KB;
+    __device__ __forceinline__ void place() {
+      const bool none = at >= kb1;
+      const int seg = at >= KB, k = seg ? at - KB : at;
+      op.place(k, seg, KB, none);
+      asm volatile("");   // a branch, not a row of selects in every block
+      const int e = seg * KB + (k == KB - 1 ? KB : KB - 1);
+      event = none ? 0x7fffffff : min(e, kb1);
+    }
+    __device__ __forceinline__ void next() {
+      ++at;
+      op.next();
+      if (at == event) place();
+    }
+  };
 
   // acc[i][j]: sub-tile row i, column j of this wave over blocks kb0 .. kb1 - 1 (one at
   // least); block kb is block kb % KB of segment kb / KB (at most two).
@@ -155,51 +190,24 @@ struct Bf16Tile {
       for (int j = 0; j < MJ; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
     lo.wave = ro.wave = wave;
     lo.l = ro.l = l;
-    // The block that is loaded next, and the one at which more than its place changes: a
-    // segment's last (k may end within it), its end, the end of all (from there on zeros).
-    int at = kb0, event;
-    const auto place = [&] {
-      const bool none = at >= kb1;
-      const int seg = at >= KB, k = seg ? at - KB : at;
-      lo.place(k, seg, KB, none);
-      ro.place(k, seg, KB, none);
-      asm volatile("");   // a branch, not a row of selects in every block
-      const int e = seg * KB + (k == KB - 1 ? KB : KB - 1);
-      event = none ? 0x7fffffff : min(e, kb1);
-    };
-    const auto next = [&] {
-      ++at;
-      lo.next();
-      ro.next();
-      if (at == event) place();
-    };
-    place();
-    uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(w4_lds_t*)lds + wave * 1024);
-    const auto load_one = [&](auto nn, auto half) {
-      constexpr int n = decltype(nn)::value, s = decltype(half)::value * BLOCK;
-      if constexpr (n < LU) lo.template load<s + 8192 * n>(n, base);
-      else ro.template load<s + L_BYTES + 8192 * (n - LU)>(n - LU, base);
-    };
-    // addresses within the block that is read from, of its first step (KC: of both)
-    constexpr int LP = LKS ? NI / 2 : 2, RP = RKS ? MJ / 2 : 2;
-    int la[LP], ra[RP];
-    const int kr = 8 * g + (lr >> 2), a = lr & 3;   // KS: row of the first four k, group of 4 columns
+    Feed<L> fl_ = {lo, kb0, 0, kb1, KB};
+    Feed<R> fr_ = {ro, kb0, 0, kb1, KB};
+    fl_.place();
+    fr_.place();
     const int lds0 = (int)(uintptr_t)(w4_lds_t*)lds;
+    const uint32_t lbase = __builtin_amdgcn_readfirstlane(lds0 + wave * 1024), rbase = lbase + R_OFF;
+    // addresses within a block, of its first step (KC: of both)
+    constexpr int LP = LKS ? NI / 2 : 2, RP = RKS ? MJ / 2 : 2;
+    int la[LP], ra[RP], lat[LP];   // lat: within the block that is read from
+    const int kr = 8 * g + (lr >> 2), a = lr & 3;   // KS: row of the first four k, group of 4 columns
 #pragma unroll
     for (int p = 0; p < LP; ++p)
-      la[p] = lds0 + (LKS ? kr * (BN * 2) + (((wn * (NI / 2) + p) ^ KsOp<LU, BN>::swz(kr)) << 6) + 16 * a
-                          : (wn * NI * 16 + lr) * 128 + (((4 * p + g) ^ swz8q(lr)) << 4));
+      la[p] = lat[p] = lds0 + (LKS ? kr * (BN * 2) + (((wn * (NI / 2) + p) ^ KsOp<LU, NW, BN>::swz(kr)) << 6) + 16 * a
+                                   : (wn * NI * 16 + lr) * 128 + (((4 * p + g) ^ swz8q(lr)) << 4));
 #pragma unroll
     for (int p = 0; p < RP; ++p)
-      ra[p] = lds0 + L_BYTES + (RKS ? kr * (BM * 2) + (((wm * (MJ / 2) + p) ^ KsOp<RU, BM>::swz(kr)) << 6) + 8 * a
-                                    : (wm * MJ * 16 + lr) * 128 + (((4 * p + g) ^ swz8q(lr)) << 4));
-    int flip = BLOCK;   // to the other block
-    const auto turn = [&] {
-#pragma unroll
-      for (int p = 0; p < LP; ++p) la[p] += flip;
-#pragma unroll
-      for (int p = 0; p < RP; ++p) ra[p] += flip;
-    };
+      ra[p] = lds0 + R_OFF + (RKS ? kr * (BM * 2) + (((wm * (MJ / 2) + p) ^ KsOp<RU, NW, BM>::swz(kr)) << 6) + 8 * a
+                                  : (wm * MJ * 16 + lr) * 128 + (((4 * p + g) ^ swz8q(lr)) << 4));
     typedef __attribute__((address_space(3))) const uint8_t lds_u8;
     typedef __attribute__((address_space(3))) const v4i lds_v4i;
     const auto tr8 = [&](lds_u8* p, int row4) {   // four k and the four after them, row4 bytes on
@@ -209,8 +217,8 @@ struct Bf16Tile {
     };
     // operands of step q of the block
     const auto read_l = [&](int q, int i) {
-      if constexpr (LKS) return tr8((lds_u8*)(la[i >> 1] + q * (32 * BN * 2) + 8 * (i & 1)), 4 * BN * 2);
-      else return *(lds_v4i*)(la[q] + i * 2048);
+      if constexpr (LKS) return tr8((lds_u8*)(lat[i >> 1] + q * (32 * BN * 2) + 8 * (i & 1)), 4 * BN * 2);
+      else return *(lds_v4i*)(lat[q] + i * 2048);
     };
     const auto read_r = [&](int q, int j) {
       if constexpr (RKS) return tr8((lds_u8*)(ra[j >> 1] + q * (32 * BM * 2) + 32 * (j & 1)), 4 * BM * 2);
@@ -220,61 +228,69 @@ struct Bf16Tile {
     using F = std::false_type;
     using Zero = std::integral_constant<int, 0>;
     using One = std::integral_constant<int, 1>;
-    unroll<LOADS>([&](auto nn) { load_one(nn, Zero{}); });
-    next();
-    unroll<LOADS>([&](auto nn) { load_one(nn, One{}); });
-    next();
-    w4_wait<LOADS>();
+    unroll<LU>([&](auto n) { lo.template load<n, 1024 * NW * n>(lbase); });
+    fl_.next();
+    unroll<RU>([&](auto n) { ro.template load<n, 1024 * NW * n>(rbase); });
+    fr_.next();
+    unroll<LU>([&](auto n) { lo.template load<n, L_BLOCK + 1024 * NW * n>(lbase); });
+    fl_.next();
+    w4_wait<LU>();
     lds_barrier();
-    v4i fl[NI], fr[2][MJ];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) fl[i] = read_l(0, i);
-#pragma unroll
-    for (int j = 0; j < MJ; ++j) fr[0][j] = read_r(0, j);
-    // Step q of a block; NEXT: another step follows, whose operands are read; LOAD: the
-    // block after the next is loaded into this one's place.
-    const auto step = [&](auto qq, auto load, auto nextp) {
+    if (LAG && wave >= NW / 2) lds_barrier();   // from here on a phase behind
+    v4i fl[NI], fr[MJ];
+    int lread = 0, lfill = 2 * L_BLOCK, rflip = R_BLOCK, rfill = R_BLOCK;   // places in the rings
+    // Step q of a block: its operands from LDS; LOAD: the right operand of the next block
+    // (q = 0) or the left one of the block after (q = 1) is asked for; FLY: loads that may
+    // be in flight when those of the next block have landed.
+    const auto step = [&](auto qq, auto load, auto fly) {
       constexpr int q = decltype(qq)::value;
-      constexpr bool LOAD = decltype(load)::value && q == 1, NEXT = decltype(nextp)::value;
-      unroll<NI>([&](auto ii) {
-        constexpr int i = decltype(ii)::value;
+      constexpr bool LOAD = decltype(load)::value;
 #pragma unroll
-        for (int j = 0; j < MJ; ++j) acc[i][j] = w4_mfma(fl[i], fr[q][j], acc[i][j]);
-        __builtin_amdgcn_sched_barrier(0);   // the read below takes the registers of fl[i]
-        if constexpr (i == 0 && q == 1 && NEXT) {
-          // own loads of the next block have landed; every wave has read all of this one
-          w4_wait<0>();
-          lds_barrier();
-          turn();
-        }
-        if constexpr (NEXT) {
-          fl[i] = read_l(q ^ 1, i);
+      for (int j = 0; j < MJ; ++j) fr[j] = read_r(q, j);
 #pragma unroll
-          for (int j = i * MJ / NI; j < (i + 1) * MJ / NI; ++j) fr[q ^ 1][j] = read_r(q ^ 1, j);
-        }
-        if constexpr (LOAD) {
-          unroll<LOADS>([&](auto nn) {
-            constexpr int n = decltype(nn)::value;
-            if constexpr (n >= i * LOADS / NI && n < (i + 1) * LOADS / NI) load_one(nn, Zero{});
-          });
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      });
-      if constexpr (LOAD) next();
-      if constexpr (q == 1) {
-        base += flip;
-        flip = -flip;
+      for (int i = 0; i < NI; ++i) fl[i] = read_l(q, i);
+      if constexpr (LOAD && q == 0) {
+        const uint32_t to = rbase + rfill;
+        unroll<RU>([&](auto n) { ro.template load<n, 1024 * NW * n>(to); });
+        fr_.next();
+        rfill ^= R_BLOCK;
       }
+      if constexpr (LOAD && q == 1) {
+        const uint32_t to = lbase + lfill;
+        unroll<LU>([&](auto n) { lo.template load<n, 1024 * NW * n>(to); });
+        fl_.next();
+        lfill = lfill == 2 * L_BLOCK ? 0 : lfill + L_BLOCK;
+      }
+      if constexpr (q == 1) {
+        lread = lread == 2 * L_BLOCK ? 0 : lread + L_BLOCK;
+#pragma unroll
+        for (int p = 0; p < LP; ++p) lat[p] = la[p] + lread;
+#pragma unroll
+        for (int p = 0; p < RP; ++p) ra[p] += rflip;
+        rflip = -rflip;
+        w4_wait<decltype(fly)::value>();
+      }
+      lds_barrier();
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < MJ; ++j) acc[i][j] = w4_mfma(fl[i], fr[j], acc[i][j]);
+      __builtin_amdgcn_s_setprio(0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (LAG) lds_barrier();
+      __builtin_amdgcn_sched_barrier(0);
     };
     // two blocks at least, zeros behind the last
     for (int left = max(kb1 - kb0, 2); left > 2; --left) {
-      step(Zero{}, T{}, T{});
-      step(One{}, T{}, T{});
+      step(Zero{}, T{}, Zero{});
+      step(One{}, T{}, std::integral_constant<int, LU>{});
     }
-    step(Zero{}, F{}, T{});
-    step(One{}, F{}, T{});
-    step(Zero{}, F{}, T{});
-    step(One{}, F{}, F{});
+    step(Zero{}, T{}, Zero{});
+    step(One{}, F{}, Zero{});
+    step(Zero{}, F{}, Zero{});
+    step(One{}, F{}, Zero{});
+    if (LAG && wave < NW / 2) lds_barrier();   // of the others' last phase
   }
   template <int N, int I = 0, typename Fn>
   __device__ static __forceinline__ void unroll(Fn fn) {

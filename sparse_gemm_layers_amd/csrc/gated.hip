@@ -123,21 +123,22 @@ __device__ __forceinline__ void gated_finish(const GatedArgs& a, int64_t m, int 
 
 // Left rows of a tile: a wave's first NI / 2 sub-tiles are gate rows, the others up rows
 // of the same f.
-template <int NI>
+template <int NI, int NW>
 struct GatedRow {
+  static constexpr int MATS = 2, HALF = NI / 2;
+  static_assert(NW / 2 <= HALF, "an instruction of every wave is of the same matrix");
 #if SG_DEVICE_PASS
-  static constexpr int HALF = NI / 2;
   __device__ static __forceinline__ int row(int u, int wave, int l) {
-    const int s = (8 * u + wave) >> 1, r = 8 * (wave & 1) + (l >> 3);
+    const int s = (NW * u + wave) >> 1, r = 8 * (wave & 1) + (l >> 3);
     return s / NI * (16 * HALF) + tile_n(s % HALF, r);
   }
-  __device__ static __forceinline__ int sel(int u, int wave) { return ((8 * u + wave) >> 1) / HALF & 1; }
+  __device__ static constexpr int sel(int u) { return NW / 2 * u / HALF & 1; }
 #endif
 };
 
 // Many rows: tiles of BN / 2 rows of each weight x BM tokens (bf16_tile.h).
 template <typename T, bool BACK>
-__global__ void __launch_bounds__(512) k_gated_tile(GatedArgs a, int tiles_m, int tiles_n) {
+__global__ void __launch_bounds__(T::NW * 64) k_gated_tile(GatedArgs a, int tiles_m, int tiles_n) {
 #if SG_DEVICE_PASS
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   int tn, tm;
@@ -312,7 +313,7 @@ struct GatedGradArgs {
 // dX [T, D]: left the weights' columns (k across rows), right dG and dU; the sum runs
 // over dG . Wg, then dU . Wu.
 template <typename T>
-__global__ void __launch_bounds__(512) k_gated_dx(GatedGradArgs a, int tiles_m, int tiles_n) {
+__global__ void __launch_bounds__(T::NW * 64) k_gated_dx(GatedGradArgs a, int tiles_m, int tiles_n) {
 #if SG_DEVICE_PASS
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   int tn, tm;
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(256) k_gated_dx_join(GatedGradArgs a) {
 // dWg and dWu [F, D]: left the columns of X, right those of dG (the first half of the
 // tiles along m) or dU; the sum runs over tokens, across the rows of both.
 template <typename T>
-__global__ void __launch_bounds__(512) k_gated_dw(GatedGradArgs a, int tiles_m, int tiles_n) {
+__global__ void __launch_bounds__(T::NW * 64) k_gated_dw(GatedGradArgs a, int tiles_m, int tiles_n) {
 #if SG_DEVICE_PASS
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
   int tn, tm;
@@ -425,8 +426,10 @@ __global__ void __launch_bounds__(512) k_gated_dw(GatedGradArgs a, int tiles_m, 
 #endif  // SG_DEVICE_PASS
 }
 
-template <bool L, bool R, typename Row = PlainRow> using TileA = Bf16Tile<L, R, 2, 4, 8, 4, Row>;   // 256 x 256
-template <bool L, bool R, typename Row = PlainRow> using TileB = Bf16Tile<L, R, 2, 4, 4, 2, Row>;   // 128 x 128
+template <bool L, bool R, typename Row = PlainRow<8>> using TileA = Bf16Tile<L, R, 2, 4, 8, 4, Row>;   // 256 x 256
+template <bool L, bool R, typename Row = PlainRow<4>> using TileB = Bf16Tile<L, R, 2, 2, 4, 4, Row>;   // 128 x 128
+using RowA = GatedRow<8, 8>;
+using RowB = GatedRow<4, 4>;
 
 template <bool BACK, int MT>
 static void launch_gated_rows(const GatedArgs& a, hipStream_t st) {
@@ -445,13 +448,13 @@ static void launch_gated(const GatedArgs& a, hipStream_t st) {
     return;
   }
   if (cdiv(a.T, 256) * cdiv(a.F, 128) >= 256) {
-    using T = TileA<false, false, GatedRow<8>>;
+    using T = TileA<false, false, RowA>;
     const int tm = (int)cdiv(a.T, 256), tn = (int)cdiv(a.F, 128);
-    k_gated_tile<T, BACK><<<(unsigned)tm * tn, 512, 0, st>>>(a, tm, tn);
+    k_gated_tile<T, BACK><<<(unsigned)tm * tn, T::NW * 64, 0, st>>>(a, tm, tn);
   } else {
-    using T = TileB<false, false, GatedRow<4>>;
+    using T = TileB<false, false, RowB>;
     const int tm = (int)cdiv(a.T, 128), tn = (int)cdiv(a.F, 64);
-    k_gated_tile<T, BACK><<<(unsigned)tm * tn, 512, 0, st>>>(a, tm, tn);
+    k_gated_tile<T, BACK><<<(unsigned)tm * tn, T::NW * 64, 0, st>>>(a, tm, tn);
   }
 }
 
@@ -552,20 +555,20 @@ extern "C" sg_status sg_gated_gemm_backward(int64_t T, int64_t F, int64_t D, con
   if (dx) {
     if (plan.big) {
       const int tm = (int)cdiv(T, 256), tn = (int)cdiv(D, 256);
-      k_gated_dx<TileA<true, false>><<<(unsigned)(tm * tn * plan.splits), 512, 0, stream>>>(b, tm, tn);
+      k_gated_dx<TileA<true, false>><<<(unsigned)(tm * tn * plan.splits), TileA<true, false>::NW * 64, 0, stream>>>(b, tm, tn);
     } else {
       const int tm = (int)cdiv(T, 128), tn = (int)cdiv(D, 128);
-      k_gated_dx<TileB<true, false>><<<(unsigned)(tm * tn * plan.splits), 512, 0, stream>>>(b, tm, tn);
+      k_gated_dx<TileB<true, false>><<<(unsigned)(tm * tn * plan.splits), TileB<true, false>::NW * 64, 0, stream>>>(b, tm, tn);
     }
     if (plan.splits > 1) k_gated_dx_join<<<grid_for(T * (D / 8), 256, 8192), 256, 0, stream>>>(b);
   }
   if (dgate) {
     if (2 * cdiv(F, 256) * cdiv(D, 256) >= 256) {
       const int tm = 2 * (int)cdiv(F, 256), tn = (int)cdiv(D, 256);
-      k_gated_dw<TileA<true, true>><<<(unsigned)tm * tn, 512, 0, stream>>>(b, tm, tn);
+      k_gated_dw<TileA<true, true>><<<(unsigned)tm * tn, TileA<true, true>::NW * 64, 0, stream>>>(b, tm, tn);
     } else {
       const int tm = 2 * (int)cdiv(F, 128), tn = (int)cdiv(D, 128);
-      k_gated_dw<TileB<true, true>><<<(unsigned)tm * tn, 512, 0, stream>>>(b, tm, tn);
+      k_gated_dw<TileB<true, true>><<<(unsigned)tm * tn, TileB<true, true>::NW * 64, 0, stream>>>(b, tm, tn);
     }
   }
   return launch_status();
