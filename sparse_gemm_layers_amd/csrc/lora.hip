@@ -4,17 +4,19 @@
 //   u = x . A_e^T, v = s_e dy . B_e, dx = base + v . A_e,
 //   dA_e = sum_t v[t]^T x[t], dB_e = s_e sum_t dy[t]^T u[t].
 // Three kinds of kernel, all bound by memory: "down" products [T, C] -> [T, r], the
-// long side summed in parts over workgroups; "up" products [T, r] -> [T, C], which add up
-// those parts as they read them; and the sums over an adapter's tokens [T, r]^T [T, C].
+// long side summed in up to LORA_PARTS parts over workgroups; "up" products [T, r] ->
+// [T, C], which add up those parts as they read them; and the sums over an adapter's
+// tokens [T, r]^T [T, C].
 //
 // The [T, r] values between two products stay fp32 in memory and enter the matrix
 // core as a sum of NP bf16 parts (each the rounding of what the ones before leave):
 // with so few ranks that costs matrix instructions only, which nothing waits for.
 //
-// Down and up go by blocks of 16 TM consecutive tokens and, within one, by the adapters
-// that appear in it: one for a prompt, up to 16 in a decoding batch, where the
-// third dimension of the grid shares them out.  A token's row of a product is kept from the
-// pass of its own adapter alone.  The sums gather the rows of one adapter.
+// Down and up go by blocks of 64 tokens, one to a lane.  The tokens of one adapter in
+// a block are gathered, 16 TM at a time, into the columns of a matrix product (an
+// "item"): a prompt's block is few items, a decoding batch's many, which the third
+// dimension of the grid shares out, and either way an adapter is read once for
+// all of them.  The sums over tokens gather the rows of one adapter likewise.
 #include "bf16_tile.h"
 #include "sg_lora.h"
 
@@ -28,20 +30,39 @@ __device__ __forceinline__ int lora_id(const int32_t* ids, int64_t t, int64_t T,
   return e >= 0 && e < L ? e : -1;
 }
 
-// The next adapter among those of this block's tokens (id[j]: token 16 j + l % 16) that are not
-// done, which it marks; -1: no more.
-template <int TM>
-__device__ __forceinline__ int lora_next(const int (&id)[TM], bool (&done)[TM]) {
-  int e = -1;
-#pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    const uint64_t m = __ballot(id[j] >= 0 && !done[j]);
-    if (e < 0 && m) e = __builtin_amdgcn_readlane(id[j], __builtin_ctzll(m));
+// The items of a block of 64 tokens: lane l holds the adapter of token t0 + l.
+struct LoraItems {
+  int id;
+  uint64_t left;
+  int* list;   // 64 in LDS, this wave's own
+  __device__ __forceinline__ void start(const int32_t* ids, int64_t t0, int64_t T, int L, int l, bool none, int* lds) {
+    id = lora_id(ids, t0 + l, T, L);
+    left = __ballot(t0 + l < T && (none || id >= 0));
+    list = lds;
   }
+  // The next adapter (-1: tokens without one) and up to 16 TM of its tokens: tok[j] is
+  // column 16 j + l % 16's place in the block, -1: none.
+  template <int TM>
+  __device__ __forceinline__ bool next(int l, int& e, int (&tok)[TM]) {
+    if (!left) return false;
+    e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+    const uint64_t m = __ballot(id == e) & left;
+    const int rank = __builtin_popcountll(m & ((1ull << l) - 1));
+    const bool mine = ((m >> l) & 1) && rank < 16 * TM;
+    const uint64_t taken = __ballot(mine);
+    left &= ~taken;
+    const int n = __builtin_popcountll(taken);
+    if (mine) list[rank] = l;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
-  for (int j = 0; j < TM; ++j) done[j] = done[j] || id[j] == e;
-  return e;
-}
+    for (int j = 0; j < TM; ++j) {
+      const int c = 16 * j + (l & 15);
+      tok[j] = c < n ? list[c] : -1;
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    return true;
+  }
+};
 
 // NP bf16 parts of eight fp32 values.  What an infinite part or a NaN leaves is nothing,
 // not the NaN that subtracting it gives.
@@ -60,6 +81,9 @@ __device__ __forceinline__ void lora_parts(float (&v)[8], v4i (&p)[NP]) {
 }
 #endif
 
+constexpr int LORA_PARTS = 4;    // of a down product's sum, at most
+constexpr int LORA_WAVES = 8;    // of a down workgroup
+
 // ------------------------------------------------------------------ down
 
 struct LoraDown {
@@ -71,85 +95,98 @@ struct LoraDown {
   float* part;             // [splits][T][r]
 };
 
+// A workgroup's waves take every LORA_WAVES-th 64 columns of its part; the next ones are asked
+// for while these are multiplied.
 template <bool KS, int TM, int RM>
-__global__ void __launch_bounds__(256) k_lora_down(LoraDown a) {
+__global__ void __launch_bounds__(512) k_lora_down(LoraDown a) {
 #if SG_DEVICE_PASS
   constexpr int PITCH = 32 * RM + 16;   // KS: one row's ranks in LDS
-  constexpr int RED = 4 * RM * TM * 1024, STG = KS ? 4 * 64 * PITCH : 0;
+  constexpr int RED = LORA_WAVES * RM * TM * 1024, STG = KS ? LORA_WAVES * 64 * PITCH : 0;
   __shared__ __attribute__((aligned(16))) uint8_t lds[RED > STG ? RED : STG];
+  __shared__ int lists[LORA_WAVES][64];
   const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int64_t t0 = (int64_t)blockIdx.x * (16 * TM);
+  const int64_t t0 = (int64_t)blockIdx.x * 64;
   const int split = blockIdx.y % a.splits, rho0 = (int)(blockIdx.y / a.splits) * 16 * RM;
-  const int rows = (int)min((int64_t)(16 * TM), a.T - t0);
+  const int rows = (int)min((int64_t)64, a.T - t0);
   const int units = (a.C + 63) >> 6;   // of 64 columns
   const int u0 = (int)((int64_t)units * split / a.splits), u1 = (int)((int64_t)units * (split + 1) / a.splits);
-  int id[TM];
-  bool done[TM];
-  uint32_t zo[TM];
-#pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    id[j] = lora_id(a.ids, t0 + 16 * j + lr, a.T, a.L);
-    done[j] = false;
-    zo[j] = 16 * j + lr < rows ? (uint32_t)(((16 * j + lr) * a.ldz + 8 * g) * 2) : W4_OUT;
-  }
+  LoraItems items;
+  items.start(a.ids, t0, a.T, a.L, l, false, lists[wave]);
   const __amdgpu_buffer_rsrc_t rz = w4_rsrc(a.z + t0 * a.ldz, (uint32_t)(((rows - 1) * a.ldz + a.C) * 2));
-  for (int d = 0;; ++d) {
-    const int e = lora_next<TM>(id, done);
-    if (e < 0) break;
+  int e, tok[TM];
+  for (int d = 0; items.next<TM>(l, e, tok); ++d) {
     if (d % gridDim.z != blockIdx.z) continue;
     const uint16_t* const w = a.w + (int64_t)e * a.r * a.C;
-    const __amdgpu_buffer_rsrc_t rw = KS ? w4_rsrc(w, 0) : w4_rsrc(w + (int64_t)rho0 * a.C, (uint32_t)(min(a.r - rho0, 16 * RM) * a.C * 2));
+    // KC: rows of ranks past r are outside; KS: its rows hold all ranks
+    const __amdgpu_buffer_rsrc_t rw =
+        KS ? w4_rsrc(w, (uint32_t)(a.C * a.r * 2))
+           : w4_rsrc(w + (int64_t)rho0 * a.C, (uint32_t)(min(a.r - rho0, 16 * RM) * a.C * 2));
+    uint32_t zo[TM];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) zo[j] = tok[j] >= 0 ? (uint32_t)((tok[j] * a.ldz + 8 * g) * 2) : W4_OUT;
     v4f acc[RM][TM];
 #pragma unroll
     for (int m = 0; m < RM; ++m)
 #pragma unroll
       for (int j = 0; j < TM; ++j) acc[m][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-    for (int u = u0 + wave; u < u1; u += 4) {
-      v4i zf[TM][2], wf[RM][2];
+    v4i zf[2][TM][2], wv[2][RM][2];
+    const auto load = [&](int s, int u) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const bool in = 64 * u + 32 * q + 8 * g < a.C;
 #pragma unroll
-        for (int j = 0; j < TM; ++j) zf[j][q] = w4_ld16(rz, in ? zo[j] + 64 * q : W4_OUT, u * 128);
-        if (!KS) {
+        for (int j = 0; j < TM; ++j) zf[s][j][q] = w4_ld16(rz, in ? zo[j] + 64 * q : W4_OUT, u * 128);
 #pragma unroll
-          for (int m = 0; m < RM; ++m) {
-            const int rho = 16 * m + lr;
-            wf[m][q] = w4_ld16(rw, in && rho0 + rho < a.r ? (uint32_t)((rho * a.C + 8 * g + 32 * q) * 2) : W4_OUT, u * 128);
+        for (int m = 0; m < RM; ++m) {
+          if (KS) {   // 16 bytes c of row k; the 64 rows of 16 RM ranks are 2 RM loads
+            const int i = (2 * m + q) * 64 + l, k = i / (2 * RM), c = i % (2 * RM);
+            wv[s][m][q] = w4_ld16(rw, rho0 + 8 * c < a.r ? ((uint32_t)(64 * u + k) * a.r + rho0 + 8 * c) * 2 : W4_OUT, 0);
+          } else {
+            wv[s][m][q] = w4_ld16(rw, in ? (uint32_t)(((16 * m + lr) * a.C + 8 * g + 32 * q) * 2) : W4_OUT, u * 128);
           }
         }
       }
-      if (KS) {   // 64 rows of 16 RM ranks through this wave's part of LDS
+    };
+    const auto compute = [&](int s) {
+      if (KS) {
         uint8_t* const st = lds + wave * 64 * PITCH;
-        uint4 v[2 * RM];
 #pragma unroll
-        for (int i = 0; i < 2 * RM; ++i) {
-          const int k = (i * 64 + l) / (2 * RM), c = (i * 64 + l) % (2 * RM);
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (64 * u + k < a.C && rho0 + 8 * c < a.r)
-            v[i] = *reinterpret_cast<const uint4*>(w + (int64_t)(64 * u + k) * a.r + rho0 + 8 * c);
-        }
+        for (int m = 0; m < RM; ++m)
 #pragma unroll
-        for (int i = 0; i < 2 * RM; ++i) {
-          const int k = (i * 64 + l) / (2 * RM), c = (i * 64 + l) % (2 * RM);
-          *reinterpret_cast<uint4*>(st + k * PITCH + 16 * c) = v[i];
-        }
+          for (int q = 0; q < 2; ++q) {
+            const int i = (2 * m + q) * 64 + l;
+            *reinterpret_cast<v4i*>(st + i / (2 * RM) * PITCH + 16 * (i % (2 * RM))) = wv[s][m][q];
+          }
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
           for (int m = 0; m < RM; ++m) {
             const uint8_t* const at = st + (32 * q + 8 * g + (lr >> 2)) * PITCH + 32 * m + 8 * (lr & 3);
             const uint2 x = lds_tr4(at), y = lds_tr4(at + 4 * PITCH);
-            wf[m][q] = (v4i){(int)x.x, (int)x.y, (int)y.x, (int)y.y};
+            const v4i wf = {(int)x.x, (int)x.y, (int)y.x, (int)y.y};
+#pragma unroll
+            for (int j = 0; j < TM; ++j) acc[m][j] = w4_mfma(wf, zf[s][j][q], acc[m][j]);
           }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int m = 0; m < RM; ++m)
+#pragma unroll
+            for (int j = 0; j < TM; ++j) acc[m][j] = w4_mfma(wv[s][m][q], zf[s][j][q], acc[m][j]);
       }
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int m = 0; m < RM; ++m)
-#pragma unroll
-          for (int j = 0; j < TM; ++j) acc[m][j] = w4_mfma(wf[m][q], zf[j][q], acc[m][j]);
+    };
+    int u = u0 + wave;
+    if (u < u1) load(0, u);
+    for (; u < u1; u += 2 * LORA_WAVES) {
+      const bool more = u + LORA_WAVES < u1;
+      if (more) load(1, u + LORA_WAVES);
+      compute(0);
+      if (more) {
+        if (u + 2 * LORA_WAVES < u1) load(0, u + 2 * LORA_WAVES);
+        compute(1);
+      }
     }
     float(*const red)[RM * TM][64][4] = reinterpret_cast<float(*)[RM * TM][64][4]>(lds);
     if (KS) __syncthreads();
@@ -158,17 +195,17 @@ __global__ void __launch_bounds__(256) k_lora_down(LoraDown a) {
 #pragma unroll
       for (int j = 0; j < TM; ++j) *reinterpret_cast<v4f*>(&red[wave][m * TM + j][l][0]) = acc[m][j];
     __syncthreads();
-    for (int q = wave; q < RM * TM; q += 4) {
+    for (int q = wave; q < RM * TM; q += LORA_WAVES) {
       const int m = q / TM, j = q % TM;
       v4f s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) s += *reinterpret_cast<const v4f*>(&red[k][q][l][0]);
-      int mine = -1;   // the id of token 16 j + lr
+      for (int k = 0; k < LORA_WAVES; ++k) s += *reinterpret_cast<const v4f*>(&red[k][q][l][0]);
+      int mine = -1;
 #pragma unroll
-      for (int i = 0; i < TM; ++i) mine = i == j ? id[i] : mine;
+      for (int i = 0; i < TM; ++i) mine = i == j ? tok[i] : mine;
       const int rho = rho0 + 16 * m + 4 * g;
-      if (mine == e && rho < a.r)
-        *reinterpret_cast<float4*>(a.part + ((int64_t)split * a.T + t0 + 16 * j + lr) * a.r + rho) =
+      if (mine >= 0 && rho < a.r)
+        *reinterpret_cast<float4*>(a.part + ((int64_t)split * a.T + t0 + mine) * a.r + rho) =
             make_float4(s[0], s[1], s[2], s[3]);
     }
     __syncthreads();
@@ -194,48 +231,65 @@ struct LoraUp {
 };
 
 #if SG_DEVICE_PASS
-// Ranks rho .. rho + 7 of token t's [T, r] value: its parts added in order, scaled.
-__device__ __forceinline__ void lora_value(const float* part, int splits, int64_t T, int r, int64_t t, int rho,
-                                           float scale, float (&v)[8]) {
+// Ranks rho .. rho + 7 of token t's [T, r] value: its parts, all asked for at once;
+// lora_total adds them in order and scales.
+struct LoraValue {
+  float4 x[LORA_PARTS][2];
+  __device__ __forceinline__ void load(const float* part, int splits, int64_t T, int r, int64_t t, int rho, bool there) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  for (int s = 0; s < splits; ++s) {
-    float x[8];
-    load4(part + ((int64_t)s * T + t) * r + rho, x);
-    load4(part + ((int64_t)s * T + t) * r + rho + 4, x + 4);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += x[i];
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= scale;
-}
-
-// Columns n .. n + 7 of row t: base plus v.
-__device__ __forceinline__ void lora_store(const LoraUp& a, int64_t t, int n, float (&v)[8]) {
-  if (a.base) {
-    float x[8];
-    if (a.base_f32) {
-      const float* const p = reinterpret_cast<const float*>(a.base) + t * a.ld_base + n;
-      load4(p, x);
-      load4(p + 4, x + 4);
-    } else {
-      const uint16_t* const p = reinterpret_cast<const uint16_t*>(a.base) + t * a.ld_base + n;
-      load4(p, x);
-      load4(p + 4, x + 4);
+    for (int s = 0; s < LORA_PARTS; ++s) {
+      x[s][0] = x[s][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < splits && there) {
+        const float4* const p = reinterpret_cast<const float4*>(part + ((int64_t)s * T + t) * r + rho);
+        x[s][0] = p[0];
+        x[s][1] = p[1];
+      }
     }
+  }
+  __device__ __forceinline__ void total(float scale, float (&v)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += x[i];
+    for (int i = 0; i < 8; ++i) {
+      const auto at = [&](int s) {
+        const float4 q = x[s][i >> 2];
+        return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+      };
+      float t = at(0);
+#pragma unroll
+      for (int s = 1; s < LORA_PARTS; ++s) t += at(s);
+      v[i] = t * scale;
+    }
   }
-  if (a.y_f32) {
-    float* const o = reinterpret_cast<float*>(a.y) + t * a.ldy + n;
-    *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
-  } else {
-    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.y) + t * a.ldy + n) =
-        make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
-                   f32x2_to_bf16x2(v[6], v[7]));
+};
+
+// Eight neighbours of base, as they are stored.
+struct LoraBase {
+  uint4 x[2];
+  __device__ __forceinline__ void load(const LoraUp& a, int64_t t, int n, bool there) {
+    x[0] = x[1] = make_uint4(0, 0, 0, 0);
+    if (a.base && there) {
+      const uint8_t* const p = reinterpret_cast<const uint8_t*>(a.base) + (t * a.ld_base + n) * (a.base_f32 ? 4 : 2);
+      x[0] = *reinterpret_cast<const uint4*>(p);
+      if (a.base_f32) x[1] = *reinterpret_cast<const uint4*>(p + 16);
+    }
   }
-}
+  __device__ __forceinline__ void store(const LoraUp& a, int64_t t, int n, float (&v)[8]) const {
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    if (a.base) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] += __uint_as_float(a.base_f32 ? w[i] : (i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+    }
+    if (a.y_f32) {
+      float* const o = reinterpret_cast<float*>(a.y) + t * a.ldy + n;
+      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.y) + t * a.ldy + n) =
+          make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
+                     f32x2_to_bf16x2(v[6], v[7]));
+    }
+  }
+};
 #endif
 
 // A workgroup's four waves take 64 columns each.
@@ -244,52 +298,54 @@ __global__ void __launch_bounds__(256) k_lora_up(LoraUp a) {
 #if SG_DEVICE_PASS
   constexpr int PITCH = 128 + 16;   // KS: 64 columns of one rank in LDS
   __shared__ __attribute__((aligned(16))) uint8_t lds[KS ? 4 * 32 * PITCH : 16];
+  __shared__ int lists[4][64];
   const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int64_t t0 = (int64_t)blockIdx.x * (16 * TM);
+  const int64_t t0 = (int64_t)blockIdx.x * 64;
   const int n0 = (blockIdx.y * 4 + wave) * 64;
   if (n0 >= a.C) return;   // no barrier follows
-  int id[TM];
-  bool done[TM];
-#pragma unroll
-  for (int j = 0; j < TM; ++j) {
-    id[j] = lora_id(a.ids, t0 + 16 * j + lr, a.T, a.L);
-    done[j] = false;
-  }
-  for (int d = 0;; ++d) {
-    const int e = lora_next<TM>(id, done);
-    if (e < 0) break;
+  LoraItems items;
+  items.start(a.ids, t0, a.T, a.L, l, a.y != a.base, lists[wave]);
+  int e, tok[TM];
+  for (int d = 0; items.next<TM>(l, e, tok); ++d) {
     if (d % gridDim.z != blockIdx.z) continue;
-    const float scale = a.scale ? a.scale[e] : 1.0f;
-    const uint16_t* const w = a.w + (int64_t)e * a.r * a.C;
+    LoraBase base[TM][2];
+#pragma unroll
+    for (int j = 0; j < TM; ++j)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int n = n0 + 32 * q + 8 * g;
+        base[j][q].load(a, t0 + tok[j], n, tok[j] >= 0 && n < a.C);
+      }
     v4f acc[4][TM];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < TM; ++j) acc[i][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-    for (int rho0 = 0; rho0 < a.r; rho0 += 32) {
+    const float scale = a.scale && e >= 0 ? a.scale[e] : 1.0f;
+    const uint16_t* const w = a.w + (int64_t)e * a.r * a.C;
+    for (int rho0 = 0; e >= 0 && rho0 < a.r; rho0 += 32) {
       const int rho = rho0 + 8 * g;
       v4i wf[4];
-      if (!KS) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; ++i) {
+        wf[i] = (v4i){0, 0, 0, 0};
+        if (!KS) {
           const int n = n0 + tile_n(i, lr);
-          wf[i] = (v4i){0, 0, 0, 0};
           if (n < a.C && rho < a.r) wf[i] = *reinterpret_cast<const v4i*>(w + (int64_t)n * a.r + rho);
+        } else {
+          const int k = rho0 + 8 * i + (l >> 3), c = n0 + 8 * (l & 7);
+          if (k < a.r && c < a.C) wf[i] = *reinterpret_cast<const v4i*>(w + (int64_t)k * a.C + c);
         }
-      } else {
+      }
+      LoraValue value[TM];
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+        value[j].load(a.part, a.splits, a.T, a.r, t0 + tok[j], rho, tok[j] >= 0 && rho < a.r);
+      if (KS) {
         uint8_t* const st = lds + wave * 32 * PITCH;
-        uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = 8 * i + (l >> 3), c = 8 * (l & 7);
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (rho0 + k < a.r && n0 + c < a.C)
-            v[i] = *reinterpret_cast<const uint4*>(w + (int64_t)(rho0 + k) * a.C + n0 + c);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(st + (8 * i + (l >> 3)) * PITCH + 16 * (l & 7)) = v[i];
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<v4i*>(st + (8 * i + (l >> 3)) * PITCH + 16 * (l & 7)) = wf[i];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint8_t* const at = st + (8 * g + (lr >> 2)) * PITCH + 64 * (i >> 1) + 16 * (lr & 3) + 8 * (i & 1);
@@ -299,8 +355,8 @@ __global__ void __launch_bounds__(256) k_lora_up(LoraUp a) {
       }
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (id[j] == e && rho < a.r) lora_value(a.part, a.splits, a.T, a.r, t0 + 16 * j + lr, rho, scale, v);
+        float v[8];
+        value[j].total(scale, v);
         v4i p[NP];
         lora_parts<NP>(v, p);
 #pragma unroll
@@ -314,23 +370,11 @@ __global__ void __launch_bounds__(256) k_lora_up(LoraUp a) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int n = n0 + 32 * q + 8 * g;
-        if (id[j] == e && n < a.C) {
+        if (tok[j] >= 0 && n < a.C) {
           float v[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = acc[2 * q + (i >> 2)][j][i & 3];
-          lora_store(a, t0 + 16 * j + lr, n, v);
-        }
-      }
-  }
-  if (blockIdx.z == 0 && a.y != a.base) {   // tokens without an adapter
-#pragma unroll
-    for (int j = 0; j < TM; ++j)
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int n = n0 + 32 * q + 8 * g;
-        if (id[j] < 0 && t0 + 16 * j + lr < a.T && n < a.C) {
-          float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          lora_store(a, t0 + 16 * j + lr, n, v);
+          base[j][q].store(a, t0 + tok[j], n, v);
         }
       }
   }
@@ -408,22 +452,29 @@ __global__ void __launch_bounds__(256) k_lora_sum(LoraSum a) {
         if (k < total && c < a.C) zv[i] = *reinterpret_cast<const uint4*>(a.z + (c0 + list[k]) * a.ldz + c);
       }
     };
+    LoraValue value;   // eight ranks of one token
+    const int vk = t / (2 * RM), vrho = rho0 + 8 * (t % (2 * RM));
+    const auto load_v = [&](int k0) {
+      const bool there = t < 64 * RM && k0 + vk < total && vrho < a.r;
+      value.load(a.part, a.splits, a.T, a.r, there ? c0 + list[k0 + vk] : 0, vrho, there);
+    };
     load_z(0);
+    load_v(0);
     for (int k0 = 0; k0 < total; k0 += 32) {
-      for (int o = t; o < 64 * RM; o += 256) {   // eight ranks of one token each
-        const int k = o / (2 * RM), rho = rho0 + 8 * (o % (2 * RM));
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (k0 + k < total && rho < a.r) lora_value(a.part, a.splits, a.T, a.r, c0 + list[k0 + k], rho, scale, v);
+      if (t < 64 * RM) {
+        float v[8];
+        value.total(scale, v);
         v4i p[NP];
         lora_parts<NP>(v, p);
 #pragma unroll
-        for (int q = 0; q < NP; ++q) *reinterpret_cast<v4i*>(pl + (q * 32 + k) * PP + 16 * (o % (2 * RM))) = p[q];
+        for (int q = 0; q < NP; ++q) *reinterpret_cast<v4i*>(pl + (q * 32 + vk) * PP + 16 * (t % (2 * RM))) = p[q];
       }
       uint8_t* const st = zl + wave * 32 * ZP;
 #pragma unroll
       for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(st + (8 * i + (l >> 3)) * ZP + 16 * (l & 7)) = zv[i];
       __syncthreads();
       load_z(k0 + 32);
+      load_v(k0 + 32);
       v4i zf[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -515,20 +566,21 @@ __global__ void __launch_bounds__(256) k_lora_join(LoraJoin a) {
 
 // ------------------------------------------------------------------ sizes
 
-// Workgroups' share of the adapters in a block of 16 tokens: all of one block where
-// there are few blocks.
-static int lora_slots(int64_t T, int64_t L, int64_t groups) {
-  const int64_t most = L < 16 ? L : 16, n = T < most ? T : most;
+// Workgroups that share the items of a block of 64 tokens: as many as it may have,
+// while that does not come to more than 1024.
+static int lora_slots(int64_t T, int64_t L, int64_t groups, int tm) {
+  const int64_t n = T < 64 ? T : 64, most = (L < n ? L : n) + n / (16 * tm);
   int64_t s = 1024 / (groups < 1 ? 1 : groups);
-  return (int)(s < 1 ? 1 : s > n ? n : s);
+  return (int)(s < 1 ? 1 : s > most ? most : s);
 }
 
-// Parts of a down product's sum: enough workgroups, and at least 256 columns each.
+// Parts of a down product's sum: 256 workgroups where 16-token items give fewer, at
+// least two units of 64 columns a wave each.
 static int lora_splits(int64_t T, int64_t C) {
-  int64_t s = 512 / cdiv(T, 16);
-  const int64_t most = cdiv(C, 256);
+  int64_t s = 256 / cdiv(T, 16);
+  const int64_t most = cdiv(C, 64 * 2 * LORA_WAVES);
   s = s > most ? most : s;
-  return (int)(s < 1 ? 1 : s > 16 ? 16 : s);
+  return (int)(s < 1 ? 1 : s > LORA_PARTS ? LORA_PARTS : s);
 }
 
 static int lora_tsplits(int64_t T, int64_t C, int64_t L) {
@@ -562,24 +614,30 @@ struct LoraSpace {
 
 template <bool KS, int TM>
 static void launch_down_rm(const LoraDown& a, hipStream_t st) {
-  const unsigned gx = (unsigned)cdiv(a.T, 16 * TM);
+  const unsigned gx = (unsigned)cdiv(a.T, 64);
   const auto grid = [&](int rm) {
     const int64_t gy = a.splits * cdiv(a.r, 16 * rm);
-    return dim3(gx, (unsigned)gy, (unsigned)lora_slots(a.T, a.L, gx * gy));
+    return dim3(gx, (unsigned)gy, (unsigned)lora_slots(a.T, a.L, gx * gy, TM));
   };
-  if (a.r <= 16) k_lora_down<KS, TM, 1><<<grid(1), 256, 0, st>>>(a);
-  else if (a.r <= 32) k_lora_down<KS, TM, 2><<<grid(2), 256, 0, st>>>(a);
-  else k_lora_down<KS, TM, 4><<<grid(4), 256, 0, st>>>(a);
+  if (a.r <= 16) k_lora_down<KS, TM, 1><<<grid(1), 512, 0, st>>>(a);
+  else if (a.r <= 32) k_lora_down<KS, TM, 2><<<grid(2), 512, 0, st>>>(a);
+  else k_lora_down<KS, TM, 4><<<grid(4), 512, 0, st>>>(a);
 }
 template <bool KS>
-static void launch_down(const LoraDown& a, hipStream_t st) { launch_down_rm<KS, 1>(a, st); }
+static void launch_down(const LoraDown& a, hipStream_t st) {
+  launch_down_rm<KS, 1>(a, st);
+}
 
+template <bool KS, int TM>
+static void launch_up_tm(const LoraUp& a, hipStream_t st) {
+  const unsigned gx = (unsigned)cdiv(a.T, 64), gy = (unsigned)cdiv(a.C, 256);
+  const dim3 grid(gx, gy, (unsigned)lora_slots(a.T, a.L, (int64_t)gx * gy, TM));
+  if (a.y_f32) k_lora_up<KS, TM, 3><<<grid, 256, 0, st>>>(a);
+  else k_lora_up<KS, TM, 2><<<grid, 256, 0, st>>>(a);
+}
 template <bool KS>
 static void launch_up(const LoraUp& a, hipStream_t st) {
-  const unsigned gx = (unsigned)cdiv(a.T, 16), gy = (unsigned)cdiv(a.C, 256);
-  const dim3 grid(gx, gy, (unsigned)lora_slots(a.T, a.L, (int64_t)gx * gy));
-  if (a.y_f32) k_lora_up<KS, 1, 3><<<grid, 256, 0, st>>>(a);
-  else k_lora_up<KS, 1, 2><<<grid, 256, 0, st>>>(a);
+  launch_up_tm<KS, 1>(a, st);
 }
 
 template <bool CR, int NP>
