@@ -40,10 +40,10 @@ struct LoraItems {
     left = __ballot(t0 + l < T && (none || id >= 0));
     list = lds;
   }
-  // The next adapter (-1: tokens without one) and up to 16 TM of its tokens: tok[j] is
-  // column 16 j + l % 16's place in the block, -1: none.
+  // The next adapter (-1: tokens without one) and the number of its tokens, up to 16 TM,
+  // whose places in the block list then holds.
   template <int TM>
-  __device__ __forceinline__ bool next(int l, int& e, int (&tok)[TM]) {
+  __device__ __forceinline__ bool next(int l, int& e, int& n) {
     if (!left) return false;
     e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
     const uint64_t m = __ballot(id == e) & left;
@@ -51,37 +51,32 @@ struct LoraItems {
     const bool mine = ((m >> l) & 1) && rank < 16 * TM;
     const uint64_t taken = __ballot(mine);
     left &= ~taken;
-    const int n = __builtin_popcountll(taken);
+    n = __builtin_popcountll(taken);
     if (mine) list[rank] = l;
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-#pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const int c = 16 * j + (l & 15);
-      tok[j] = c < n ? list[c] : -1;
-    }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     return true;
   }
 };
 
-// NP bf16 parts of eight fp32 values.  What an infinite part or a NaN leaves is nothing,
+// NP bf16 parts of V fp32 values.  What an infinite part or a NaN leaves is nothing,
 // not the NaN that subtracting it gives.
-template <int NP>
-__device__ __forceinline__ void lora_parts(float (&v)[8], v4i (&p)[NP]) {
+template <int NP, int V>
+__device__ __forceinline__ void lora_parts(float (&v)[V], uint32_t (&p)[NP][V / 2]) {
 #pragma unroll
   for (int n = 0; n < NP; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < V / 2; ++i) {
       const uint32_t w = f32x2_to_bf16x2(v[2 * i], v[2 * i + 1]);
-      p[n][i] = (int)w;
+      p[n][i] = w;
       if (n + 1 == NP) continue;
       v[2 * i] = (w & 0x7f80u) == 0x7f80u ? 0.0f : v[2 * i] - __uint_as_float(w << 16);
       v[2 * i + 1] = (w & 0x7f800000u) == 0x7f800000u ? 0.0f : v[2 * i + 1] - __uint_as_float(w & 0xffff0000u);
     }
 }
+__device__ __forceinline__ uint4 lora_pack(const uint32_t (&p)[4]) { return make_uint4(p[0], p[1], p[2], p[3]); }
 #endif
 
-constexpr int LORA_PARTS = 4;    // of a down product's sum, at most
+constexpr int LORA_PARTS = 2;    // of a down product's sum, at most
 constexpr int LORA_WAVES = 8;    // of a down workgroup
 
 // ------------------------------------------------------------------ down
@@ -96,13 +91,17 @@ struct LoraDown {
 };
 
 // A workgroup's waves take every LORA_WAVES-th 64 columns of its part; the next ones are asked
-// for while these are multiplied.
+// for while these are multiplied.  Rows come whole, 8 lanes to 128 bytes of one, and go
+// through the wave's own LDS: as the matrix core wants them, neighbouring lanes in
+// different rows, a load keeps the compute unit's address path busy four times as long
+// (2048 x 4096, rank 16: 10.4 us).
 template <bool KS, int TM, int RM>
 __global__ void __launch_bounds__(512) k_lora_down(LoraDown a) {
 #if SG_DEVICE_PASS
   constexpr int PITCH = 32 * RM + 16;   // KS: one row's ranks in LDS
-  constexpr int RED = LORA_WAVES * RM * TM * 1024, STG = KS ? LORA_WAVES * 64 * PITCH : 0;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[RED > STG ? RED : STG];
+  constexpr int W_BYTES = KS ? 64 * PITCH : 2048 * RM, WAVE = 2048 * TM + W_BYTES;
+  constexpr int RED = LORA_WAVES * RM * TM * 1024;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[RED > LORA_WAVES * WAVE ? RED : LORA_WAVES * WAVE];
   __shared__ int lists[LORA_WAVES][64];
   const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -114,67 +113,69 @@ __global__ void __launch_bounds__(512) k_lora_down(LoraDown a) {
   LoraItems items;
   items.start(a.ids, t0, a.T, a.L, l, false, lists[wave]);
   const __amdgpu_buffer_rsrc_t rz = w4_rsrc(a.z + t0 * a.ldz, (uint32_t)(((rows - 1) * a.ldz + a.C) * 2));
-  int e, tok[TM];
-  for (int d = 0; items.next<TM>(l, e, tok); ++d) {
+  uint8_t *const zl = lds + wave * WAVE, *const wl = zl + 2048 * TM;
+  const int put = (l >> 3) * 128 + (((l & 7) ^ swz8q(l >> 3)) << 4);   // of 8 rows of 128 bytes
+  int e, n;
+  for (int d = 0; items.next<TM>(l, e, n); ++d) {
     if (d % gridDim.z != blockIdx.z) continue;
     const uint16_t* const w = a.w + (int64_t)e * a.r * a.C;
     // KC: rows of ranks past r are outside; KS: its rows hold all ranks
     const __amdgpu_buffer_rsrc_t rw =
         KS ? w4_rsrc(w, (uint32_t)(a.C * a.r * 2))
            : w4_rsrc(w + (int64_t)rho0 * a.C, (uint32_t)(min(a.r - rho0, 16 * RM) * a.C * 2));
-    uint32_t zo[TM];
+    uint32_t zo[2 * TM];
 #pragma unroll
-    for (int j = 0; j < TM; ++j) zo[j] = tok[j] >= 0 ? (uint32_t)((tok[j] * a.ldz + 8 * g) * 2) : W4_OUT;
+    for (int i = 0; i < 2 * TM; ++i) {
+      const int c = 8 * i + (l >> 3);
+      zo[i] = c < n ? (uint32_t)(items.list[c] * a.ldz * 2) + 16 * (l & 7) : W4_OUT;
+    }
     v4f acc[RM][TM];
 #pragma unroll
     for (int m = 0; m < RM; ++m)
 #pragma unroll
       for (int j = 0; j < TM; ++j) acc[m][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-    v4i zf[2][TM][2], wv[2][RM][2];
+    v4i zv[2][2 * TM], wv[2][2 * RM];
     const auto load = [&](int s, int u) {
+      const bool in = 64 * u + 8 * (l & 7) < a.C;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const bool in = 64 * u + 32 * q + 8 * g < a.C;
-#pragma unroll
-        for (int j = 0; j < TM; ++j) zf[s][j][q] = w4_ld16(rz, in ? zo[j] + 64 * q : W4_OUT, u * 128);
-#pragma unroll
-        for (int m = 0; m < RM; ++m) {
-          if (KS) {   // 16 bytes c of row k; the 64 rows of 16 RM ranks are 2 RM loads
-            const int i = (2 * m + q) * 64 + l, k = i / (2 * RM), c = i % (2 * RM);
-            wv[s][m][q] = w4_ld16(rw, rho0 + 8 * c < a.r ? ((uint32_t)(64 * u + k) * a.r + rho0 + 8 * c) * 2 : W4_OUT, 0);
-          } else {
-            wv[s][m][q] = w4_ld16(rw, in ? (uint32_t)(((16 * m + lr) * a.C + 8 * g + 32 * q) * 2) : W4_OUT, u * 128);
-          }
+      for (int i = 0; i < 2 * RM; ++i) {
+        if (KS) {   // 16 bytes c of row k; the 64 rows of 16 RM ranks are 2 RM loads
+          const int k = (i * 64 + l) / (2 * RM), c = (i * 64 + l) % (2 * RM);
+          wv[s][i] = w4_ld16(rw, rho0 + 8 * c < a.r ? ((uint32_t)(64 * u + k) * a.r + rho0 + 8 * c) * 2 : W4_OUT, 0);
+        } else {
+          wv[s][i] = w4_ld16(rw, in ? (uint32_t)((8 * i + (l >> 3)) * a.C * 2 + 16 * (l & 7)) : W4_OUT, u * 128);
         }
       }
+#pragma unroll
+      for (int i = 0; i < 2 * TM; ++i) zv[s][i] = w4_ld16(rz, in ? zo[i] : W4_OUT, u * 128);
     };
     const auto compute = [&](int s) {
-      if (KS) {
-        uint8_t* const st = lds + wave * 64 * PITCH;
 #pragma unroll
-        for (int m = 0; m < RM; ++m)
+      for (int i = 0; i < 2 * RM; ++i) {
+        if (KS) *reinterpret_cast<v4i*>(wl + (i * 64 + l) / (2 * RM) * PITCH + 16 * ((i * 64 + l) % (2 * RM))) = wv[s][i];
+        else *reinterpret_cast<v4i*>(wl + 1024 * i + put) = wv[s][i];
+      }
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int i = (2 * m + q) * 64 + l;
-            *reinterpret_cast<v4i*>(st + i / (2 * RM) * PITCH + 16 * (i % (2 * RM))) = wv[s][m][q];
+      for (int i = 0; i < 2 * TM; ++i) *reinterpret_cast<v4i*>(zl + 1024 * i + put) = zv[s][i];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int at = lr * 128 + (((4 * q + g) ^ swz8q(lr)) << 4);
+        v4i zf[TM];
+#pragma unroll
+        for (int j = 0; j < TM; ++j) zf[j] = *reinterpret_cast<const v4i*>(zl + 2048 * j + at);
+#pragma unroll
+        for (int m = 0; m < RM; ++m) {
+          v4i wf;
+          if (KS) {
+            const uint8_t* const from = wl + (32 * q + 8 * g + (lr >> 2)) * PITCH + 32 * m + 8 * (lr & 3);
+            const uint2 x = lds_tr4(from), y = lds_tr4(from + 4 * PITCH);
+            wf = (v4i){(int)x.x, (int)x.y, (int)y.x, (int)y.y};
+          } else {
+            wf = *reinterpret_cast<const v4i*>(wl + 2048 * m + at);
           }
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int m = 0; m < RM; ++m) {
-            const uint8_t* const at = st + (32 * q + 8 * g + (lr >> 2)) * PITCH + 32 * m + 8 * (lr & 3);
-            const uint2 x = lds_tr4(at), y = lds_tr4(at + 4 * PITCH);
-            const v4i wf = {(int)x.x, (int)x.y, (int)y.x, (int)y.y};
-#pragma unroll
-            for (int j = 0; j < TM; ++j) acc[m][j] = w4_mfma(wf, zf[s][j][q], acc[m][j]);
-          }
-      } else {
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int m = 0; m < RM; ++m)
-#pragma unroll
-            for (int j = 0; j < TM; ++j) acc[m][j] = w4_mfma(wv[s][m][q], zf[s][j][q], acc[m][j]);
+          for (int j = 0; j < TM; ++j) acc[m][j] = w4_mfma(wf, zf[j], acc[m][j]);
+        }
       }
     };
     int u = u0 + wave;
@@ -189,23 +190,19 @@ __global__ void __launch_bounds__(512) k_lora_down(LoraDown a) {
       }
     }
     float(*const red)[RM * TM][64][4] = reinterpret_cast<float(*)[RM * TM][64][4]>(lds);
-    if (KS) __syncthreads();
+    __syncthreads();
 #pragma unroll
     for (int m = 0; m < RM; ++m)
 #pragma unroll
       for (int j = 0; j < TM; ++j) *reinterpret_cast<v4f*>(&red[wave][m * TM + j][l][0]) = acc[m][j];
     __syncthreads();
     for (int q = wave; q < RM * TM; q += LORA_WAVES) {
-      const int m = q / TM, j = q % TM;
+      const int m = q / TM, c = 16 * (q % TM) + lr, rho = rho0 + 16 * m + 4 * g;
       v4f s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < LORA_WAVES; ++k) s += *reinterpret_cast<const v4f*>(&red[k][q][l][0]);
-      int mine = -1;
-#pragma unroll
-      for (int i = 0; i < TM; ++i) mine = i == j ? tok[i] : mine;
-      const int rho = rho0 + 16 * m + 4 * g;
-      if (mine >= 0 && rho < a.r)
-        *reinterpret_cast<float4*>(a.part + ((int64_t)split * a.T + t0 + mine) * a.r + rho) =
+      if (c < n && rho < a.r)
+        *reinterpret_cast<float4*>(a.part + ((int64_t)split * a.T + t0 + items.list[c]) * a.r + rho) =
             make_float4(s[0], s[1], s[2], s[3]);
     }
     __syncthreads();
@@ -261,35 +258,30 @@ struct LoraValue {
   }
 };
 
-// Eight neighbours of base, as they are stored.
-struct LoraBase {
-  uint4 x[2];
-  __device__ __forceinline__ void load(const LoraUp& a, int64_t t, int n, bool there) {
-    x[0] = x[1] = make_uint4(0, 0, 0, 0);
-    if (a.base && there) {
-      const uint8_t* const p = reinterpret_cast<const uint8_t*>(a.base) + (t * a.ld_base + n) * (a.base_f32 ? 4 : 2);
-      x[0] = *reinterpret_cast<const uint4*>(p);
-      if (a.base_f32) x[1] = *reinterpret_cast<const uint4*>(p + 16);
-    }
-  }
-  __device__ __forceinline__ void store(const LoraUp& a, int64_t t, int n, float (&v)[8]) const {
-    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-    if (a.base) {
+// Columns n .. n + 7 of row t: v plus base, of which bf16 ones have been read.
+__device__ __forceinline__ void lora_store(const LoraUp& a, int64_t t, int n, const uint4& base, float (&v)[8]) {
+  if (a.base_f32) {
+    float x[8];
+    const float* const p = reinterpret_cast<const float*>(a.base) + t * a.ld_base + n;
+    load4(p, x);
+    load4(p + 4, x + 4);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] += __uint_as_float(a.base_f32 ? w[i] : (i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-    }
-    if (a.y_f32) {
-      float* const o = reinterpret_cast<float*>(a.y) + t * a.ldy + n;
-      *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.y) + t * a.ldy + n) =
-          make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
-                     f32x2_to_bf16x2(v[6], v[7]));
-    }
+    for (int i = 0; i < 8; ++i) v[i] += x[i];
+  } else if (a.base) {
+    const uint32_t w[4] = {base.x, base.y, base.z, base.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
   }
-};
+  if (a.y_f32) {
+    float* const o = reinterpret_cast<float*>(a.y) + t * a.ldy + n;
+    *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(o + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.y) + t * a.ldy + n) =
+        make_uint4(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
+                   f32x2_to_bf16x2(v[6], v[7]));
+  }
+}
 #endif
 
 // A workgroup's four waves take 64 columns each.
@@ -306,16 +298,22 @@ __global__ void __launch_bounds__(256) k_lora_up(LoraUp a) {
   if (n0 >= a.C) return;   // no barrier follows
   LoraItems items;
   items.start(a.ids, t0, a.T, a.L, l, a.y != a.base, lists[wave]);
-  int e, tok[TM];
-  for (int d = 0; items.next<TM>(l, e, tok); ++d) {
+  int e, count;
+  for (int d = 0; items.next<TM>(l, e, count); ++d) {
     if (d % gridDim.z != blockIdx.z) continue;
-    LoraBase base[TM][2];
+    int tok[TM];   // of column 16 j + lr, -1: none
+    uint4 base[TM][2];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) tok[j] = 16 * j + lr < count ? items.list[16 * j + lr] : -1;
 #pragma unroll
     for (int j = 0; j < TM; ++j)
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int n = n0 + 32 * q + 8 * g;
-        base[j][q].load(a, t0 + tok[j], n, tok[j] >= 0 && n < a.C);
+        base[j][q] = make_uint4(0, 0, 0, 0);
+        if (a.base && !a.base_f32 && tok[j] >= 0 && n < a.C)
+          base[j][q] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.base) +
+                                                       (t0 + tok[j]) * a.ld_base + n);
       }
     v4f acc[4][TM];
 #pragma unroll
@@ -357,12 +355,12 @@ __global__ void __launch_bounds__(256) k_lora_up(LoraUp a) {
       for (int j = 0; j < TM; ++j) {
         float v[8];
         value[j].total(scale, v);
-        v4i p[NP];
+        uint32_t p[NP][4];
         lora_parts<NP>(v, p);
 #pragma unroll
         for (int n = NP - 1; n >= 0; --n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i][j] = w4_mfma(wf[i], p[n], acc[i][j]);
+          for (int i = 0; i < 4; ++i) acc[i][j] = w4_mfma(wf[i], __builtin_bit_cast(v4i, lora_pack(p[n])), acc[i][j]);
       }
     }
 #pragma unroll
@@ -374,7 +372,7 @@ __global__ void __launch_bounds__(256) k_lora_up(LoraUp a) {
           float v[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = acc[2 * q + (i >> 2)][j][i & 3];
-          base[j][q].store(a, t0 + tok[j], n, v);
+          lora_store(a, t0 + tok[j], n, base[j][q], v);
         }
       }
   }
@@ -464,10 +462,10 @@ __global__ void __launch_bounds__(256) k_lora_sum(LoraSum a) {
       if (t < 64 * RM) {
         float v[8];
         value.total(scale, v);
-        v4i p[NP];
+        uint32_t p[NP][4];
         lora_parts<NP>(v, p);
 #pragma unroll
-        for (int q = 0; q < NP; ++q) *reinterpret_cast<v4i*>(pl + (q * 32 + vk) * PP + 16 * (t % (2 * RM))) = p[q];
+        for (int q = 0; q < NP; ++q) *reinterpret_cast<uint4*>(pl + (q * 32 + vk) * PP + 16 * (t % (2 * RM))) = lora_pack(p[q]);
       }
       uint8_t* const st = zl + wave * 32 * ZP;
 #pragma unroll
@@ -615,19 +613,26 @@ struct LoraSpace {
 template <bool KS, int TM>
 static void launch_down_rm(const LoraDown& a, hipStream_t st) {
   const unsigned gx = (unsigned)cdiv(a.T, 64);
-  const auto grid = [&](int rm) {
-    const int64_t gy = a.splits * cdiv(a.r, 16 * rm);
-    return dim3(gx, (unsigned)gy, (unsigned)lora_slots(a.T, a.L, gx * gy, TM));
-  };
-  if (a.r <= 16) k_lora_down<KS, TM, 1><<<grid(1), 512, 0, st>>>(a);
-  else if (a.r <= 32) k_lora_down<KS, TM, 2><<<grid(2), 512, 0, st>>>(a);
-  else k_lora_down<KS, TM, 4><<<grid(4), 512, 0, st>>>(a);
+  // ranks of a workgroup: more where there are many, so that z is read less often
+  const int64_t tiles = a.splits * cdiv(a.T, 16) * cdiv(a.r, 16);
+  const int rm = a.r <= 16 || tiles <= 256 ? 1 : a.r <= 32 || tiles <= 512 ? 2 : 4;
+  const int64_t gy = a.splits * cdiv(a.r, 16 * rm);
+  const dim3 grid(gx, (unsigned)gy, (unsigned)lora_slots(a.T, a.L, gx * gy, TM));
+  switch (rm) {
+    case 1: k_lora_down<KS, TM, 1><<<grid, 512, 0, st>>>(a); break;
+    case 2: k_lora_down<KS, TM, 2><<<grid, 512, 0, st>>>(a); break;
+    default: k_lora_down<KS, TM, 4><<<grid, 512, 0, st>>>(a); break;
+  }
 }
 template <bool KS>
 static void launch_down(const LoraDown& a, hipStream_t st) {
-  launch_down_rm<KS, 1>(a, st);
+  if (a.T >= 512 && a.r > 32) launch_down_rm<KS, 2>(a, st);
+  else launch_down_rm<KS, 1>(a, st);
 }
 
+#ifndef UPTM
+#define UPTM 1
+#endif
 template <bool KS, int TM>
 static void launch_up_tm(const LoraUp& a, hipStream_t st) {
   const unsigned gx = (unsigned)cdiv(a.T, 64), gy = (unsigned)cdiv(a.C, 256);
@@ -637,7 +642,8 @@ static void launch_up_tm(const LoraUp& a, hipStream_t st) {
 }
 template <bool KS>
 static void launch_up(const LoraUp& a, hipStream_t st) {
-  launch_up_tm<KS, 1>(a, st);
+  if (a.T >= 512) launch_up_tm<KS, UPTM>(a, st);
+  else launch_up_tm<KS, 1>(a, st);
 }
 
 template <bool CR, int NP>
@@ -693,10 +699,11 @@ extern "C" sg_status sg_lora_gemm(int64_t T, int64_t K, int64_t N, int r, int64_
     return SG_ERR_ALIGN;
   clear_hip_error();
   float* const part = reinterpret_cast<float*>(workspace);
-  launch_down<false>(LoraDown{T, (int)K, r, (int)L, ws.su, x, a, ldx, ids, part}, stream);
+  LoraDown q = {T, (int)K, r, (int)L, ws.su, x, a, ldx, ids, part};
   LoraUp p = {};
   p.T = T; p.C = (int)N; p.r = r; p.L = (int)L; p.splits = ws.su; p.part = part; p.scale = scale; p.ids = ids; p.w = b;
-  p.base = base; p.ld_base = ld_base; p.base_f32 = base_dt == SG_F32; p.y = y; p.ldy = ldy; p.y_f32 = y_dt == SG_F32;
+  p.base = base; p.ld_base = ld_base; p.base_f32 = base && base_dt == SG_F32; p.y = y; p.ldy = ldy; p.y_f32 = y_dt == SG_F32;
+  launch_down<false>(q, stream);
   launch_up<false>(p, stream);
   return launch_status();
 }
