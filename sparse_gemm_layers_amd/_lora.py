@@ -87,8 +87,8 @@ def lora_gemm(x, ids, a, b, scale=None, base=None, out_dtype=torch.bfloat16, y=N
     bfloat16: the shared projection's output, from any of the library's products, or
     None for 0.  y may be base: then the adapters are added in place.  fp32 sums, the
     inner product included; y is rounded once.  workspace: uint8, at least
-    lora_gemm_workspace(T, K, N, r, L) bytes (allocated if not given; keep it to one
-    stream)."""
+    lora_gemm_workspace(T, K, N, r, L) bytes where that is not 0 (allocated if not
+    given; keep it to one stream)."""
     T, K, N, r, L, ldx, pi, pa, pb, ps = _adapters(x, ids, a, b, scale)
     dev = x.device
     ldb = 0 if base is None else _result(base, "base", _FB, (T, N), dev)
@@ -99,11 +99,13 @@ def lora_gemm(x, ids, a, b, scale=None, base=None, out_dtype=torch.bfloat16, y=N
         ldy = N
     else:
         ldy = _result(y, "y", _FB, (T, N), dev)
-    workspace = _space(workspace, _need(False, T, K, N, r, L), x)
+    need, pw, wn = _need(False, T, K, N, r, L), None, 0
+    if need:
+        workspace = _space(workspace, need, x)
+        pw, wn = workspace.data_ptr(), workspace.numel()
     st = _lib().sg_lora_gemm(T, K, N, r, L, x.data_ptr(), ldx, pi, pa, pb, ps,
                              None if base is None else base.data_ptr(), 0 if base is None else _CODE[base.dtype], ldb,
-                             y.data_ptr(), _CODE[y.dtype], ldy, workspace.data_ptr(), workspace.numel(),
-                             _current_stream(x))
+                             y.data_ptr(), _CODE[y.dtype], ldy, pw, wn, _current_stream(x))
     if st:
         _check(st, "sg_lora_gemm")
     return y

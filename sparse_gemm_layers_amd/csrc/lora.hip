@@ -96,17 +96,19 @@ struct LoraDown {
 // different rows, a load keeps the compute unit's address path busy four times as long
 // (2048 x 4096, rank 16: 10.4 us).
 template <bool KS, int TM, int RM>
-__global__ void __launch_bounds__(512) k_lora_down(LoraDown a) {
+struct LoraDownLds {
+  static constexpr int PITCH = 32 * RM + 16;   // KS: one row's ranks
+  static constexpr int WAVE = 2048 * TM + (KS ? 64 * PITCH : 2048 * RM), RED = LORA_WAVES * RM * TM * 1024;
+  static constexpr int BYTES = RED > LORA_WAVES * WAVE ? RED : LORA_WAVES * WAVE;
+};
 #if SG_DEVICE_PASS
-  constexpr int PITCH = 32 * RM + 16;   // KS: one row's ranks in LDS
-  constexpr int W_BYTES = KS ? 64 * PITCH : 2048 * RM, WAVE = 2048 * TM + W_BYTES;
-  constexpr int RED = LORA_WAVES * RM * TM * 1024;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[RED > LORA_WAVES * WAVE ? RED : LORA_WAVES * WAVE];
-  __shared__ int lists[LORA_WAVES][64];
+template <bool KS, int TM, int RM>
+__device__ __forceinline__ void lora_down(const LoraDown& a, uint8_t* lds, int (*lists)[64], int by) {
+  constexpr int PITCH = LoraDownLds<KS, TM, RM>::PITCH, WAVE = LoraDownLds<KS, TM, RM>::WAVE;
   const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int64_t t0 = (int64_t)blockIdx.x * 64;
-  const int split = blockIdx.y % a.splits, rho0 = (int)(blockIdx.y / a.splits) * 16 * RM;
+  const int split = by % a.splits, rho0 = by / a.splits * 16 * RM;
   const int rows = (int)min((int64_t)64, a.T - t0);
   const int units = (a.C + 63) >> 6;   // of 64 columns
   const int u0 = (int)((int64_t)units * split / a.splits), u1 = (int)((int64_t)units * (split + 1) / a.splits);
@@ -207,7 +209,27 @@ __global__ void __launch_bounds__(512) k_lora_down(LoraDown a) {
     }
     __syncthreads();
   }
+}
 #endif  // SG_DEVICE_PASS
+
+template <bool KS, int TM, int RM>
+__global__ void __launch_bounds__(512) k_lora_down(LoraDown a) {
+#if SG_DEVICE_PASS
+  __shared__ __attribute__((aligned(16))) uint8_t lds[LoraDownLds<KS, TM, RM>::BYTES];
+  __shared__ int lists[LORA_WAVES][64];
+  lora_down<KS, TM, RM>(a, lds, lists, blockIdx.y);
+#endif
+}
+
+// Both of the backward pass: v's workgroups come first along y, then u's.
+template <int TM, int RM>
+__global__ void __launch_bounds__(512) k_lora_down_two(LoraDown v, LoraDown u, int v_y) {
+#if SG_DEVICE_PASS
+  __shared__ __attribute__((aligned(16))) uint8_t lds[LoraDownLds<true, TM, RM>::BYTES];   // the larger
+  __shared__ int lists[LORA_WAVES][64];
+  if ((int)blockIdx.y < v_y) lora_down<true, TM, RM>(v, lds, lists, blockIdx.y);
+  else lora_down<false, TM, RM>(u, lds, lists, blockIdx.y - v_y);
+#endif
 }
 
 // ------------------------------------------------------------------ up
@@ -379,6 +401,188 @@ __global__ void __launch_bounds__(256) k_lora_up(LoraUp a) {
 #endif  // SG_DEVICE_PASS
 }
 
+// ------------------------------------------------------------------ both at once
+
+// Down and up in one launch, for few tokens with short adapters (lora_both), where a second
+// launch costs more than that every workgroup goes through the whole of an adapter's
+// down part: it takes an item of 16 tokens at a time and a slice of the columns.  Its
+// waves split the long sum and add it in LDS, where it stays as the other product's
+// operand; then they take 64 columns each.  (One token, 4096 x 4096, rank 16: 7.4 us, two
+// launches 8.6 and a gap; but 2048 tokens 28 us for 20, and 37 of 16 adapters of rank 64
+// beside 14336 columns 35 us for 19.)
+struct LoraBoth {
+  LoraDown d;
+  LoraUp u;
+  int slice;       // columns of one workgroup, a multiple of 64
+};
+
+template <int RM, int NP>
+__global__ void __launch_bounds__(512) k_lora_both(LoraBoth b) {
+#if SG_DEVICE_PASS
+  constexpr int RC = 16 * RM, WL = 2 * RM, DEPTH = RM == 1 ? 4 : RM == 2 ? 2 : 1;
+  constexpr int PP = 2 * RC + 16, OP = 256 + 16;           // pitches of ranks, of one token's results
+  constexpr int D_BYTES = 2048 + 2048 * RM, U_BYTES = 64 * PP;
+  constexpr int WAVE0 = D_BYTES > U_BYTES ? D_BYTES : U_BYTES, WAVE = WAVE0 > 16 * OP ? WAVE0 : 16 * OP;
+  constexpr int RED = LORA_WAVES * RM * 1024;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[RED > LORA_WAVES * WAVE ? RED : LORA_WAVES * WAVE], pl[NP * 16 * PP];
+  __shared__ int lists[LORA_WAVES][64];
+  const LoraDown& a = b.d;
+  const LoraUp& y = b.u;
+  const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int64_t t0 = (int64_t)blockIdx.x * 64;
+  const int rows = (int)min((int64_t)64, a.T - t0);
+  const int units = (a.C + 63) >> 6;
+  const int s0 = blockIdx.y * b.slice, s1 = min(s0 + b.slice, y.C);
+  LoraItems items;
+  items.start(a.ids, t0, a.T, a.L, l, y.y != y.base, lists[wave]);
+  const __amdgpu_buffer_rsrc_t rz = w4_rsrc(a.z + t0 * a.ldz, (uint32_t)(((rows - 1) * a.ldz + a.C) * 2));
+  uint8_t *const zl = lds + wave * WAVE, *const wl = zl + 2048;
+  const int put = (l >> 3) * 128 + (((l & 7) ^ swz8q(l >> 3)) << 4);   // of 8 rows of 128 bytes
+  int e, n;
+  for (int d = 0; items.next<1>(l, e, n); ++d) {
+    if (d % gridDim.z != blockIdx.z) continue;
+    const int place0 = items.list[l >> 3], place1 = items.list[8 + (l >> 3)];   // of the lane's pieces of rows
+    // what the second product reads of memory: adapter rows and base of 64 columns
+    const __amdgpu_buffer_rsrc_t r2 = w4_rsrc(y.w + (int64_t)e * a.r * y.C, e >= 0 ? (uint32_t)(a.r * y.C * 2) : 0u);
+    v4i uv[WL];
+    uint4 base[2];
+    const auto load_up = [&](int n0) {
+      const int col = n0 + 8 * (l & 7);
+#pragma unroll
+      for (int i = 0; i < WL; ++i) {
+        const int c = n0 + (64 * i + l) / WL, k = 8 * ((64 * i + l) % WL);
+        uv[i] = w4_ld16(r2, c < s1 && k < a.r ? (uint32_t)((c * a.r + k) * 2) : W4_OUT, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        base[i] = make_uint4(0, 0, 0, 0);
+        if (y.base && !y.base_f32 && 8 * i + (l >> 3) < n && col < s1)
+          base[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(y.base) +
+                                                    (t0 + (i ? place1 : place0)) * y.ld_base + col);
+      }
+    };
+    if (e >= 0) {
+      const uint16_t* const w = a.w + (int64_t)e * a.r * a.C;
+      const __amdgpu_buffer_rsrc_t rw = w4_rsrc(w, (uint32_t)(a.C * a.r * 2));   // rows of ranks past r are outside
+      const uint32_t zo0 = (l >> 3) < n ? (uint32_t)(place0 * a.ldz * 2) + 16 * (l & 7) : W4_OUT;
+      const uint32_t zo1 = 8 + (l >> 3) < n ? (uint32_t)(place1 * a.ldz * 2) + 16 * (l & 7) : W4_OUT;
+      v4f acc[RM];
+#pragma unroll
+      for (int m = 0; m < RM; ++m) acc[m] = (v4f){0.f, 0.f, 0.f, 0.f};
+      v4i zv[DEPTH][2], wv[DEPTH][2 * RM];
+      const auto load = [&](int s, int u) {
+        const bool in = 64 * u + 8 * (l & 7) < a.C;
+#pragma unroll
+        for (int i = 0; i < 2 * RM; ++i) {
+          wv[s][i] = w4_ld16(rw, in ? (uint32_t)((8 * i + (l >> 3)) * a.C * 2 + 16 * (l & 7)) : W4_OUT, u * 128);
+        }
+        zv[s][0] = w4_ld16(rz, in ? zo0 : W4_OUT, u * 128);
+        zv[s][1] = w4_ld16(rz, in ? zo1 : W4_OUT, u * 128);
+      };
+      const auto compute = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < 2 * RM; ++i) {
+          *reinterpret_cast<v4i*>(wl + 1024 * i + put) = wv[s][i];
+        }
+        *reinterpret_cast<v4i*>(zl + put) = zv[s][0];
+        *reinterpret_cast<v4i*>(zl + 1024 + put) = zv[s][1];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int at = lr * 128 + (((4 * q + g) ^ swz8q(lr)) << 4);
+          const v4i zf = *reinterpret_cast<const v4i*>(zl + at);
+#pragma unroll
+          for (int m = 0; m < RM; ++m) {
+            acc[m] = w4_mfma(*reinterpret_cast<const v4i*>(wl + 2048 * m + at), zf, acc[m]);
+          }
+        }
+      };
+#pragma unroll
+      for (int s = 0; s < DEPTH; ++s)
+        if (wave + s * LORA_WAVES < units) load(s, wave + s * LORA_WAVES);
+      for (int u = wave; u < units; u += DEPTH * LORA_WAVES) {
+#pragma unroll
+        for (int s = 0; s < DEPTH; ++s) {
+          if (u + s * LORA_WAVES >= units) break;
+          compute(s);
+          if (u + (s + DEPTH) * LORA_WAVES < units) load(s, u + (s + DEPTH) * LORA_WAVES);
+        }
+      }
+      if (s0 + 64 * wave < s1) load_up(s0 + 64 * wave);
+      float(*const red)[RM][64][4] = reinterpret_cast<float(*)[RM][64][4]>(lds);
+      __syncthreads();
+#pragma unroll
+      for (int m = 0; m < RM; ++m) *reinterpret_cast<v4f*>(&red[wave][m][l][0]) = acc[m];
+      __syncthreads();
+      if (wave < RM) {
+        v4f s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < LORA_WAVES; ++k) s += *reinterpret_cast<const v4f*>(&red[k][wave][l][0]);
+        const int rho = 16 * wave + 4 * g;
+        const float scale = y.scale ? y.scale[e] : 1.0f;
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = s[k] * scale;
+        uint32_t p[NP][2];
+        lora_parts<NP>(v, p);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) *reinterpret_cast<uint2*>(pl + (q * 16 + lr) * PP + 2 * rho) = make_uint2(p[q][0], p[q][1]);
+      }
+      __syncthreads();
+    } else if (s0 + 64 * wave < s1) {
+      load_up(s0 + 64 * wave);
+    }
+    for (int n0 = s0 + 64 * wave; n0 < s1; n0 += 64 * LORA_WAVES) {
+      const int col = n0 + 8 * (l & 7);
+      v4f acc[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] = (v4f){0.f, 0.f, 0.f, 0.f};
+      const uint4 base0 = base[0], base1 = base[1];
+      if (e >= 0) {
+#pragma unroll
+        for (int i = 0; i < WL; ++i) {
+          *reinterpret_cast<v4i*>(zl + (64 * i + l) / WL * PP + 16 * ((64 * i + l) % WL)) = uv[i];
+        }
+      }
+      if (n0 + 64 * LORA_WAVES < s1) load_up(n0 + 64 * LORA_WAVES);
+      if (e >= 0) {
+#pragma unroll
+        for (int k = 0; k < RC; k += 32) {
+          const bool in = k + 8 * g < RC;   // a step of 32 ranks, of which 16 may be all
+          v4i pf[NP];
+#pragma unroll
+          for (int q = 0; q < NP; ++q) {
+            pf[q] = (v4i){0, 0, 0, 0};
+            if (in) pf[q] = *reinterpret_cast<const v4i*>(pl + (q * 16 + lr) * PP + 2 * (k + 8 * g));
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            v4i wf = {0, 0, 0, 0};
+            if (in) wf = *reinterpret_cast<const v4i*>(zl + (16 * i + lr) * PP + 2 * (k + 8 * g));
+#pragma unroll
+            for (int q = NP - 1; q >= 0; --q) acc[i] = w4_mfma(wf, pf[q], acc[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<v4f*>(zl + lr * OP + 4 * (16 * i + 4 * g)) = acc[i];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint8_t* const from = zl + (8 * i + (l >> 3)) * OP + 32 * (l & 7);
+        const v4f x = *reinterpret_cast<const v4f*>(from), z = *reinterpret_cast<const v4f*>(from + 16);
+        if (8 * i + (l >> 3) < n && col < s1) {
+          float v[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = x[k], v[4 + k] = z[k];
+          lora_store(y, t0 + (i ? place1 : place0), col, i ? base1 : base0, v);
+        }
+      }
+    }
+    __syncthreads();   // the next item's sum goes where the last results went
+  }
+#endif  // SG_DEVICE_PASS
+}
+
 // ------------------------------------------------------------------ sums over tokens
 
 [[maybe_unused]] constexpr int LORA_LIST = 1024;   // tokens looked through at a time
@@ -399,17 +603,23 @@ struct LoraSum {
 
 // Adapter blockIdx.y's sum over its tokens in range blockIdx.z, columns of 64 a wave.  CR:
 // results are [C][r] (dB), else [r][C] (dA).
-template <bool CR, int RM, int NP>
-__global__ void __launch_bounds__(256) k_lora_sum(LoraSum a) {
+template <int RM, int NP>
+struct LoraSumLds {
+  static constexpr int PP = 32 * RM + 16, ZP = 128 + 16;   // pitches of one token's ranks and columns
+  uint8_t pl[NP * 32 * PP], zl[4 * 32 * ZP];
+  int list[LORA_LIST], count[4];
+};
 #if SG_DEVICE_PASS
-  constexpr int PP = 32 * RM + 16, ZP = 128 + 16;   // pitches of one token's ranks and columns
-  __shared__ __attribute__((aligned(16))) uint8_t pl[NP * 32 * PP], zl[4 * 32 * ZP];
-  __shared__ int list[LORA_LIST], count[4];
+template <bool CR, int RM, int NP>
+__device__ __forceinline__ void lora_sum(const LoraSum& a, LoraSumLds<RM, NP>& lds, int bx) {
+  constexpr int PP = LoraSumLds<RM, NP>::PP, ZP = LoraSumLds<RM, NP>::ZP;
+  uint8_t *const pl = lds.pl, *const zl = lds.zl;
+  int *const list = lds.list, *const count = lds.count;
   const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int chunks = (a.r + 16 * RM - 1) / (16 * RM);
   const int e = blockIdx.y / chunks, rho0 = (int)(blockIdx.y % chunks) * 16 * RM;
-  const int n0 = (blockIdx.x * 4 + wave) * 64;
+  const int n0 = (bx * 4 + wave) * 64;
   const int64_t b0 = a.T * blockIdx.z / a.tsplits, b1 = a.T * (blockIdx.z + 1) / a.tsplits;
   const float scale = a.scale ? a.scale[e] : 1.0f;
   v4f acc[4][RM];
@@ -530,7 +740,17 @@ __global__ void __launch_bounds__(256) k_lora_sum(LoraSum a) {
         }
       }
   }
+}
 #endif  // SG_DEVICE_PASS
+
+// dA's workgroups come first along x, then dB's.
+template <int RM, int NP>
+__global__ void __launch_bounds__(256) k_lora_sum(LoraSum a, LoraSum b, int a_x) {
+#if SG_DEVICE_PASS
+  __shared__ __attribute__((aligned(16))) LoraSumLds<RM, NP> lds;
+  if ((int)blockIdx.x < a_x) lora_sum<false, RM, NP>(a, lds, blockIdx.x);
+  else lora_sum<true, RM, NP>(b, lds, blockIdx.x - a_x);
+#endif
 }
 
 // The parts of both gradients, added in order.  n: values of one part, of dA then dB.
@@ -610,29 +830,35 @@ struct LoraSpace {
   }
 };
 
-template <bool KS, int TM>
-static void launch_down_rm(const LoraDown& a, hipStream_t st) {
-  const unsigned gx = (unsigned)cdiv(a.T, 64);
-  // ranks of a workgroup: more where there are many, so that z is read less often
-  const int64_t tiles = a.splits * cdiv(a.T, 16) * cdiv(a.r, 16);
-  const int rm = a.r <= 16 || tiles <= 256 ? 1 : a.r <= 32 || tiles <= 512 ? 2 : 4;
-  const int64_t gy = a.splits * cdiv(a.r, 16 * rm);
-  const dim3 grid(gx, (unsigned)gy, (unsigned)lora_slots(a.T, a.L, gx * gy, TM));
-  switch (rm) {
-    case 1: k_lora_down<KS, TM, 1><<<grid, 512, 0, st>>>(a); break;
-    case 2: k_lora_down<KS, TM, 2><<<grid, 512, 0, st>>>(a); break;
-    default: k_lora_down<KS, TM, 4><<<grid, 512, 0, st>>>(a); break;
+// Ranks of a down workgroup in 16s: more where there are many, so that z is read less often.
+static int lora_rm(int64_t T, int64_t r, int splits) {
+  const int64_t tiles = splits * cdiv(T, 16) * cdiv(r, 16);
+  return r <= 16 || tiles <= 256 ? 1 : r <= 32 || tiles <= 512 ? 2 : 4;
+}
+template <int TM, int RM>
+static void launch_down_tm(const LoraDown* v, const LoraDown* u, hipStream_t st) {
+  const LoraDown& a = v ? *v : *u;
+  const unsigned gx = (unsigned)cdiv(a.T, 64), chunks = (unsigned)cdiv(a.r, 16 * RM);
+  const unsigned gv = v ? v->splits * chunks : 0, gu = u ? u->splits * chunks : 0;
+  const dim3 grid(gx, gv + gu, (unsigned)lora_slots(a.T, a.L, (int64_t)gx * (gv + gu), TM));
+  if (v && u) k_lora_down_two<TM, RM><<<grid, 512, 0, st>>>(*v, *u, (int)gv);
+  else if (v) k_lora_down<true, TM, RM><<<grid, 512, 0, st>>>(*v);
+  else k_lora_down<false, TM, RM><<<grid, 512, 0, st>>>(*u);
+}
+// dy . B (v) and x . A^T (u), either or both.
+static void launch_down(const LoraDown* v, const LoraDown* u, hipStream_t st) {
+  const LoraDown& a = v ? *v : *u;
+  const int rm = lora_rm(a.T, a.r, a.splits);
+  if (a.T >= 512 && a.r > 32) {
+    if (rm <= 2) launch_down_tm<2, 2>(v, u, st);
+    else launch_down_tm<2, 4>(v, u, st);
+  } else {
+    if (rm == 1) launch_down_tm<1, 1>(v, u, st);
+    else if (rm == 2) launch_down_tm<1, 2>(v, u, st);
+    else launch_down_tm<1, 4>(v, u, st);
   }
 }
-template <bool KS>
-static void launch_down(const LoraDown& a, hipStream_t st) {
-  if (a.T >= 512 && a.r > 32) launch_down_rm<KS, 2>(a, st);
-  else launch_down_rm<KS, 1>(a, st);
-}
 
-#ifndef UPTM
-#define UPTM 1
-#endif
 template <bool KS, int TM>
 static void launch_up_tm(const LoraUp& a, hipStream_t st) {
   const unsigned gx = (unsigned)cdiv(a.T, 64), gy = (unsigned)cdiv(a.C, 256);
@@ -642,23 +868,35 @@ static void launch_up_tm(const LoraUp& a, hipStream_t st) {
 }
 template <bool KS>
 static void launch_up(const LoraUp& a, hipStream_t st) {
-  if (a.T >= 512) launch_up_tm<KS, UPTM>(a, st);
-  else launch_up_tm<KS, 1>(a, st);
+  launch_up_tm<KS, 1>(a, st);
 }
 
-template <bool CR, int NP>
-static void launch_sum_np(const LoraSum& a, hipStream_t st) {
-  const auto grid = [&](int rm) {
-    return dim3((unsigned)cdiv(a.C, 256), (unsigned)(a.L * cdiv(a.r, 16 * rm)), (unsigned)a.tsplits);
-  };
-  if (a.r <= 16) k_lora_sum<CR, 1, NP><<<grid(1), 256, 0, st>>>(a);
-  else if (a.r <= 32) k_lora_sum<CR, 2, NP><<<grid(2), 256, 0, st>>>(a);
-  else k_lora_sum<CR, 4, NP><<<grid(4), 256, 0, st>>>(a);
+template <int NP>
+static void launch_sum(const LoraSum& a, const LoraSum& b, hipStream_t st) {
+  const unsigned ax = (unsigned)cdiv(a.C, 256), bx = (unsigned)cdiv(b.C, 256);
+  const auto grid = [&](int rm) { return dim3(ax + bx, (unsigned)(a.L * cdiv(a.r, 16 * rm)), (unsigned)a.tsplits); };
+  if (a.r <= 16) k_lora_sum<1, NP><<<grid(1), 256, 0, st>>>(a, b, (int)ax);
+  else if (a.r <= 32) k_lora_sum<2, NP><<<grid(2), 256, 0, st>>>(a, b, (int)ax);
+  else k_lora_sum<4, NP><<<grid(4), 256, 0, st>>>(a, b, (int)ax);
 }
-template <bool CR>
-static void launch_sum(const LoraSum& a, hipStream_t st) {
-  if (a.out_f32) launch_sum_np<CR, 3>(a, st);
-  else launch_sum_np<CR, 2>(a, st);
+
+// Whether a call's two products go in one launch.
+static bool lora_both(int64_t T, int64_t C, int64_t r) { return T <= 64 && r <= 64 && 2 * C * r <= 256 * 1024; }
+
+template <int RM>
+static void launch_both_rm(const LoraBoth& b, dim3 grid, hipStream_t st) {
+  if (b.u.y_f32) k_lora_both<RM, 3><<<grid, 512, 0, st>>>(b);
+  else k_lora_both<RM, 2><<<grid, 512, 0, st>>>(b);
+}
+static void launch_both(LoraBoth b, hipStream_t st) {
+  const int64_t T = b.d.T, items = (b.d.L < T ? b.d.L : T) + T / 16;
+  int64_t slices = 256 / items, most = cdiv(b.u.C, 64 * LORA_WAVES);
+  slices = slices < 1 ? 1 : slices > most ? most : slices;
+  b.slice = (int)cdiv(cdiv(b.u.C, 64), slices) * 64;
+  const dim3 grid((unsigned)cdiv(T, 64), (unsigned)cdiv(b.u.C, b.slice), (unsigned)items);
+  if (b.d.r <= 16) launch_both_rm<1>(b, grid, st);
+  else if (b.d.r <= 32) launch_both_rm<2>(b, grid, st);
+  else launch_both_rm<4>(b, grid, st);
 }
 
 static bool lora_shape_ok(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
@@ -674,7 +912,7 @@ using namespace sg;
 
 extern "C" int64_t sg_lora_gemm_workspace(int64_t T, int64_t K, int64_t N, int r, int64_t L) {
   if (!lora_shape_ok(T, K, N, r, L)) return -1;
-  return LoraSpace(T, K, N, r, L, false).bytes;
+  return lora_both(T, K, r) ? 0 : LoraSpace(T, K, N, r, L, false).bytes;
 }
 
 extern "C" int64_t sg_lora_gemm_backward_workspace(int64_t T, int64_t K, int64_t N, int r, int64_t L) {
@@ -686,16 +924,19 @@ extern "C" sg_status sg_lora_gemm(int64_t T, int64_t K, int64_t N, int r, int64_
                                   const int32_t* ids, const uint16_t* a, const uint16_t* b, const float* scale,
                                   const void* base, sg_dtype base_dt, int64_t ld_base, void* y, sg_dtype y_dt,
                                   int64_t ldy, void* workspace, int64_t workspace_bytes, hipStream_t stream) {
-  if (!x || !a || !b || !y || !workspace) return SG_ERR_NULL;
+  if (!x || !a || !b || !y) return SG_ERR_NULL;
   if ((y_dt != SG_F32 && y_dt != SG_BF16) || (base && base_dt != SG_F32 && base_dt != SG_BF16))
     return SG_ERR_UNSUPPORTED;
   if (!lora_shape_ok(T, K, N, r, L) || !lora_ld_ok(ldx, K) || !lora_ld_ok(ldy, N) ||
       (base && !lora_ld_ok(ld_base, N)) || (base == y && (base_dt != y_dt || ld_base != ldy)))
     return SG_ERR_SHAPE;
   const LoraSpace ws(T, K, N, r, L, false);
-  if (workspace_bytes < ws.bytes) return SG_ERR_SHAPE;
+  const bool both = lora_both(T, K, r);
+  if (!both && !workspace) return SG_ERR_NULL;
+  if (!both && workspace_bytes < ws.bytes) return SG_ERR_SHAPE;
   if (ldx % 8 || ldy % 8 || (base && ld_base % 8) || !aligned(x, 16) || !aligned(ids, 4) || !aligned(a, 16) ||
-      !aligned(b, 16) || !aligned(scale, 4) || !aligned(base, 16) || !aligned(y, 16) || !aligned(workspace, 256))
+      !aligned(b, 16) || !aligned(scale, 4) || !aligned(base, 16) || !aligned(y, 16) ||
+      (!both && !aligned(workspace, 256)))
     return SG_ERR_ALIGN;
   clear_hip_error();
   float* const part = reinterpret_cast<float*>(workspace);
@@ -703,8 +944,12 @@ extern "C" sg_status sg_lora_gemm(int64_t T, int64_t K, int64_t N, int r, int64_
   LoraUp p = {};
   p.T = T; p.C = (int)N; p.r = r; p.L = (int)L; p.splits = ws.su; p.part = part; p.scale = scale; p.ids = ids; p.w = b;
   p.base = base; p.ld_base = ld_base; p.base_f32 = base && base_dt == SG_F32; p.y = y; p.ldy = ldy; p.y_f32 = y_dt == SG_F32;
-  launch_down<false>(q, stream);
-  launch_up<false>(p, stream);
+  if (both) {
+    launch_both(LoraBoth{q, p, 0}, stream);
+  } else {
+    launch_down(nullptr, &q, stream);
+    launch_up<false>(p, stream);
+  }
   return launch_status();
 }
 
@@ -728,8 +973,8 @@ extern "C" sg_status sg_lora_gemm_backward(int64_t T, int64_t K, int64_t N, int 
   clear_hip_error();
   uint8_t* const w = reinterpret_cast<uint8_t*>(workspace);
   float *const u = reinterpret_cast<float*>(w + ws.u), *const v = reinterpret_cast<float*>(w + ws.v);
-  launch_down<true>(LoraDown{T, (int)N, r, (int)L, ws.sv, dy, b, ld_dy, ids, v}, stream);
-  if (da) launch_down<false>(LoraDown{T, (int)K, r, (int)L, ws.su, x, a, ldx, ids, u}, stream);
+  const LoraDown dv = {T, (int)N, r, (int)L, ws.sv, dy, b, ld_dy, ids, v}, du = {T, (int)K, r, (int)L, ws.su, x, a, ldx, ids, u};
+  launch_down(&dv, da ? &du : nullptr, stream);
   if (dx) {
     LoraUp p = {};
     p.T = T; p.C = (int)K; p.r = r; p.L = (int)L; p.splits = ws.sv; p.part = v; p.scale = scale; p.ids = ids; p.w = a;
@@ -741,10 +986,11 @@ extern "C" sg_status sg_lora_gemm_backward(int64_t T, int64_t K, int64_t N, int 
     s.T = T; s.C = (int)K; s.r = r; s.L = (int)L; s.splits = ws.sv; s.z = x; s.ldz = ldx; s.part = v; s.scale = scale;
     s.ids = ids; s.tsplits = ws.ts; s.sums = reinterpret_cast<float*>(w + ws.sa); s.out = da;
     s.out_f32 = grad_dt == SG_F32;
-    launch_sum<false>(s, stream);
-    s.C = (int)N; s.splits = ws.su; s.z = dy; s.ldz = ld_dy; s.part = u; s.sums = reinterpret_cast<float*>(w + ws.sb);
-    s.out = db;
-    launch_sum<true>(s, stream);
+    LoraSum q = s;
+    q.C = (int)N; q.splits = ws.su; q.z = dy; q.ldz = ld_dy; q.part = u; q.sums = reinterpret_cast<float*>(w + ws.sb);
+    q.out = db;
+    if (s.out_f32) launch_sum<3>(s, q, stream);
+    else launch_sum<2>(s, q, stream);
     if (ws.ts > 1) {
       LoraJoin j = {};
       j.sums[0] = reinterpret_cast<float*>(w + ws.sa); j.sums[1] = reinterpret_cast<float*>(w + ws.sb);

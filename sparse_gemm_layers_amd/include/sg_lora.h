@@ -30,8 +30,9 @@ extern "C" {
  *   base  : SG_F32 or SG_BF16 [T, N], leading dim ld_base, or NULL: 0; may be y itself
  *           (same type and leading dim)
  *   y     : SG_F32 or SG_BF16 [T, N], leading dim ldy
- *   workspace : at least sg_lora_gemm_workspace(T, K, N, r, L) bytes, 256-byte
- *           aligned, in use until the work on `stream` is done
+ *   workspace : at least sg_lora_gemm_workspace(T, K, N, r, L) bytes (0: none),
+ *           256-byte aligned, in use until the work on `stream` is done
+ * No output may overlap an input, but for y that is base.
  * Requires K, N and r multiples of 8, r <= 256, K and N under 2^22, L <= 65535, leading
  * dims at least the row, multiples of 8 and under 2^22, T < 2^22; all arrays 16-byte
  * aligned (ids and scale 4).
@@ -58,6 +59,7 @@ sg_status sg_lora_gemm(int64_t T, int64_t K, int64_t N, int r, int64_t L, const 
  *   dx   : bf16 [T, K], leading dim ld_dx, or NULL;  da, db: SG_F32 or SG_BF16 of
  *          the shapes of a and b, contiguous, or both NULL
  *   workspace : at least sg_lora_gemm_backward_workspace(T, K, N, r, L) bytes, as above
+ * No output may overlap an input, but for dx that is base.
  * Requires what sg_lora_gemm does.
  */
 int64_t sg_lora_gemm_backward_workspace(int64_t T, int64_t K, int64_t N, int r, int64_t L);

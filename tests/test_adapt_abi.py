@@ -92,7 +92,7 @@ def test_gated_backward_checks_its_workspace():
     assert call(_gated, "sg_gated_gemm_backward", GATED_BACK, dict(size, ws=ODD)) == ALIGN
 
 
-LORA = dict(T=3, K=40, N=48, r=16, L=5, x=P[0], ldx=40, ids=P[1], a=P[2], b=P[3], scale=P[4], base=P[5], bdt=1, ldb=48, y=P[6],
+LORA = dict(T=100, K=40, N=48, r=16, L=5, x=P[0], ldx=40, ids=P[1], a=P[2], b=P[3], scale=P[4], base=P[5], bdt=1, ldb=48, y=P[6],
             dt=0, ldy=48, ws=P[7], wsb=1 << 40, st=None)
 LORA_SHARED = [
     *[({n: None}, NULL) for n in ("x", "a", "b", "ws")],
@@ -130,13 +130,13 @@ def test_lora_backward_refusals(kw, code):
 
 
 def test_lora_workspaces():
+    assert sg.lora_gemm_workspace(1, 4096, 4096, 16, 8) == 0 and sg.lora_gemm_backward_workspace(1, 4096, 4096, 16, 8) > 0
     for need in (sg.lora_gemm_workspace, sg.lora_gemm_backward_workspace):
-        assert need(1, 4096, 4096, 16, 8) > 0
         assert need(70000, 64, 64, 16, 1) >= 4 * 70000 * 16
         for bad in ((0, 8, 8, 8, 1), (1, 4, 8, 8, 1), (1, 8, 12, 8, 1), (1, 8, 8, 4, 1), (1, 8, 8, 264, 1), (1, 8, 8, 8, 0),
                     (1, 8, 8, 8, 65536), (BIG, 8, 8, 8, 1), (1, BIG, 8, 8, 1)):
             assert need(*bad) == -1
-    assert sg.lora_gemm_backward_workspace(64, 64, 64, 16, 1) > sg.lora_gemm_workspace(64, 64, 64, 16, 1)
+    assert sg.lora_gemm_backward_workspace(80, 64, 64, 16, 1) > sg.lora_gemm_workspace(80, 64, 64, 16, 1) > 0
 
 
 @pytest.mark.parametrize("call", [
