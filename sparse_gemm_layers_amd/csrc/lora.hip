@@ -307,22 +307,28 @@ __device__ __forceinline__ void lora_store(const LoraUp& a, int64_t t, int n, co
 #endif
 
 // A workgroup's four waves take 64 columns each.
-template <bool KS, int TM, int NP>
-__global__ void __launch_bounds__(256) k_lora_up(LoraUp a) {
+template <bool KS>
+struct LoraUpLds {
+  static constexpr int PITCH = 128 + 16;   // KS: 64 columns of one rank
+  uint8_t w[KS ? 4 * 32 * PITCH : 16];
+  int lists[4][64];
+};
 #if SG_DEVICE_PASS
-  constexpr int PITCH = 128 + 16;   // KS: 64 columns of one rank in LDS
-  __shared__ __attribute__((aligned(16))) uint8_t lds[KS ? 4 * 32 * PITCH : 16];
-  __shared__ int lists[4][64];
+// bx, by, bz: the workgroup's block of tokens, its columns, its share gz-th of the items
+template <bool KS, int NP>
+__device__ __forceinline__ void lora_up(const LoraUp& a, LoraUpLds<KS>& shared, int bx, int by, int bz, int gz) {
+  constexpr int TM = 1, PITCH = LoraUpLds<KS>::PITCH;
+  uint8_t* const lds = shared.w;
   const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int64_t t0 = (int64_t)blockIdx.x * 64;
-  const int n0 = (blockIdx.y * 4 + wave) * 64;
+  const int64_t t0 = (int64_t)bx * 64;
+  const int n0 = (by * 4 + wave) * 64;
   if (n0 >= a.C) return;   // no barrier follows
   LoraItems items;
-  items.start(a.ids, t0, a.T, a.L, l, a.y != a.base, lists[wave]);
+  items.start(a.ids, t0, a.T, a.L, l, a.y != a.base, shared.lists[wave]);
   int e, count;
   for (int d = 0; items.next<TM>(l, e, count); ++d) {
-    if (d % gridDim.z != blockIdx.z) continue;
+    if (d % gz != bz) continue;
     int tok[TM];   // of column 16 j + lr, -1: none
     uint4 base[TM][2];
 #pragma unroll
@@ -398,7 +404,15 @@ __global__ void __launch_bounds__(256) k_lora_up(LoraUp a) {
         }
       }
   }
+}
 #endif  // SG_DEVICE_PASS
+
+template <bool KS, int NP>
+__global__ void __launch_bounds__(256) k_lora_up(LoraUp a) {
+#if SG_DEVICE_PASS
+  __shared__ __attribute__((aligned(16))) LoraUpLds<KS> lds;
+  lora_up<KS, NP>(a, lds, blockIdx.x, blockIdx.y, blockIdx.z, gridDim.z);
+#endif
 }
 
 // ------------------------------------------------------------------ both at once
@@ -601,7 +615,7 @@ struct LoraSum {
   int out_f32;
 };
 
-// Adapter blockIdx.y's sum over its tokens in range blockIdx.z, columns of 64 a wave.  CR:
+// Adapter (and ranks) by's sum over its tokens in range bz, columns of 64 a wave.  CR:
 // results are [C][r] (dB), else [r][C] (dA).
 template <int RM, int NP>
 struct LoraSumLds {
@@ -611,16 +625,16 @@ struct LoraSumLds {
 };
 #if SG_DEVICE_PASS
 template <bool CR, int RM, int NP>
-__device__ __forceinline__ void lora_sum(const LoraSum& a, LoraSumLds<RM, NP>& lds, int bx) {
+__device__ __forceinline__ void lora_sum(const LoraSum& a, LoraSumLds<RM, NP>& lds, int bx, int by, int bz) {
   constexpr int PP = LoraSumLds<RM, NP>::PP, ZP = LoraSumLds<RM, NP>::ZP;
   uint8_t *const pl = lds.pl, *const zl = lds.zl;
   int *const list = lds.list, *const count = lds.count;
   const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int chunks = (a.r + 16 * RM - 1) / (16 * RM);
-  const int e = blockIdx.y / chunks, rho0 = (int)(blockIdx.y % chunks) * 16 * RM;
+  const int e = by / chunks, rho0 = (int)(by % chunks) * 16 * RM;
   const int n0 = (bx * 4 + wave) * 64;
-  const int64_t b0 = a.T * blockIdx.z / a.tsplits, b1 = a.T * (blockIdx.z + 1) / a.tsplits;
+  const int64_t b0 = a.T * bz / a.tsplits, b1 = a.T * (bz + 1) / a.tsplits;
   const float scale = a.scale ? a.scale[e] : 1.0f;
   v4f acc[4][RM];
 #pragma unroll
@@ -707,7 +721,7 @@ __device__ __forceinline__ void lora_sum(const LoraSum& a, LoraSumLds<RM, NP>& l
   }
   const int64_t one = (int64_t)a.r * a.C;
   const bool f32 = a.tsplits > 1 || a.out_f32;
-  float* const of = (a.tsplits > 1 ? a.sums + (int64_t)blockIdx.z * a.L * one : reinterpret_cast<float*>(a.out)) + e * one;
+  float* const of = (a.tsplits > 1 ? a.sums + (int64_t)bz * a.L * one : reinterpret_cast<float*>(a.out)) + e * one;
   uint16_t* const ob = reinterpret_cast<uint16_t*>(a.out) + e * one;
   if (CR) {
 #pragma unroll
@@ -743,13 +757,28 @@ __device__ __forceinline__ void lora_sum(const LoraSum& a, LoraSumLds<RM, NP>& l
 }
 #endif  // SG_DEVICE_PASS
 
-// dA's workgroups come first along x, then dB's.
+// dA's workgroups come first along x, then dB's; behind those of the sums, dx's, whose
+// product needs v as dA does: a launch less.
+struct LoraGrid {
+  int x, y, z;
+  __host__ __device__ int64_t all() const { return (int64_t)x * y * z; }
+};
 template <int RM, int NP>
-__global__ void __launch_bounds__(256) k_lora_sum(LoraSum a, LoraSum b, int a_x) {
+__global__ void __launch_bounds__(256) k_lora_sum(LoraSum a, LoraSum b, int a_x, LoraGrid sums, LoraUp dx, LoraGrid ups) {
 #if SG_DEVICE_PASS
-  __shared__ __attribute__((aligned(16))) LoraSumLds<RM, NP> lds;
-  if ((int)blockIdx.x < a_x) lora_sum<false, RM, NP>(a, lds, blockIdx.x);
-  else lora_sum<true, RM, NP>(b, lds, blockIdx.x - a_x);
+  __shared__ __attribute__((aligned(16))) union {
+    LoraSumLds<RM, NP> sum;
+    LoraUpLds<true> up;
+  } lds;
+  unsigned i = blockIdx.x;
+  if (i < sums.all()) {
+    const int bx = i % sums.x, by = i / sums.x % sums.y, bz = i / sums.x / sums.y;
+    if (bx < a_x) lora_sum<false, RM, NP>(a, lds.sum, bx, by, bz);
+    else lora_sum<true, RM, NP>(b, lds.sum, bx - a_x, by, bz);
+  } else {
+    i -= (unsigned)sums.all();
+    lora_up<true, 2>(dx, lds.up, i % ups.x, i / ups.x % ups.y, i / ups.x / ups.y, ups.z);
+  }
 #endif
 }
 
@@ -801,9 +830,11 @@ static int lora_splits(int64_t T, int64_t C) {
   return (int)(s < 1 ? 1 : s > LORA_PARTS ? LORA_PARTS : s);
 }
 
+// Parts of the tokens in the sums over them: 256 workgroups, 256 tokens of an adapter each
+// at least, so that small calls need no launch to join them.
 static int lora_tsplits(int64_t T, int64_t C, int64_t L) {
   int64_t s = 256 / (cdiv(C, 256) * L);
-  const int64_t most = cdiv(T, 128);
+  const int64_t most = T / (256 * L);
   s = s > most ? most : s;
   return (int)(s < 1 ? 1 : s > 32 ? 32 : s);
 }
@@ -859,25 +890,30 @@ static void launch_down(const LoraDown* v, const LoraDown* u, hipStream_t st) {
   }
 }
 
-template <bool KS, int TM>
-static void launch_up_tm(const LoraUp& a, hipStream_t st) {
-  const unsigned gx = (unsigned)cdiv(a.T, 64), gy = (unsigned)cdiv(a.C, 256);
-  const dim3 grid(gx, gy, (unsigned)lora_slots(a.T, a.L, (int64_t)gx * gy, TM));
-  if (a.y_f32) k_lora_up<KS, TM, 3><<<grid, 256, 0, st>>>(a);
-  else k_lora_up<KS, TM, 2><<<grid, 256, 0, st>>>(a);
+static LoraGrid lora_up_grid(const LoraUp& a) {
+  const int64_t gx = cdiv(a.T, 64), gy = cdiv(a.C, 256);
+  return {(int)gx, (int)gy, lora_slots(a.T, a.L, gx * gy, 1)};
 }
 template <bool KS>
 static void launch_up(const LoraUp& a, hipStream_t st) {
-  launch_up_tm<KS, 1>(a, st);
+  const LoraGrid g = lora_up_grid(a);
+  const dim3 grid(g.x, g.y, g.z);
+  if (a.y_f32) k_lora_up<KS, 3><<<grid, 256, 0, st>>>(a);
+  else k_lora_up<KS, 2><<<grid, 256, 0, st>>>(a);
 }
 
+// Both sums, and dx where it is not NULL.
 template <int NP>
-static void launch_sum(const LoraSum& a, const LoraSum& b, hipStream_t st) {
-  const unsigned ax = (unsigned)cdiv(a.C, 256), bx = (unsigned)cdiv(b.C, 256);
-  const auto grid = [&](int rm) { return dim3(ax + bx, (unsigned)(a.L * cdiv(a.r, 16 * rm)), (unsigned)a.tsplits); };
-  if (a.r <= 16) k_lora_sum<1, NP><<<grid(1), 256, 0, st>>>(a, b, (int)ax);
-  else if (a.r <= 32) k_lora_sum<2, NP><<<grid(2), 256, 0, st>>>(a, b, (int)ax);
-  else k_lora_sum<4, NP><<<grid(4), 256, 0, st>>>(a, b, (int)ax);
+static void launch_sum(const LoraSum& a, const LoraSum& b, const LoraUp* dx, hipStream_t st) {
+  const int ax = (int)cdiv(a.C, 256), bx = (int)cdiv(b.C, 256);
+  const LoraUp none = {};
+  const LoraGrid ups = dx ? lora_up_grid(*dx) : LoraGrid{0, 0, 0};
+  const auto sums = [&](int rm) { return LoraGrid{ax + bx, (int)(a.L * cdiv(a.r, 16 * rm)), a.tsplits}; };
+  const auto all = [&](int rm) { return (unsigned)(sums(rm).all() + ups.all()); };
+  const LoraUp& u = dx ? *dx : none;
+  if (a.r <= 16) k_lora_sum<1, NP><<<all(1), 256, 0, st>>>(a, b, ax, sums(1), u, ups);
+  else if (a.r <= 32) k_lora_sum<2, NP><<<all(2), 256, 0, st>>>(a, b, ax, sums(2), u, ups);
+  else k_lora_sum<4, NP><<<all(4), 256, 0, st>>>(a, b, ax, sums(4), u, ups);
 }
 
 // Whether a call's two products go in one launch.
@@ -901,8 +937,11 @@ static void launch_both(LoraBoth b, hipStream_t st) {
 
 static bool lora_shape_ok(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
   if (T < 1 || K < 8 || N < 8 || r < 8 || L < 1 || K % 8 || N % 8 || r % 8) return false;
-  // grids: ranks in chunks of 64 by adapters
-  return T < (1LL << 22) && K < (1LL << 22) && N < (1LL << 22) && r <= 256 && L * cdiv(r, 64) <= 65535;
+  if (T >= (1LL << 22) || K >= (1LL << 22) || N >= (1LL << 22) || r > 256 || L > 65535) return false;
+  // workgroups of the sums and of dx, in one launch (parts of the tokens, and of a block's items,
+  // are only where there are few)
+  const int64_t c = K > N ? K : N;
+  return launch_fits(cdiv(c, 256) * (2 * L * cdiv(r, 64) + cdiv(T, 64)) + 4096, 256);
 }
 static bool lora_ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld < (1LL << 22); }
 
@@ -975,11 +1014,11 @@ extern "C" sg_status sg_lora_gemm_backward(int64_t T, int64_t K, int64_t N, int 
   float *const u = reinterpret_cast<float*>(w + ws.u), *const v = reinterpret_cast<float*>(w + ws.v);
   const LoraDown dv = {T, (int)N, r, (int)L, ws.sv, dy, b, ld_dy, ids, v}, du = {T, (int)K, r, (int)L, ws.su, x, a, ldx, ids, u};
   launch_down(&dv, da ? &du : nullptr, stream);
+  LoraUp p = {};
   if (dx) {
-    LoraUp p = {};
     p.T = T; p.C = (int)K; p.r = r; p.L = (int)L; p.splits = ws.sv; p.part = v; p.scale = scale; p.ids = ids; p.w = a;
     p.base = base; p.ld_base = ld_base; p.y = dx; p.ldy = ld_dx;
-    launch_up<true>(p, stream);
+    if (!da) launch_up<true>(p, stream);
   }
   if (da) {
     LoraSum s = {};
@@ -989,8 +1028,8 @@ extern "C" sg_status sg_lora_gemm_backward(int64_t T, int64_t K, int64_t N, int 
     LoraSum q = s;
     q.C = (int)N; q.splits = ws.su; q.z = dy; q.ldz = ld_dy; q.part = u; q.sums = reinterpret_cast<float*>(w + ws.sb);
     q.out = db;
-    if (s.out_f32) launch_sum<3>(s, q, stream);
-    else launch_sum<2>(s, q, stream);
+    if (s.out_f32) launch_sum<3>(s, q, dx ? &p : nullptr, stream);
+    else launch_sum<2>(s, q, dx ? &p : nullptr, stream);
     if (ws.ts > 1) {
       LoraJoin j = {};
       j.sums[0] = reinterpret_cast<float*>(w + ws.sa); j.sums[1] = reinterpret_cast<float*>(w + ws.sb);

@@ -98,7 +98,7 @@ LORA_SHARED = [
     *[({n: None}, NULL) for n in ("x", "a", "b", "ws")],
     (dict(T=0), SHAPE), (dict(K=0), SHAPE), (dict(N=0), SHAPE), (dict(r=0), SHAPE), (dict(L=0), SHAPE),
     (dict(K=36), SHAPE), (dict(N=44), SHAPE), (dict(r=12), SHAPE), (dict(r=264), SHAPE), (dict(L=65536), SHAPE),
-    (dict(L=65535, r=72), SHAPE), (dict(T=BIG), SHAPE), (dict(ldx=32), SHAPE), (dict(ldx=BIG), SHAPE), (dict(wsb=100), SHAPE),
+    (dict(T=BIG), SHAPE), (dict(ldx=32), SHAPE), (dict(ldx=BIG), SHAPE), (dict(wsb=100), SHAPE),
     (dict(ldx=44), ALIGN), *[({n: ODD}, ALIGN) for n in ("x", "a", "b", "base", "ws")], (dict(ids=ODD1), ALIGN),
     (dict(scale=ODD1), ALIGN),
 ]
