@@ -5,11 +5,13 @@
 // that of its weight all read the matrices as the caller has them.
 //
 // k goes by blocks of 64 (two steps of 32: one 16x16x32 matrix instruction per pair of
-// sub-tiles), which buffer loads bring to LDS directly, three of the left operand and
-// two of the right at a time.  A KC block holds 128-byte rows (16-byte piece c of row r
+// sub-tiles), which buffer loads bring to LDS directly, SL of the left operand and
+// SR of the right at a time.  A KC block holds 128-byte rows (16-byte piece c of row r
 // at c ^ swz8q(r)), read 16 bytes a lane: with 64-byte rows every line came from L2
 // twice.  A KS block holds 64 rows of one k each (64-byte piece c of row k at c ^ swz(k)),
-// read with ds_read_b64_tr_b16, which hands each lane four k of one column.
+// read with ds_read_b64_tr_b16, which hands each lane four k of one column.  (Three and
+// two in the largest tile, which leave no LDS; more in those that few workgroups share out,
+// where a block's way from memory is longer than its product.)
 //
 // A wave first takes a step's operands from LDS and asks for what comes blocks later,
 // then multiplies.  With 8 waves those of the second half, one to a SIMD as those of the
@@ -40,6 +42,7 @@ struct PlainRow {
 #if SG_DEVICE_PASS
   __device__ static __forceinline__ int row(int u, int wave, int l) { return 8 * (NW * u + wave) + (l >> 3); }
   __device__ static constexpr int sel(int) { return 0; }
+  __device__ static constexpr int sel_wave(int) { return 0; }
 #endif
 };
 
@@ -74,8 +77,8 @@ __device__ __forceinline__ int tile_n(int s, int r) { return 32 * (s >> 1) + 8 *
 // One wave's loads of a KC operand: U instructions of 8 rows a block, NW waves.  The sum over k
 // has one segment or two of KB blocks, each with a matrix of its own; p[seg] is the
 // first column of row 0.  Row::row(u, wave, l) is the row that lane l of instruction u
-// loads; Row::sel(u, wave) which of the two matrices it is of, where it is not the
-// segment that says so.  Rows past the last lie outside of the descriptor (it ends
+// loads; Row::sel(u) ^ Row::sel_wave(wave) which of the two matrices it is of, where it
+// is not the segment that says so.  Rows past the last lie outside of the descriptor (it ends
 // with the last row) and read as zero.
 template <int U, int NW, typename Row>
 struct KcOp {
@@ -93,12 +96,12 @@ struct KcOp {
     const bool out = k * 64 + c >= K;
 #pragma unroll
     for (int m = 0; m < Row::MATS; ++m) {
-      const int s = m ^ seg;
+      const int s = m ^ seg ^ Row::sel_wave(wave);
       r[m] = tile_rsrc(s ? p[1] : p[0], none ? 0u : s ? bytes[1] : bytes[0]);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int s = Row::sel(u) ^ seg;
+      const int s = Row::sel(u) ^ seg ^ Row::sel_wave(wave);
       cur[u] = out ? W4_OUT : (uint32_t)((Row::row(u, wave, l) * (s ? ld[1] : ld[0]) + c) * 2);
     }
   }
@@ -141,15 +144,17 @@ struct KsOp {
 };
 #endif  // SG_DEVICE_PASS
 
-// WN x WM waves of NI x MJ sub-tiles each.  LRow: the left operand's rows, where it is KC.
-template <bool LKS_, bool RKS_, int WN_, int WM_, int NI_, int MJ_, typename LRow = void>
+// WN x WM waves of NI x MJ sub-tiles each; SL and SR places for blocks of the operands.
+// LRow: the left operand's rows, where it is KC.
+template <bool LKS_, bool RKS_, int WN_, int WM_, int NI_, int MJ_, int SL_, int SR_, typename LRow = void>
 struct Bf16Tile {
   static constexpr bool LKS = LKS_, RKS = RKS_;
   static constexpr int WN = WN_, WM = WM_, NI = NI_, MJ = MJ_, NW = WN * WM;
   static constexpr bool LAG = NW == 8;
-  static_assert(NI % 2 == 0 && MJ % 2 == 0, "pairs of sub-tiles");
+  static constexpr int SL = SL_, SR = SR_;
+  static_assert(NI % 2 == 0 && (!RKS || MJ % 2 == 0) && SL >= 2 && SR >= 2, "pairs of sub-tiles, places");
   static constexpr int BN = WN * NI * 16, BM = WM * MJ * 16;
-  static constexpr int L_BLOCK = BN * 128, R_BLOCK = BM * 128, R_OFF = 3 * L_BLOCK, LDS = R_OFF + 2 * R_BLOCK;
+  static constexpr int L_BLOCK = BN * 128, R_BLOCK = BM * 128, R_OFF = SL * L_BLOCK, LDS = R_OFF + SR * R_BLOCK;
   static constexpr int LU = BN / 8 / NW, RU = BM / 8 / NW;   // loads of one wave and block
   static_assert(LDS <= 160 * 1024, "LDS");
 #if SG_DEVICE_PASS
@@ -198,7 +203,7 @@ struct Bf16Tile {
     const uint32_t lbase = __builtin_amdgcn_readfirstlane(lds0 + wave * 1024), rbase = lbase + R_OFF;
     // addresses within a block, of its first step (KC: of both)
     constexpr int LP = LKS ? NI / 2 : 2, RP = RKS ? MJ / 2 : 2;
-    int la[LP], ra[RP], lat[LP];   // lat: within the block that is read from
+    int la[LP], ra[RP], lat[LP], rat[RP];   // lat, rat: within the block that is read from
     const int kr = 8 * g + (lr >> 2), a = lr & 3;   // KS: row of the first four k, group of 4 columns
 #pragma unroll
     for (int p = 0; p < LP; ++p)
@@ -206,7 +211,7 @@ struct Bf16Tile {
                                    : (wn * NI * 16 + lr) * 128 + (((4 * p + g) ^ swz8q(lr)) << 4));
 #pragma unroll
     for (int p = 0; p < RP; ++p)
-      ra[p] = lds0 + R_OFF + (RKS ? kr * (BM * 2) + (((wm * (MJ / 2) + p) ^ KsOp<RU, NW, BM>::swz(kr)) << 6) + 8 * a
+      ra[p] = rat[p] = lds0 + R_OFF + (RKS ? kr * (BM * 2) + (((wm * (MJ / 2) + p) ^ KsOp<RU, NW, BM>::swz(kr)) << 6) + 8 * a
                                   : (wm * MJ * 16 + lr) * 128 + (((4 * p + g) ^ swz8q(lr)) << 4));
     typedef __attribute__((address_space(3))) const uint8_t lds_u8;
     typedef __attribute__((address_space(3))) const v4i lds_v4i;
@@ -221,54 +226,51 @@ struct Bf16Tile {
       else return *(lds_v4i*)(lat[q] + i * 2048);
     };
     const auto read_r = [&](int q, int j) {
-      if constexpr (RKS) return tr8((lds_u8*)(ra[j >> 1] + q * (32 * BM * 2) + 32 * (j & 1)), 4 * BM * 2);
-      else return *(lds_v4i*)(ra[q] + j * 2048);
+      if constexpr (RKS) return tr8((lds_u8*)(rat[j >> 1] + q * (32 * BM * 2) + 32 * (j & 1)), 4 * BM * 2);
+      else return *(lds_v4i*)(rat[q] + j * 2048);
     };
-    using T = std::true_type;
-    using F = std::false_type;
-    using Zero = std::integral_constant<int, 0>;
-    using One = std::integral_constant<int, 1>;
-    unroll<LU>([&](auto n) { lo.template load<n, 1024 * NW * n>(lbase); });
-    fl_.next();
-    unroll<RU>([&](auto n) { ro.template load<n, 1024 * NW * n>(rbase); });
-    fr_.next();
-    unroll<LU>([&](auto n) { lo.template load<n, L_BLOCK + 1024 * NW * n>(lbase); });
-    fl_.next();
-    w4_wait<LU>();
+    // Loads that may be in flight when a block's have landed: of the blocks after it.
+    constexpr int FLY = (SL - 2) * LU + (SR - 2) * RU;
+    unroll<(SL > SR ? SL : SR) - 1>([&](auto c) {
+      if constexpr (c < SL - 1) {
+        unroll<LU>([&](auto n) { lo.template load<n, c * L_BLOCK + 1024 * NW * n>(lbase); });
+        fl_.next();
+      }
+      if constexpr (c < SR - 1) {
+        unroll<RU>([&](auto n) { ro.template load<n, c * R_BLOCK + 1024 * NW * n>(rbase); });
+        fr_.next();
+      }
+    });
+    w4_wait<FLY>();
     lds_barrier();
     if (LAG && wave >= NW / 2) lds_barrier();   // from here on a phase behind
     v4i fl[NI], fr[MJ];
-    int lread = 0, lfill = 2 * L_BLOCK, rflip = R_BLOCK, rfill = R_BLOCK;   // places in the rings
-    // Step q of a block: its operands from LDS; LOAD: the right operand of the next block
-    // (q = 0) or the left one of the block after (q = 1) is asked for; FLY: loads that may
-    // be in flight when those of the next block have landed.
-    const auto step = [&](auto qq, auto load, auto fly) {
+    int lread = 0, rread = 0, lfill = (SL - 1) * L_BLOCK, rfill = (SR - 1) * R_BLOCK;   // places in the rings
+    // Step q of block c: its operands from LDS; then the right operand of block c + SR - 1
+    // (q = 0) or the left one of block c + SL - 1 (q = 1), zeros past the end, is asked for.
+    const auto step = [&](auto qq) {
       constexpr int q = decltype(qq)::value;
-      constexpr bool LOAD = decltype(load)::value;
 #pragma unroll
       for (int j = 0; j < MJ; ++j) fr[j] = read_r(q, j);
 #pragma unroll
       for (int i = 0; i < NI; ++i) fl[i] = read_l(q, i);
-      if constexpr (LOAD && q == 0) {
+      if constexpr (q == 0) {
         const uint32_t to = rbase + rfill;
         unroll<RU>([&](auto n) { ro.template load<n, 1024 * NW * n>(to); });
         fr_.next();
-        rfill ^= R_BLOCK;
-      }
-      if constexpr (LOAD && q == 1) {
+        rfill = rfill == (SR - 1) * R_BLOCK ? 0 : rfill + R_BLOCK;
+      } else {
         const uint32_t to = lbase + lfill;
         unroll<LU>([&](auto n) { lo.template load<n, 1024 * NW * n>(to); });
         fl_.next();
-        lfill = lfill == 2 * L_BLOCK ? 0 : lfill + L_BLOCK;
-      }
-      if constexpr (q == 1) {
-        lread = lread == 2 * L_BLOCK ? 0 : lread + L_BLOCK;
+        lfill = lfill == (SL - 1) * L_BLOCK ? 0 : lfill + L_BLOCK;
+        lread = lread == (SL - 1) * L_BLOCK ? 0 : lread + L_BLOCK;
+        rread = rread == (SR - 1) * R_BLOCK ? 0 : rread + R_BLOCK;
 #pragma unroll
         for (int p = 0; p < LP; ++p) lat[p] = la[p] + lread;
 #pragma unroll
-        for (int p = 0; p < RP; ++p) ra[p] += rflip;
-        rflip = -rflip;
-        w4_wait<decltype(fly)::value>();
+        for (int p = 0; p < RP; ++p) rat[p] = ra[p] + rread;
+        w4_wait<FLY>();   // own loads of the next block have landed
       }
       lds_barrier();
       __builtin_amdgcn_s_setprio(1);
@@ -281,16 +283,12 @@ struct Bf16Tile {
       if (LAG) lds_barrier();
       __builtin_amdgcn_sched_barrier(0);
     };
-    // two blocks at least, zeros behind the last
-    for (int left = max(kb1 - kb0, 2); left > 2; --left) {
-      step(Zero{}, T{}, Zero{});
-      step(One{}, T{}, std::integral_constant<int, LU>{});
+    for (int left = kb1 - kb0; left > 0; --left) {
+      step(std::integral_constant<int, 0>{});
+      step(std::integral_constant<int, 1>{});
     }
-    step(Zero{}, T{}, Zero{});
-    step(One{}, F{}, Zero{});
-    step(Zero{}, F{}, Zero{});
-    step(One{}, F{}, Zero{});
     if (LAG && wave < NW / 2) lds_barrier();   // of the others' last phase
+    w4_wait<0>();   // the zeros past the end too, before LDS is given up
   }
   template <int N, int I = 0, typename Fn>
   __device__ static __forceinline__ void unroll(Fn fn) {

@@ -10,6 +10,7 @@
 // product whose left rows are those of dWg and dWu.
 #include "bf16_tile.h"
 #include "sg_gated.h"
+#include <stdlib.h>
 
 namespace sg {
 
@@ -125,14 +126,16 @@ __device__ __forceinline__ void gated_finish(const GatedArgs& a, int64_t m, int 
 // of the same f.
 template <int NI, int NW>
 struct GatedRow {
-  static constexpr int MATS = 2, HALF = NI / 2;
-  static_assert(NW / 2 <= HALF, "an instruction of every wave is of the same matrix");
+  // the waves of an instruction cover NW / 2 sub-tiles: half of a wave's at most, or all of them
+  static constexpr int HALF = NI / 2, MATS = NW / 2 <= HALF ? 2 : 1;
+  static_assert(NW / 2 <= HALF || NW / 2 == NI, "sub-tiles of an instruction");
 #if SG_DEVICE_PASS
   __device__ static __forceinline__ int row(int u, int wave, int l) {
     const int s = (NW * u + wave) >> 1, r = 8 * (wave & 1) + (l >> 3);
     return s / NI * (16 * HALF) + tile_n(s % HALF, r);
   }
-  __device__ static constexpr int sel(int u) { return NW / 2 * u / HALF & 1; }
+  __device__ static constexpr int sel(int u) { return MATS == 1 ? 0 : NW / 2 * u / HALF & 1; }
+  __device__ static __forceinline__ int sel_wave(int wave) { return MATS == 1 ? (wave >> 1) / HALF : 0; }
 #endif
 };
 
@@ -426,19 +429,28 @@ __global__ void __launch_bounds__(T::NW * 64) k_gated_dw(GatedGradArgs a, int ti
 #endif  // SG_DEVICE_PASS
 }
 
-template <bool L, bool R, typename Row = PlainRow<8>> using TileA = Bf16Tile<L, R, 2, 4, 8, 4, Row>;   // 256 x 256
-template <bool L, bool R, typename Row = PlainRow<4>> using TileB = Bf16Tile<L, R, 2, 2, 4, 4, Row>;   // 128 x 128
-using RowA = GatedRow<8, 8>;
-using RowB = GatedRow<4, 4>;
+// Tiles of n x m, their waves, and blocks of k in LDS.
+template <bool L, bool R, typename Row = PlainRow<8>> using TileA = Bf16Tile<L, R, 2, 4, 8, 4, 3, 2, Row>;   // 256 x 256
+template <bool L, bool R, typename Row = PlainRow<8>> using TileC = Bf16Tile<L, R, 2, 4, 4, 4, 3, 3, Row>;   // 128 x 256
+template <bool L, bool R, typename Row = PlainRow<8>> using TileB = Bf16Tile<L, R, 2, 4, 4, 2, 5, 5, Row>;   // 128 x 128
+template <bool L, bool R, typename Row = PlainRow<8>> using TileB2 = Bf16Tile<L, R, 2, 4, 4, 2, 3, 2, Row>;   // 128 x 128
+template <bool L, bool R, typename Row = PlainRow<4>> using TileD = Bf16Tile<L, R, 1, 4, 4, 1, 5, 5, Row>;   // 64 x 64
 
 template <bool BACK, int MT>
 static void launch_gated_rows(const GatedArgs& a, hipStream_t st) {
   k_gated_rows<1, MT, BACK><<<dim3((unsigned)cdiv(a.F, 16), (unsigned)cdiv(a.T, 16 * MT)), 512, 0, st>>>(a);
 }
 
+template <typename T, bool BACK>
+static void launch_gated_tile(const GatedArgs& a, hipStream_t st) {
+  const int tm = (int)cdiv(a.T, T::BM), tn = (int)cdiv(a.F, T::BN / 2);
+  k_gated_tile<T, BACK><<<(unsigned)tm * tn, T::NW * 64, 0, st>>>(a, tm, tn);
+}
+
 template <bool BACK>
 static void launch_gated(const GatedArgs& a, hipStream_t st) {
-  if (a.T <= 64) {
+  static const int few = getenv("FEW") ? atoi(getenv("FEW")) : 64;
+  if (a.T <= few) {
     switch ((a.T + 15) / 16) {
       case 1: launch_gated_rows<BACK, 1>(a, st); break;
       case 2: launch_gated_rows<BACK, 2>(a, st); break;
@@ -447,15 +459,14 @@ static void launch_gated(const GatedArgs& a, hipStream_t st) {
     }
     return;
   }
-  if (cdiv(a.T, 256) * cdiv(a.F, 128) >= 256) {
-    using T = TileA<false, false, RowA>;
-    const int tm = (int)cdiv(a.T, 256), tn = (int)cdiv(a.F, 128);
-    k_gated_tile<T, BACK><<<(unsigned)tm * tn, T::NW * 64, 0, st>>>(a, tm, tn);
-  } else {
-    using T = TileB<false, false, RowB>;
-    const int tm = (int)cdiv(a.T, 128), tn = (int)cdiv(a.F, 64);
-    k_gated_tile<T, BACK><<<(unsigned)tm * tn, T::NW * 64, 0, st>>>(a, tm, tn);
-  }
+  static const int way = getenv("WAY") ? atoi(getenv("WAY")) : 0;
+  if (way == 1) launch_gated_tile<TileA<false, false, GatedRow<8, 8>>, BACK>(a, st);
+  else if (way == 2) launch_gated_tile<TileB<false, false, GatedRow<4, 8>>, BACK>(a, st);
+  else if (way == 3) launch_gated_tile<TileC<false, false, GatedRow<4, 8>>, BACK>(a, st);
+  else if (way == 5) launch_gated_tile<TileB2<false, false, GatedRow<4, 8>>, BACK>(a, st);
+  else if (way == 4) launch_gated_tile<TileD<false, false, GatedRow<4, 4>>, BACK>(a, st);
+  else if (cdiv(a.T, 256) * cdiv(a.F, 128) >= 256) launch_gated_tile<TileA<false, false, GatedRow<8, 8>>, BACK>(a, st);
+  else launch_gated_tile<TileB<false, false, GatedRow<4, 8>>, BACK>(a, st);
 }
 
 // How dX is computed: tiles of 256 or 128, parts of its sum over 2 F.
