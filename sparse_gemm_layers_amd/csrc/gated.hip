@@ -10,7 +10,6 @@
 // product whose left rows are those of dWg and dWu.
 #include "bf16_tile.h"
 #include "sg_gated.h"
-#include <stdlib.h>
 
 namespace sg {
 
@@ -186,61 +185,40 @@ __global__ void __launch_bounds__(T::NW * 64) k_gated_tile(GatedArgs a, int tile
 #endif  // SG_DEVICE_PASS
 }
 
-// Few rows: a workgroup takes RB blocks of 16 rows of each weight and 16 MT tokens;
-// its 8 waves split K and add their partial tiles in LDS.  Weights come from HBM and
-// are all that counts: a wave asks for the next K block's while it multiplies one.
-template <int RB, int MT, bool BACK>
+// Up to 16 tokens: a workgroup takes 16 rows of each weight; its 8 waves split K and add
+// their partial tiles in LDS.  Weights come from HBM and are all that counts: a wave asks
+// for the next K block's while it multiplies one.  (One token, 14336 x 4096: 44 us, 5.3
+// TB/s.)
+template <bool BACK>
 __global__ void __launch_bounds__(512) k_gated_rows(GatedArgs a) {
 #if SG_DEVICE_PASS
-  __shared__ __attribute__((aligned(1024))) float red[8][RB * 2 * MT][64][4];
+  __shared__ __attribute__((aligned(1024))) float red[8][2][64][4];
   const int t = threadIdx.x, l = t & 63, g = l >> 4, lr = l & 15;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int f0 = blockIdx.x * (16 * RB);
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
-  const int rows = (int)min((int64_t)(16 * MT), a.T - m0), wrows = min(16 * RB, a.F - f0);
+  const int f0 = blockIdx.x * 16, rows = (int)a.T, wrows = min(16, a.F - f0);
   const int KB = (a.D + 127) >> 7;
-  const __amdgpu_buffer_rsrc_t rx = w4_rsrc(a.x + m0 * a.ldx, (uint32_t)(((rows - 1) * a.ldx + a.D) * 2));
+  const __amdgpu_buffer_rsrc_t rx = w4_rsrc(a.x, (uint32_t)(((rows - 1) * a.ldx + a.D) * 2));
   const __amdgpu_buffer_rsrc_t rg = w4_rsrc(a.gate + f0 * a.ldg, (uint32_t)(((wrows - 1) * a.ldg + a.D) * 2));
   const __amdgpu_buffer_rsrc_t ru = w4_rsrc(a.up + f0 * a.ldu, (uint32_t)(((wrows - 1) * a.ldu + a.D) * 2));
-  uint32_t xo[MT], wo[RB][2];
-#pragma unroll
-  for (int j = 0; j < MT; ++j) xo[j] = 16 * j + lr < rows ? (uint32_t)(((16 * j + lr) * a.ldx + 8 * g) * 2) : W4_OUT;
-#pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    const int f = 16 * b + lr;
-    wo[b][0] = f < wrows ? (uint32_t)((f * a.ldg + 8 * g) * 2) : W4_OUT;
-    wo[b][1] = f < wrows ? (uint32_t)((f * a.ldu + 8 * g) * 2) : W4_OUT;
-  }
-  v4f acc[RB][2][MT];
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < MT; ++j) acc[b][h][j] = (v4f){0.f, 0.f, 0.f, 0.f};
-  v4i w[2][RB][2][4], x[2][MT][4];
+  const uint32_t xo = lr < rows ? (uint32_t)((lr * a.ldx + 8 * g) * 2) : W4_OUT;
+  const uint32_t go = lr < wrows ? (uint32_t)((lr * a.ldg + 8 * g) * 2) : W4_OUT;
+  const uint32_t uo = lr < wrows ? (uint32_t)((lr * a.ldu + 8 * g) * 2) : W4_OUT;
+  v4f acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  v4i w[2][2][4], x[2][4];
   const auto load = [&](int s, int kb) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const bool in = kb * 128 + 32 * q + 8 * g < a.D;
-#pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        w[s][b][0][q] = w4_ld16(rg, in ? wo[b][0] + 64 * q : W4_OUT, kb * 256);
-        w[s][b][1][q] = w4_ld16(ru, in ? wo[b][1] + 64 * q : W4_OUT, kb * 256);
-      }
-#pragma unroll
-      for (int j = 0; j < MT; ++j) x[s][j][q] = w4_ld16(rx, in ? xo[j] + 64 * q : W4_OUT, kb * 256);
+      w[s][0][q] = w4_ld16(rg, in ? go + 64 * q : W4_OUT, kb * 256);
+      w[s][1][q] = w4_ld16(ru, in ? uo + 64 * q : W4_OUT, kb * 256);
+      x[s][q] = w4_ld16(rx, in ? xo + 64 * q : W4_OUT, kb * 256);
     }
   };
   const auto compute = [&](int s) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < MT; ++j) acc[b][h][j] = w4_mfma(w[s][b][h][q], x[s][j][q], acc[b][h][j]);
+      for (int h = 0; h < 2; ++h) acc[h] = w4_mfma(w[s][h][q], x[s][q], acc[h]);
   };
   if (wave < KB) load(0, wave);
   for (int kb = wave; kb < KB; kb += 16) {
@@ -252,30 +230,23 @@ __global__ void __launch_bounds__(512) k_gated_rows(GatedArgs a) {
     }
   }
 #pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int j = 0; j < MT; ++j) *reinterpret_cast<v4f*>(&red[wave][(b * 2 + h) * MT + j][l][0]) = acc[b][h][j];
+  for (int h = 0; h < 2; ++h) *reinterpret_cast<v4f*>(&red[wave][h][l][0]) = acc[h];
   __syncthreads();
-  // token 16 j + i, values 8 o .. 8 o + 7 of the workgroup's
-  for (int q = t; q < 32 * RB * MT; q += 512) {
-    const int i = q & 15, o = (q >> 4) % (2 * RB), j = q / (32 * RB);
-    if (16 * j + i >= rows || 8 * o >= wrows) continue;
-    float v[2][8];
+  // token t % 16, values 8 o .. 8 o + 7 of the workgroup's
+  const int i = t & 15, o = t >> 4;
+  if (o >= 2 || i >= rows || 8 * o >= wrows) return;
+  float v[2][8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        v4f s = {0.f, 0.f, 0.f, 0.f};
+    for (int e = 0; e < 8; e += 4) {
+      v4f s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          s += *reinterpret_cast<const v4f*>(&red[k][((o >> 1) * 2 + h) * MT + j][16 * (2 * (o & 1) + (e >> 2)) + i][0]);
+      for (int k = 0; k < 8; ++k) s += *reinterpret_cast<const v4f*>(&red[k][h][16 * (2 * o + (e >> 2)) + i][0]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[h][e + k] = s[k];
-      }
-    gated_finish<BACK>(a, m0 + 16 * j + i, f0 + 8 * o, v[0], v[1]);
-  }
+      for (int k = 0; k < 4; ++k) v[h][e + k] = s[k];
+    }
+  gated_finish<BACK>(a, i, f0 + 8 * o, v[0], v[1]);
 #endif  // SG_DEVICE_PASS
 }
 
@@ -311,16 +282,17 @@ struct GatedGradArgs {
   int64_t ld_dw;
   float* part;      // split sums [splits][T][D]
   int splits;
+  int dx_m, dx_n, dw_m, dw_n;   // tiles of either; none of what is not asked for
 };
 
 // dX [T, D]: left the weights' columns (k across rows), right dG and dU; the sum runs
 // over dG . Wg, then dU . Wu.
-template <typename T>
-__global__ void __launch_bounds__(T::NW * 64) k_gated_dx(GatedGradArgs a, int tiles_m, int tiles_n) {
 #if SG_DEVICE_PASS
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+template <typename T>
+__device__ __forceinline__ void gated_dx(const GatedGradArgs& a, uint8_t* lds, int block) {
+  const int tiles_m = a.dx_m, tiles_n = a.dx_n;
   int tn, tm;
-  const int tiles = tiles_m * tiles_n, b = xcd_order(blockIdx.x, tiles * a.splits);
+  const int tiles = tiles_m * tiles_n, b = xcd_order(block, tiles * a.splits);
   const int split = b / tiles;
   tile_of(b - split * tiles, tiles_m, tiles_n, tn, tm);
   const int l = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -363,38 +335,17 @@ __global__ void __launch_bounds__(T::NW * 64) k_gated_dx(GatedGradArgs a, int ti
       }
     }
   }
+}
 #endif  // SG_DEVICE_PASS
-}
-
-// The split sums of dX, added in order.
-__global__ void __launch_bounds__(256) k_gated_dx_join(GatedGradArgs a) {
-#if SG_DEVICE_PASS
-  const int per = a.D / 8;
-  const int64_t all = a.T * per, step = (int64_t)gridDim.x * 256;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
-    const int64_t m = i / per;
-    const int n = 8 * (int)(i - m * per);
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < a.splits; ++s) {
-      float t[8];
-      load4(a.part + ((int64_t)s * a.T + m) * a.D + n, t);
-      load4(a.part + ((int64_t)s * a.T + m) * a.D + n + 4, t + 4);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += t[e];
-    }
-    store8(a.dx + m * a.ld_dx + n, v);
-  }
-#endif
-}
 
 // dWg and dWu [F, D]: left the columns of X, right those of dG (the first half of the
 // tiles along m) or dU; the sum runs over tokens, across the rows of both.
-template <typename T>
-__global__ void __launch_bounds__(T::NW * 64) k_gated_dw(GatedGradArgs a, int tiles_m, int tiles_n) {
 #if SG_DEVICE_PASS
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::LDS];
+template <typename T>
+__device__ __forceinline__ void gated_dw(const GatedGradArgs& a, uint8_t* lds, int block) {
+  const int tiles_m = a.dw_m, tiles_n = a.dw_n;
   int tn, tm;
-  tile_coords(tiles_m, tiles_n, tn, tm);
+  tile_of(xcd_order(block, tiles_m * tiles_n), tiles_m, tiles_n, tn, tm);
   const int l = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const bool up = 2 * tm >= tiles_m;
   const int n0 = tn * T::BN, m0 = (up ? tm - tiles_m / 2 : tm) * T::BM;
@@ -426,19 +377,52 @@ __global__ void __launch_bounds__(T::NW * 64) k_gated_dw(GatedGradArgs a, int ti
       store8(out + (int64_t)(m0 + m) * a.ld_dw + n0 + n, v);
     }
   }
+}
 #endif  // SG_DEVICE_PASS
+
+// Both in one launch, dX's workgroups first: theirs are the longer ones, and the others fill
+// the card behind them.
+template <typename TX, typename TW>
+__global__ void __launch_bounds__(512) k_gated_grads(GatedGradArgs a) {
+#if SG_DEVICE_PASS
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[TX::LDS > TW::LDS ? TX::LDS : TW::LDS];
+  const int first = a.dx_m * a.dx_n * a.splits;
+  if ((int)blockIdx.x < first) gated_dx<TX>(a, lds, blockIdx.x);
+  else gated_dw<TW>(a, lds, blockIdx.x - first);
+#endif
+}
+
+// The split sums of dX, added in order.
+__global__ void __launch_bounds__(256) k_gated_dx_join(GatedGradArgs a) {
+#if SG_DEVICE_PASS
+  const int per = a.D / 8;
+  const int64_t all = a.T * per, step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
+    const int64_t m = i / per;
+    const int n = 8 * (int)(i - m * per);
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < a.splits; ++s) {
+      float t[8];
+      load4(a.part + ((int64_t)s * a.T + m) * a.D + n, t);
+      load4(a.part + ((int64_t)s * a.T + m) * a.D + n + 4, t + 4);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += t[e];
+    }
+    store8(a.dx + m * a.ld_dx + n, v);
+  }
+#endif
 }
 
 // Tiles of n x m, their waves, and blocks of k in LDS.
 template <bool L, bool R, typename Row = PlainRow<8>> using TileA = Bf16Tile<L, R, 2, 4, 8, 4, 3, 2, Row>;   // 256 x 256
 template <bool L, bool R, typename Row = PlainRow<8>> using TileC = Bf16Tile<L, R, 2, 4, 4, 4, 3, 3, Row>;   // 128 x 256
 template <bool L, bool R, typename Row = PlainRow<8>> using TileB = Bf16Tile<L, R, 2, 4, 4, 2, 5, 5, Row>;   // 128 x 128
-template <bool L, bool R, typename Row = PlainRow<8>> using TileB2 = Bf16Tile<L, R, 2, 4, 4, 2, 3, 2, Row>;   // 128 x 128
-template <bool L, bool R, typename Row = PlainRow<4>> using TileD = Bf16Tile<L, R, 1, 4, 4, 1, 5, 5, Row>;   // 64 x 64
+template <bool L, bool R, typename Row = PlainRow<8>> using TileE = Bf16Tile<L, R, 2, 4, 4, 2, 3, 2, Row>;   // 128 x 128, two a unit
+template <bool L, bool R, typename Row = PlainRow<4>> using TileD = Bf16Tile<L, R, 1, 4, 4, 1, 5, 5, Row>;   // 64 x 64, two a unit
 
-template <bool BACK, int MT>
+template <bool BACK>
 static void launch_gated_rows(const GatedArgs& a, hipStream_t st) {
-  k_gated_rows<1, MT, BACK><<<dim3((unsigned)cdiv(a.F, 16), (unsigned)cdiv(a.T, 16 * MT)), 512, 0, st>>>(a);
+  k_gated_rows<BACK><<<(unsigned)cdiv(a.F, 16), 512, 0, st>>>(a);
 }
 
 template <typename T, bool BACK>
@@ -447,39 +431,53 @@ static void launch_gated_tile(const GatedArgs& a, hipStream_t st) {
   k_gated_tile<T, BACK><<<(unsigned)tm * tn, T::NW * 64, 0, st>>>(a, tm, tn);
 }
 
+// Which tiles: a block of 64 k takes a workgroup about as long however many others there
+// are, until they take turns.  us a block, in hundredths: 256 x 256 127, 128 x 256 93,
+// 128 x 128 80, 64 x 64 50 (one a compute unit) or 73 (two).  Measured, us, tiles in
+// that order: 128 x 11008 x 4096 79 / 60 / 52 / 61; 256 tokens 81 / 62 / 85 / 95; 512 95 / 115 /
+// 125 / 167; 1024 168 / 176 / 240 / 320; 333 x 2760 x 1032 31 / 20 / 16 / 19; 64 x 5512 x 2040 51 /
+// 31 / 27 / 20; 37 x 14336 x 4096 77 / 62 / 50 / 47.
 template <bool BACK>
 static void launch_gated(const GatedArgs& a, hipStream_t st) {
-  static const int few = getenv("FEW") ? atoi(getenv("FEW")) : 64;
-  if (a.T <= few) {
-    switch ((a.T + 15) / 16) {
-      case 1: launch_gated_rows<BACK, 1>(a, st); break;
-      case 2: launch_gated_rows<BACK, 2>(a, st); break;
-      case 3: launch_gated_rows<BACK, 3>(a, st); break;
-      default: launch_gated_rows<BACK, 4>(a, st); break;
-    }
+  if (a.T <= 16) {
+    launch_gated_rows<BACK>(a, st);
     return;
   }
-  static const int way = getenv("WAY") ? atoi(getenv("WAY")) : 0;
-  if (way == 1) launch_gated_tile<TileA<false, false, GatedRow<8, 8>>, BACK>(a, st);
-  else if (way == 2) launch_gated_tile<TileB<false, false, GatedRow<4, 8>>, BACK>(a, st);
-  else if (way == 3) launch_gated_tile<TileC<false, false, GatedRow<4, 8>>, BACK>(a, st);
-  else if (way == 5) launch_gated_tile<TileB2<false, false, GatedRow<4, 8>>, BACK>(a, st);
-  else if (way == 4) launch_gated_tile<TileD<false, false, GatedRow<4, 4>>, BACK>(a, st);
-  else if (cdiv(a.T, 256) * cdiv(a.F, 128) >= 256) launch_gated_tile<TileA<false, false, GatedRow<8, 8>>, BACK>(a, st);
-  else launch_gated_tile<TileB<false, false, GatedRow<4, 8>>, BACK>(a, st);
+  const auto tiles = [&](int bm, int bf) { return cdiv(a.T, bm) * cdiv(a.F, bf); };
+  const int64_t A = 127 * cdiv(tiles(256, 128), 256), C = 93 * cdiv(tiles(256, 64), 256);
+  const int64_t B = 80 * cdiv(tiles(128, 64), 256), d = tiles(64, 32), D = d <= 256 ? 50 : 73 * cdiv(d, 512);
+  if (A <= B && A <= C && A <= D) launch_gated_tile<TileA<false, false, GatedRow<8, 8>>, BACK>(a, st);
+  else if (C <= B && C <= D) launch_gated_tile<TileC<false, false, GatedRow<4, 8>>, BACK>(a, st);
+  else if (B <= D) launch_gated_tile<TileB<false, false, GatedRow<4, 8>>, BACK>(a, st);
+  else launch_gated_tile<TileD<false, false, GatedRow<4, 4>>, BACK>(a, st);
 }
 
-// How dX is computed: tiles of 256 or 128, parts of its sum over 2 F.
-struct DxPlan {
+// How dX and dW are computed: tiles of 256 (one a compute unit) or 128 (two), and parts of
+// dX's sum over 2 F.  By the time of the rounds of tiles, us a block of 64 k as above and
+// for a tile's start and end, and that of writing, reading and adding the parts.
+struct GradPlan {
   bool big;
   int splits;
-  DxPlan(int64_t T, int64_t F, int64_t D) {
-    const int64_t steps = 2 * cdiv(F, 64);
-    big = cdiv(T, 256) * cdiv(D, 256) >= 64;
-    const int64_t tiles = big ? cdiv(T, 256) * cdiv(D, 256) : cdiv(T, 128) * cdiv(D, 128);
-    int64_t s = (big ? 256 : 512) / tiles;
-    if (s > steps / 8) s = steps / 8;
-    splits = (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+  static double rounds(bool b, int64_t tiles, int64_t blocks) {
+    if (b) return (double)cdiv(tiles, 256) * (1.2 * blocks + 8.0);
+    return tiles <= 256 ? 0.9 * blocks + 4.0 : (double)cdiv(tiles, 512) * (1.1 * blocks + 6.0);
+  }
+  static int64_t dx_tiles(bool b, int64_t T, int64_t D) {
+    return b ? cdiv(T, 256) * cdiv(D, 256) : cdiv(T, 128) * cdiv(D, 128);
+  }
+  static int64_t dw_tiles(bool b, int64_t F, int64_t D) {
+    return b ? 2 * cdiv(F, 256) * cdiv(D, 256) : 2 * cdiv(F, 128) * cdiv(D, 128);
+  }
+  GradPlan(int64_t T, int64_t F, int64_t D) {
+    const int64_t blocks = 2 * cdiv(F, 64);
+    double best = 1e30;
+    for (int b = 0; b < 2; ++b) {
+      const double dw = rounds(b, dw_tiles(b, F, D), cdiv(T, 64));
+      for (int s = 1; s <= 32 && (s == 1 || 4 * s <= blocks); ++s) {
+        const double us = rounds(b, dx_tiles(b, T, D) * s, cdiv(blocks, s)) + dw + (s > 1 ? 3.0 + 8.0 * s * T * D / 5e6 : 0.0);
+        if (us < best) best = us, big = b, splits = s;
+      }
+    }
   }
   int64_t bytes(int64_t T, int64_t D) const { return splits == 1 ? 0 : 4 * splits * T * D; }
 };
@@ -489,8 +487,8 @@ static bool gated_shape_ok(int64_t T, int64_t F, int64_t D) {
   return cdiv(T, 128) * cdiv(F, 64) < (1LL << 22);
 }
 static bool gated_back_ok(int64_t T, int64_t F, int64_t D) {
-  return gated_shape_ok(T, F, D) && cdiv(F, 128) * cdiv(D, 128) < (1LL << 22) &&
-         cdiv(T, 128) * cdiv(D, 128) < (1LL << 22);
+  // tiles of both in one launch; parts are only where there are few
+  return gated_shape_ok(T, F, D) && 2 * cdiv(F, 128) * cdiv(D, 128) + cdiv(T, 128) * cdiv(D, 128) < (1LL << 22);
 }
 static bool ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld < (1LL << 22); }
 
@@ -524,7 +522,7 @@ extern "C" sg_status sg_gated_gemm(int64_t T, int64_t F, int64_t D, const uint16
 
 extern "C" int64_t sg_gated_gemm_backward_workspace(int64_t T, int64_t F, int64_t D) {
   if (!gated_back_ok(T, F, D)) return -1;
-  return DxPlan(T, F, D).bytes(T, D);
+  return GradPlan(T, F, D).bytes(T, D);
 }
 
 extern "C" sg_status sg_gated_gemm_backward(int64_t T, int64_t F, int64_t D, const uint16_t* dh, int64_t ld_dh,
@@ -542,7 +540,7 @@ extern "C" sg_status sg_gated_gemm_backward(int64_t T, int64_t F, int64_t D, con
       (g && !ld_ok(ld_gu, F)) || (add && !ld_ok(ld_add, F)) || !ld_ok(ld_dgu, F) || (dx && !ld_ok(ld_dx, D)) ||
       (dgate && !ld_ok(ld_dw, D)))
     return SG_ERR_SHAPE;
-  const DxPlan plan(T, F, D);
+  const GradPlan plan(T, F, D);
   const int64_t need = dx ? plan.bytes(T, D) : 0;
   if (need && !workspace) return SG_ERR_NULL;
   if (need > workspace_bytes) return SG_ERR_SHAPE;
@@ -563,24 +561,12 @@ extern "C" sg_status sg_gated_gemm_backward(int64_t T, int64_t F, int64_t D, con
   b.T = T; b.F = (int)F; b.D = (int)D; b.x = x; b.gate = gate; b.up = up; b.dg = dg; b.du = du;
   b.ldx = ldx; b.ldg = ldg; b.ldu = ldu; b.ld_dgu = ld_dgu; b.dx = dx; b.ld_dx = ld_dx;
   b.dgate = dgate; b.dup = dup; b.ld_dw = ld_dw; b.part = reinterpret_cast<float*>(workspace); b.splits = plan.splits;
-  if (dx) {
-    if (plan.big) {
-      const int tm = (int)cdiv(T, 256), tn = (int)cdiv(D, 256);
-      k_gated_dx<TileA<true, false>><<<(unsigned)(tm * tn * plan.splits), TileA<true, false>::NW * 64, 0, stream>>>(b, tm, tn);
-    } else {
-      const int tm = (int)cdiv(T, 128), tn = (int)cdiv(D, 128);
-      k_gated_dx<TileB<true, false>><<<(unsigned)(tm * tn * plan.splits), TileB<true, false>::NW * 64, 0, stream>>>(b, tm, tn);
-    }
-    if (plan.splits > 1) k_gated_dx_join<<<grid_for(T * (D / 8), 256, 8192), 256, 0, stream>>>(b);
-  }
-  if (dgate) {
-    if (2 * cdiv(F, 256) * cdiv(D, 256) >= 256) {
-      const int tm = 2 * (int)cdiv(F, 256), tn = (int)cdiv(D, 256);
-      k_gated_dw<TileA<true, true>><<<(unsigned)tm * tn, TileA<true, true>::NW * 64, 0, stream>>>(b, tm, tn);
-    } else {
-      const int tm = 2 * (int)cdiv(F, 128), tn = (int)cdiv(D, 128);
-      k_gated_dw<TileB<true, true>><<<(unsigned)tm * tn, TileB<true, true>::NW * 64, 0, stream>>>(b, tm, tn);
-    }
-  }
+  const int t = plan.big ? 256 : 128;
+  if (dx) b.dx_m = (int)cdiv(T, t), b.dx_n = (int)cdiv(D, t);
+  if (dgate) b.dw_m = 2 * (int)cdiv(F, t), b.dw_n = (int)cdiv(D, t);
+  const unsigned grid = (unsigned)(b.dx_m * b.dx_n * b.splits + b.dw_m * b.dw_n);
+  if (grid && plan.big) k_gated_grads<TileA<true, false>, TileA<true, true>><<<grid, 512, 0, stream>>>(b);
+  else if (grid) k_gated_grads<TileE<true, false>, TileE<true, true>><<<grid, 512, 0, stream>>>(b);
+  if (dx && plan.splits > 1) k_gated_dx_join<<<grid_for(T * (D / 8), 256, 8192), 256, 0, stream>>>(b);
   return launch_status();
 }

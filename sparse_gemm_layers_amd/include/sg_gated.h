@@ -53,8 +53,8 @@ sg_status sg_gated_gemm(int64_t T, int64_t F, int64_t D, const uint16_t* x, int6
  *        ld_dw, or both NULL
  *   workspace : for dx, at least sg_gated_gemm_backward_workspace(T, F, D) bytes (0:
  *        none), 256-byte aligned, in use until the work on `stream` is done
- * Requires what sg_gated_gemm does; ceil(F/128) * ceil(D/128) < 2^22 and ceil(T/128) *
- * ceil(D/128) < 2^22.  dg and du may take the place of g and u, no other output that
+ * Requires what sg_gated_gemm does, and (2 ceil(F/128) + ceil(T/128)) * ceil(D/128) <
+ * 2^22.  dg and du may take the place of g and u, no other output that
  * of an input.
  */
 int64_t sg_gated_gemm_backward_workspace(int64_t T, int64_t F, int64_t D);
