@@ -6,7 +6,7 @@ import functools
 import torch
 
 from ._binding import SgError, _FB, _check, _i64, _int, _ptr, lib
-from ._moe import _BF, _CODE, _current_stream, _matrix, _refuse, _result
+from ._moe import _BF, _CODE, _matrix, _refuse, _result
 
 _SIGS = {
     "sg_gated_gemm": ([_i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _int, _ptr, _ptr, _i64, _ptr, _int, _i64,
@@ -32,6 +32,15 @@ def _lib():
             fn.restype = res
         _typed = h
     return h
+
+
+def _launch(x, fn, *args):
+    """fn(*args, stream) on x's device and the current stream there."""
+    d = x.get_device()
+    if d == torch._C._cuda_getDevice():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(d))
+    with torch.cuda.device(d):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(d))
 
 
 def _act_code(act):
@@ -97,8 +106,8 @@ def gated_gemm(x, gate, up, act: str = "silu", gate_add=None, up_add=None, out_d
     if keep and g is None and u is None:
         g, u = x.new_empty((T, F)), x.new_empty((T, F))
     pg, pu, ld_gu = _pair(g, u, ("g", "u"), (T, F), dev)
-    st = _lib().sg_gated_gemm(T, F, D, x.data_ptr(), ldx, gate.data_ptr(), ldg, up.data_ptr(), ldu, code, pga, pua,
-                              ld_add, h.data_ptr(), _CODE[h.dtype], ldh, pg, pu, ld_gu, _current_stream(x))
+    st = _launch(x, _lib().sg_gated_gemm, T, F, D, x.data_ptr(), ldx, gate.data_ptr(), ldg, up.data_ptr(), ldu, code, pga,
+                 pua, ld_add, h.data_ptr(), _CODE[h.dtype], ldh, pg, pu, ld_gu)
     if st:
         _check(st, "sg_gated_gemm")
     return (h, g, u) if pg is not None else h
@@ -153,9 +162,9 @@ def gated_gemm_backward(dh, x, gate, up, act: str = "silu", g=None, u=None, gate
                 or not workspace.is_contiguous() or workspace.numel() < need or workspace.device != dev:
             raise SgError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {dev}")
         pw, wn = workspace.data_ptr(), workspace.numel()
-    st = _lib().sg_gated_gemm_backward(T, F, D, dh.data_ptr(), ld_dh, x.data_ptr(), ldx, gate.data_ptr(), ldg,
-                                       up.data_ptr(), ldu, code, pg, pu, ld_gu, pga, pua, ld_add, pdg, pdu, ld_dgu,
-                                       pdx, ld_dx, pwg, pwu, ld_dw, pw, wn, _current_stream(x))
+    st = _launch(x, _lib().sg_gated_gemm_backward, T, F, D, dh.data_ptr(), ld_dh, x.data_ptr(), ldx, gate.data_ptr(), ldg,
+                 up.data_ptr(), ldu, code, pg, pu, ld_gu, pga, pua, ld_add, pdg, pdu, ld_dgu, pdx, ld_dx, pwg, pwu,
+                 ld_dw, pw, wn)
     if st:
         _check(st, "sg_gated_gemm_backward")
     return dx, dgate, dup, dg, du

@@ -6,7 +6,8 @@ import functools
 import torch
 
 from ._binding import SgError, _FB, _check, _i64, _int, _ptr, lib
-from ._moe import _BF, _CODE, _current_stream, _matrix, _refuse, _result, _rows
+from ._gated import _launch
+from ._moe import _BF, _CODE, _matrix, _refuse, _result, _rows
 
 _SIGS = {
     "sg_lora_gemm_workspace": ([_i64, _i64, _i64, _int, _i64], _i64),
@@ -58,12 +59,15 @@ def _adapters(x, ids, a, b, scale):
     dev = x.device
     if not isinstance(a, torch.Tensor) or a.dim() != 3 or not isinstance(b, torch.Tensor) or b.dim() != 3:
         raise SgError("a and b must be GPU tensors [L, r, K] and [L, N, r]")
-    L, r = a.shape[0], a.shape[1]
-    N = b.shape[1]
-    if min(L, r, N) < 1:
+    L, r, Ka = a.shape
+    Lb, N, rb = b.shape
+    if L < 1 or r < 1 or N < 1:
         raise SgError(f"L, r and N must be at least 1, got {L}, {r} and {N}")
-    pa = _rows(a, "a", torch.bfloat16, (L, r, K), dev)
-    pb = _rows(b, "b", torch.bfloat16, (L, N, r), dev)
+    if not (a.is_cuda and a.dtype is torch.bfloat16 and Ka == K and a.is_contiguous() and a.device == dev):
+        _refuse(a, "a", _BF, (L, r, K), dev)
+    if not (b.is_cuda and b.dtype is torch.bfloat16 and Lb == L and rb == r and b.is_contiguous() and b.device == dev):
+        _refuse(b, "b", _BF, (L, N, r), dev)
+    pa, pb = a.data_ptr(), b.data_ptr()
     pi = None if ids is None else _rows(ids, "ids", torch.int32, (T,), dev)
     ps = None if scale is None else _rows(scale, "scale", torch.float32, (L,), dev)
     return T, K, N, r, L, ldx, pi, pa, pb, ps
@@ -103,9 +107,9 @@ def lora_gemm(x, ids, a, b, scale=None, base=None, out_dtype=torch.bfloat16, y=N
     if need:
         workspace = _space(workspace, need, x)
         pw, wn = workspace.data_ptr(), workspace.numel()
-    st = _lib().sg_lora_gemm(T, K, N, r, L, x.data_ptr(), ldx, pi, pa, pb, ps,
-                             None if base is None else base.data_ptr(), 0 if base is None else _CODE[base.dtype], ldb,
-                             y.data_ptr(), _CODE[y.dtype], ldy, pw, wn, _current_stream(x))
+    st = _launch(x, _lib().sg_lora_gemm, T, K, N, r, L, x.data_ptr(), ldx, pi, pa, pb, ps,
+                 None if base is None else base.data_ptr(), 0 if base is None else _CODE[base.dtype], ldb, y.data_ptr(),
+                 _CODE[y.dtype], ldy, pw, wn)
     if st:
         _check(st, "sg_lora_gemm")
     return y
@@ -143,10 +147,9 @@ def lora_gemm_backward(dy, x, ids, a, b, scale=None, base=None, need_dx: bool = 
     if pdx is None and pda is None:
         return None, None, None
     workspace = _space(workspace, _need(True, T, K, N, r, L), x)
-    st = _lib().sg_lora_gemm_backward(T, K, N, r, L, dy.data_ptr(), ld_dy, x.data_ptr(), ldx, pi, pa, pb, ps,
-                                      None if base is None else base.data_ptr(), ldb, pdx, ldd, pda, pdb,
-                                      0 if pda is None else _CODE[da.dtype], workspace.data_ptr(), workspace.numel(),
-                                      _current_stream(x))
+    st = _launch(x, _lib().sg_lora_gemm_backward, T, K, N, r, L, dy.data_ptr(), ld_dy, x.data_ptr(), ldx, pi, pa, pb, ps,
+                 None if base is None else base.data_ptr(), ldb, pdx, ldd, pda, pdb, 0 if pda is None else _CODE[da.dtype],
+                 workspace.data_ptr(), workspace.numel())
     if st:
         _check(st, "sg_lora_gemm_backward")
     return dx, da, db

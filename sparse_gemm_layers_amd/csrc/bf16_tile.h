@@ -88,10 +88,13 @@ struct KcOp {
   int K, wave, l;
   v4i r[Row::MATS];     // where the next block's loads are
   uint32_t cur[U];
-  int soff;
+  int soff, step;
   // Block k of segment seg is next; none: nothing but zeros is.
   __device__ __forceinline__ void place(int k, int seg, int KB, bool none) {
-    soff = none ? 0 : k * 128;   // an empty descriptor takes no scalar offset: the range check subtracts that from its size
+    // an empty descriptor takes no scalar offset, nor do those after it: the range check
+    // subtracts that from its size
+    soff = none ? 0 : k * 128;
+    step = none ? 0 : 128;
     const int c = 8 * ((l & 7) ^ swz8q(l >> 3));   // k of this lane's piece of 16 bytes
     const bool out = k * 64 + c >= K;
 #pragma unroll
@@ -107,7 +110,7 @@ struct KcOp {
   }
   template <int N, int AT>
   __device__ __forceinline__ void load(uint32_t base) const { lds_dma16<AT>(r[Row::sel(N)], cur[N], soff, base); }
-  __device__ __forceinline__ void next() { soff += 128; }
+  __device__ __forceinline__ void next() { soff += step; }
 };
 
 // One wave's loads of a KS operand of B columns.  p[seg], ld[seg]: row k = 0, the

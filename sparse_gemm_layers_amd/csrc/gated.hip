@@ -453,28 +453,28 @@ static void launch_gated(const GatedArgs& a, hipStream_t st) {
 }
 
 // How dX and dW are computed: tiles of 256 (one a compute unit) or 128 (two), and parts of
-// dX's sum over 2 F.  By the time of the rounds of tiles, us a block of 64 k as above and
-// for a tile's start and end, and that of writing, reading and adding the parts.
+// dX's sum over 2 F.  By the time until all workgroups are through, the longest one's at
+// least (us a block of 64 k as above and for a tile's start and end), and that of writing,
+// reading and adding the parts.  With the many shorter workgroups of dW behind them, dX's
+// need no parts to fill the card: 2048 x 11008 x 4096, 2 parts and their sum 591 us, none 560.
 struct GradPlan {
   bool big;
   int splits;
-  static double rounds(bool b, int64_t tiles, int64_t blocks) {
-    if (b) return (double)cdiv(tiles, 256) * (1.2 * blocks + 8.0);
-    return tiles <= 256 ? 0.9 * blocks + 4.0 : (double)cdiv(tiles, 512) * (1.1 * blocks + 6.0);
-  }
-  static int64_t dx_tiles(bool b, int64_t T, int64_t D) {
-    return b ? cdiv(T, 256) * cdiv(D, 256) : cdiv(T, 128) * cdiv(D, 128);
-  }
-  static int64_t dw_tiles(bool b, int64_t F, int64_t D) {
-    return b ? 2 * cdiv(F, 256) * cdiv(D, 256) : 2 * cdiv(F, 128) * cdiv(D, 128);
-  }
-  GradPlan(int64_t T, int64_t F, int64_t D) {
+  GradPlan(int64_t T, int64_t F, int64_t D, bool dw) {
     const int64_t blocks = 2 * cdiv(F, 64);
     double best = 1e30;
     for (int b = 0; b < 2; ++b) {
-      const double dw = rounds(b, dw_tiles(b, F, D), cdiv(T, 64));
+      const int64_t t = b ? 256 : 128, nx = cdiv(T, t) * cdiv(D, t), nw = dw ? 2 * cdiv(F, t) * cdiv(D, t) : 0;
       for (int s = 1; s <= 32 && (s == 1 || 4 * s <= blocks); ++s) {
-        const double us = rounds(b, dx_tiles(b, T, D) * s, cdiv(blocks, s)) + dw + (s > 1 ? 3.0 + 8.0 * s * T * D / 5e6 : 0.0);
+        const int64_t all = nx * s + nw, slots = b ? 256 : 512;
+        const double block = b ? 1.2 : all <= 256 ? 0.9 : 1.1, ends = b ? 8.0 : 6.0;
+        const double x = cdiv(blocks, s) * block + ends, w = dw ? cdiv(T, 64) * block + ends : 0.0;
+        double us = x > w ? x : w;
+        if (all > slots) {
+          const double shared = (nx * s * x + nw * w) / slots + 0.5 * (dw ? w : x);
+          if (shared > us) us = shared;
+        }
+        if (s > 1) us += 3.0 + 8.0 * s * T * D / 5e6;
         if (us < best) best = us, big = b, splits = s;
       }
     }
@@ -522,7 +522,8 @@ extern "C" sg_status sg_gated_gemm(int64_t T, int64_t F, int64_t D, const uint16
 
 extern "C" int64_t sg_gated_gemm_backward_workspace(int64_t T, int64_t F, int64_t D) {
   if (!gated_back_ok(T, F, D)) return -1;
-  return GradPlan(T, F, D).bytes(T, D);
+  const int64_t with = GradPlan(T, F, D, true).bytes(T, D), without = GradPlan(T, F, D, false).bytes(T, D);
+  return with > without ? with : without;
 }
 
 extern "C" sg_status sg_gated_gemm_backward(int64_t T, int64_t F, int64_t D, const uint16_t* dh, int64_t ld_dh,
@@ -540,7 +541,7 @@ extern "C" sg_status sg_gated_gemm_backward(int64_t T, int64_t F, int64_t D, con
       (g && !ld_ok(ld_gu, F)) || (add && !ld_ok(ld_add, F)) || !ld_ok(ld_dgu, F) || (dx && !ld_ok(ld_dx, D)) ||
       (dgate && !ld_ok(ld_dw, D)))
     return SG_ERR_SHAPE;
-  const GradPlan plan(T, F, D);
+  const GradPlan plan(T, F, D, dgate != nullptr);
   const int64_t need = dx ? plan.bytes(T, D) : 0;
   if (need && !workspace) return SG_ERR_NULL;
   if (need > workspace_bytes) return SG_ERR_SHAPE;
