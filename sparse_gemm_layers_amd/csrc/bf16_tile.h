@@ -13,13 +13,18 @@
 // two in the largest tile, which leave no LDS; more in those that few workgroups share out,
 // where a block's way from memory is longer than its product.)
 //
-// A wave first takes a step's operands from LDS and asks for what comes blocks later,
-// then multiplies.  With 8 waves those of the second half, one to a SIMD as those of the
-// first, go one phase behind: while one wave of a SIMD multiplies the other reads.
-// Both kept going at once, with operands read ahead, is no faster (2048 x 14336 x 4096
-// forward 400 us for 383), and one wave a SIMD with 128 x 128 results of its own, which
+// LAG: a wave first takes a step's operands from LDS and asks for what comes blocks later,
+// then multiplies; the second half of the 8 waves, one to a SIMD as those of the first, goes
+// one phase behind: while one wave of a SIMD multiplies the other reads.  In the largest
+// tiles both kept going at once, with operands read ahead, is no faster (2048 x 14336 x
+// 4096 forward 400 us for 383), and one wave a SIMD with 128 x 128 results of its own, which
 // reads a third less from LDS, has its sums moved about by the compiler (690).
-// What is left: the card's power.  It holds 1.75 to 1.9 GHz under this load, with the
+// Without LAG a wave takes a whole block's operands at once and there is one barrier a block: better where
+// products are short (40 x 1000 x 8000 in tiles of 64 28 us for 38, 128 x 11008 x 4096 in tiles of 128 with the
+// weights in the cache 37 for 43), no better with 256 (256 x 11008 x 4096 65 for 63).
+// What bounds a block is LDS: a KB written by a load or read costs it 8 cycles (measured), so 128 x
+// 128 takes 1024 cycles (0.45 us a block), 128 x 256 1408 (0.60), 256 x 256 2048, as its products do.
+// What is left in the largest: the card's power.  It holds 1.75 to 1.9 GHz under this load, with the
 // matrix cores busy in 70% of the cycles of a full round; without the loads it is 80% at
 // 2.05 GHz, and a product of the library's with nothing fused runs at 1.78 GHz.
 //
@@ -147,15 +152,16 @@ struct KsOp {
 };
 #endif  // SG_DEVICE_PASS
 
-// WN x WM waves of NI x MJ sub-tiles each; SL and SR places for blocks of the operands.
+// WN x WM waves of NI x MJ sub-tiles each; SL and SR places for blocks of the operands (a wait
+// counts loads in their order: one operand further ahead than the other by two would gain nothing).
 // LRow: the left operand's rows, where it is KC.
-template <bool LKS_, bool RKS_, int WN_, int WM_, int NI_, int MJ_, int SL_, int SR_, typename LRow = void>
+template <bool LKS_, bool RKS_, bool LAG_, int WN_, int WM_, int NI_, int MJ_, int SL_, int SR_, typename LRow = void>
 struct Bf16Tile {
   static constexpr bool LKS = LKS_, RKS = RKS_;
   static constexpr int WN = WN_, WM = WM_, NI = NI_, MJ = MJ_, NW = WN * WM;
-  static constexpr bool LAG = NW == 8;
+  static constexpr bool LAG = LAG_;
   static constexpr int SL = SL_, SR = SR_;
-  static_assert(NI % 2 == 0 && (!RKS || MJ % 2 == 0) && SL >= 2 && SR >= 2, "pairs of sub-tiles, places");
+  static_assert(NI % 2 == 0 && (!RKS || MJ % 2 == 0) && SR >= 2 && (SL == SR || SL == SR + 1), "pairs of sub-tiles, places");
   static constexpr int BN = WN * NI * 16, BM = WM * MJ * 16;
   static constexpr int L_BLOCK = BN * 128, R_BLOCK = BM * 128, R_OFF = SL * L_BLOCK, LDS = R_OFF + SR * R_BLOCK;
   static constexpr int LU = BN / 8 / NW, RU = BM / 8 / NW;   // loads of one wave and block
@@ -249,6 +255,26 @@ struct Bf16Tile {
     if (LAG && wave >= NW / 2) lds_barrier();   // from here on a phase behind
     v4i fl[NI], fr[MJ];
     int lread = 0, rread = 0, lfill = (SL - 1) * L_BLOCK, rfill = (SR - 1) * R_BLOCK;   // places in the rings
+    // Block c + SR - 1 of the right operand, c + SL - 1 of the left one, zeros past the end,
+    // into the places of block c - 1; then on to block c + 1.
+    const auto fill_r = [&]() {
+      const uint32_t to = rbase + rfill;
+      unroll<RU>([&](auto n) { ro.template load<n, 1024 * NW * n>(to); });
+      fr_.next();
+      rfill = rfill == (SR - 1) * R_BLOCK ? 0 : rfill + R_BLOCK;
+    };
+    const auto fill_l = [&]() {
+      const uint32_t to = lbase + lfill;
+      unroll<LU>([&](auto n) { lo.template load<n, 1024 * NW * n>(to); });
+      fl_.next();
+      lfill = lfill == (SL - 1) * L_BLOCK ? 0 : lfill + L_BLOCK;
+      lread = lread == (SL - 1) * L_BLOCK ? 0 : lread + L_BLOCK;
+      rread = rread == (SR - 1) * R_BLOCK ? 0 : rread + R_BLOCK;
+#pragma unroll
+      for (int p = 0; p < LP; ++p) lat[p] = la[p] + lread;
+#pragma unroll
+      for (int p = 0; p < RP; ++p) rat[p] = ra[p] + rread;
+    };
     // Step q of block c: its operands from LDS; then the right operand of block c + SR - 1
     // (q = 0) or the left one of block c + SL - 1 (q = 1), zeros past the end, is asked for.
     const auto step = [&](auto qq) {
@@ -258,21 +284,9 @@ struct Bf16Tile {
 #pragma unroll
       for (int i = 0; i < NI; ++i) fl[i] = read_l(q, i);
       if constexpr (q == 0) {
-        const uint32_t to = rbase + rfill;
-        unroll<RU>([&](auto n) { ro.template load<n, 1024 * NW * n>(to); });
-        fr_.next();
-        rfill = rfill == (SR - 1) * R_BLOCK ? 0 : rfill + R_BLOCK;
+        fill_r();
       } else {
-        const uint32_t to = lbase + lfill;
-        unroll<LU>([&](auto n) { lo.template load<n, 1024 * NW * n>(to); });
-        fl_.next();
-        lfill = lfill == (SL - 1) * L_BLOCK ? 0 : lfill + L_BLOCK;
-        lread = lread == (SL - 1) * L_BLOCK ? 0 : lread + L_BLOCK;
-        rread = rread == (SR - 1) * R_BLOCK ? 0 : rread + R_BLOCK;
-#pragma unroll
-        for (int p = 0; p < LP; ++p) lat[p] = la[p] + lread;
-#pragma unroll
-        for (int p = 0; p < RP; ++p) rat[p] = ra[p] + rread;
+        fill_l();
         w4_wait<FLY>();   // own loads of the next block have landed
       }
       lds_barrier();
@@ -283,12 +297,35 @@ struct Bf16Tile {
         for (int j = 0; j < MJ; ++j) acc[i][j] = w4_mfma(fl[i], fr[j], acc[i][j]);
       __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
-      if (LAG) lds_barrier();
+      lds_barrier();
       __builtin_amdgcn_sched_barrier(0);
     };
-    for (int left = kb1 - kb0; left > 0; --left) {
-      step(std::integral_constant<int, 0>{});
-      step(std::integral_constant<int, 1>{});
+    if constexpr (LAG) {
+      for (int left = kb1 - kb0; left > 0; --left) {
+        step(std::integral_constant<int, 0>{});
+        step(std::integral_constant<int, 1>{});
+      }
+    } else {
+      for (int left = kb1 - kb0; left > 0; --left) {
+        v4i l2[2][NI], r2[2][MJ];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+          for (int j = 0; j < MJ; ++j) r2[q][j] = read_r(q, j);
+#pragma unroll
+          for (int i = 0; i < NI; ++i) l2[q][i] = read_l(q, i);
+        }
+        fill_r();
+        fill_l();
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < MJ; ++j) acc[i][j] = w4_mfma(l2[q][i], r2[q][j], acc[i][j]);
+        w4_wait<FLY>();   // own loads of the next block have landed
+        lds_barrier();
+      }
     }
     if (LAG && wave < NW / 2) lds_barrier();   // of the others' last phase
     w4_wait<0>();   // the zeros past the end too, before LDS is given up

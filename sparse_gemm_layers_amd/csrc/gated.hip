@@ -414,11 +414,11 @@ __global__ void __launch_bounds__(256) k_gated_dx_join(GatedGradArgs a) {
 }
 
 // Tiles of n x m, their waves, and blocks of k in LDS.
-template <bool L, bool R, typename Row = PlainRow<8>> using TileA = Bf16Tile<L, R, 2, 4, 8, 4, 3, 2, Row>;   // 256 x 256
-template <bool L, bool R, typename Row = PlainRow<8>> using TileC = Bf16Tile<L, R, 2, 4, 4, 4, 3, 3, Row>;   // 128 x 256
-template <bool L, bool R, typename Row = PlainRow<8>> using TileB = Bf16Tile<L, R, 2, 4, 4, 2, 5, 5, Row>;   // 128 x 128
-template <bool L, bool R, typename Row = PlainRow<8>> using TileE = Bf16Tile<L, R, 2, 4, 4, 2, 3, 2, Row>;   // 128 x 128, two a unit
-template <bool L, bool R, typename Row = PlainRow<4>> using TileD = Bf16Tile<L, R, 1, 4, 4, 1, 5, 5, Row>;   // 64 x 64, two a unit
+template <bool L, bool R, typename Row = PlainRow<8>> using TileA = Bf16Tile<L, R, true, 2, 4, 8, 4, 3, 2, Row>;   // 256 x 256
+template <bool L, bool R, typename Row = PlainRow<8>> using TileC = Bf16Tile<L, R, true, 2, 4, 4, 4, 3, 3, Row>;   // 128 x 256
+template <bool L, bool R, typename Row = PlainRow<8>> using TileB = Bf16Tile<L, R, false, 2, 4, 4, 2, 5, 5, Row>;   // 128 x 128
+template <bool L, bool R, typename Row = PlainRow<8>> using TileE = Bf16Tile<L, R, false, 2, 4, 4, 2, 3, 2, Row>;   // 128 x 128, two a unit
+template <bool L, bool R, typename Row = PlainRow<4>> using TileD = Bf16Tile<L, R, false, 1, 4, 4, 1, 5, 5, Row>;   // 64 x 64, two a unit
 
 template <bool BACK>
 static void launch_gated_rows(const GatedArgs& a, hipStream_t st) {
@@ -433,10 +433,10 @@ static void launch_gated_tile(const GatedArgs& a, hipStream_t st) {
 
 // Which tiles: a block of 64 k takes a workgroup about as long however many others there
 // are, until they take turns.  us a block, in hundredths: 256 x 256 127, 128 x 256 93,
-// 128 x 128 80, 64 x 64 50 (one a compute unit) or 73 (two).  Measured, us, tiles in
-// that order: 128 x 11008 x 4096 79 / 60 / 52 / 61; 256 tokens 81 / 62 / 85 / 95; 512 95 / 115 /
-// 125 / 167; 1024 168 / 176 / 240 / 320; 333 x 2760 x 1032 31 / 20 / 16 / 19; 64 x 5512 x 2040 51 /
-// 31 / 27 / 20; 37 x 14336 x 4096 77 / 62 / 50 / 47.
+// 128 x 128 75, 64 x 64 50 (one a compute unit) or 73 (two).  Measured, us, tiles in
+// that order: 128 x 11008 x 4096 79 / 58 / 51 / 61; 256 tokens 81 / 63 / 85 / 94; 512 96 / 114 /
+// 121 / 166; 1024 x 4096 x 4096 80 / 65 / 82 / 121; 333 x 2760 x 1032 30 / 20 / 16 / 18; 200 x 2000 x
+// 3000 58 / 41 / 31 / 18; 64 x 5512 x 2040 51 / 32 / 28 / 20; 64 x 14336 x 4096 - / - / 54 / 53.
 template <bool BACK>
 static void launch_gated(const GatedArgs& a, hipStream_t st) {
   if (a.T <= 16) {
@@ -445,7 +445,7 @@ static void launch_gated(const GatedArgs& a, hipStream_t st) {
   }
   const auto tiles = [&](int bm, int bf) { return cdiv(a.T, bm) * cdiv(a.F, bf); };
   const int64_t A = 127 * cdiv(tiles(256, 128), 256), C = 93 * cdiv(tiles(256, 64), 256);
-  const int64_t B = 80 * cdiv(tiles(128, 64), 256), d = tiles(64, 32), D = d <= 256 ? 50 : 73 * cdiv(d, 512);
+  const int64_t B = 75 * cdiv(tiles(128, 64), 256), d = tiles(64, 32), D = d <= 256 ? 50 : 73 * cdiv(d, 512);
   if (A <= B && A <= C && A <= D) launch_gated_tile<TileA<false, false, GatedRow<8, 8>>, BACK>(a, st);
   else if (C <= B && C <= D) launch_gated_tile<TileC<false, false, GatedRow<4, 8>>, BACK>(a, st);
   else if (B <= D) launch_gated_tile<TileB<false, false, GatedRow<4, 8>>, BACK>(a, st);
@@ -457,6 +457,10 @@ static void launch_gated(const GatedArgs& a, hipStream_t st) {
 // least (us a block of 64 k as above and for a tile's start and end), and that of writing,
 // reading and adding the parts.  With the many shorter workgroups of dW behind them, dX's
 // need no parts to fill the card: 2048 x 11008 x 4096, 2 parts and their sum 591 us, none 560.
+// The constants are those with which the choice is closest to the best one measured, 1.5% on
+// average over 23 sizes with and without dW (20 x 512 x 1000 to 2048 x 11008 x 4096; 64 x 11008 x
+// 4096 the furthest, 100 us for 98).  333 x 2760 x 1032, whole call: 256 with 13 parts 35 us, 128
+// with 8 parts 32, with 1 part 83; 2048 x 4096 x 1024: 256 with 4 parts 78, 128 with 2 93.
 struct GradPlan {
   bool big;
   int splits;
@@ -467,14 +471,14 @@ struct GradPlan {
       const int64_t t = b ? 256 : 128, nx = cdiv(T, t) * cdiv(D, t), nw = dw ? 2 * cdiv(F, t) * cdiv(D, t) : 0;
       for (int s = 1; s <= 32 && (s == 1 || 4 * s <= blocks); ++s) {
         const int64_t all = nx * s + nw, slots = b ? 256 : 512;
-        const double block = b ? 1.2 : all <= 256 ? 0.9 : 1.1, ends = b ? 8.0 : 6.0;
+        const double block = b ? 1.2 : all <= 256 ? 0.8 : 1.0, ends = b ? 12.0 : 5.0;
         const double x = cdiv(blocks, s) * block + ends, w = dw ? cdiv(T, 64) * block + ends : 0.0;
         double us = x > w ? x : w;
         if (all > slots) {
-          const double shared = (nx * s * x + nw * w) / slots + 0.5 * (dw ? w : x);
+          const double shared = (nx * s * x + nw * w) / slots + 0.6 * (dw ? w : x);
           if (shared > us) us = shared;
         }
-        if (s > 1) us += 3.0 + 8.0 * s * T * D / 5e6;
+        if (s > 1) us += 3.0 + 8.0 * s * T * D / 4e6;
         if (us < best) best = us, big = b, splits = s;
       }
     }
