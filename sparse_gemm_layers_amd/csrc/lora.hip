@@ -30,30 +30,45 @@ __device__ __forceinline__ int lora_id(const int32_t* ids, int64_t t, int64_t T,
   return e >= 0 && e < L ? e : -1;
 }
 
-// The items of a block of 64 tokens: lane l holds the adapter of token t0 + l.
+// The items of a block of 64 tokens that are this workgroup's, the first-th and every
+// step-th after it: adapter by adapter, of each 16 TM tokens at a time in their order.  Lane l
+// holds the adapter of token t0 + l.  Every wave goes through all of the block's adapters, so
+// that must be cheap: blocks of 256 tokens, whose items are fuller, made it four times as long
+// (700 tokens of 100 adapters of rank 32, 4096 x 4096: 117 us for 60; 150 of 10, rank 16: 14.3 for
+// 11.8; but 1000 of 16, rank 32, 4096 x 11008: 36 for 54).
+template <int TM>
 struct LoraItems {
-  int id;
-  uint64_t left;
-  int* list;   // 64 in LDS, this wave's own
-  __device__ __forceinline__ void start(const int32_t* ids, int64_t t0, int64_t T, int L, int l, bool none, int* lds) {
+  int id, e, all, at, step;   // the adapter, its tokens; the item, from its first on
+  uint64_t left, m;           // tokens of this and the adapters to come, of this one
+  int* list;                  // in LDS, this wave's own
+  __device__ __forceinline__ void start(const int32_t* ids, int64_t t0, int64_t T, int L, int l, bool none, int first,
+                                        int steps, int* lds) {
     id = lora_id(ids, t0 + l, T, L);
     left = __ballot(t0 + l < T && (none || id >= 0));
+    m = 0;
+    e = -1;
+    all = 0;
+    at = first;
+    step = steps;
     list = lds;
   }
-  // The next adapter (-1: tokens without one) and the number of its tokens, up to 16 TM,
-  // whose places in the block list then holds.
-  template <int TM>
-  __device__ __forceinline__ bool next(int l, int& e, int& n) {
-    if (!left) return false;
-    e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-    const uint64_t m = __ballot(id == e) & left;
-    const int rank = __builtin_popcountll(m & ((1ull << l) - 1));
-    const bool mine = ((m >> l) & 1) && rank < 16 * TM;
-    const uint64_t taken = __ballot(mine);
-    left &= ~taken;
-    n = __builtin_popcountll(taken);
-    if (mine) list[rank] = l;
+  // The next item: its adapter (-1: tokens without one) and number of tokens, whose places
+  // in the block list then holds.
+  __device__ __forceinline__ bool next(int l, int& adapter, int& n) {
+    while (at * (16 * TM) >= all) {
+      at -= (all + 16 * TM - 1) / (16 * TM);
+      left &= ~m;
+      if (!left) return false;
+      e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+      m = __ballot(id == e) & left;
+      all = __builtin_popcountll(m);
+    }
+    const int before = at * (16 * TM), rank = __builtin_popcountll(m & ((1ull << l) - 1)) - before;
+    n = min(all - before, 16 * TM);
+    if (((m >> l) & 1) && rank >= 0 && rank < 16 * TM) list[rank] = l;
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    adapter = e;
+    at += step;
     return true;
   }
 };
@@ -112,14 +127,13 @@ __device__ __forceinline__ void lora_down(const LoraDown& a, uint8_t* lds, int (
   const int rows = (int)min((int64_t)64, a.T - t0);
   const int units = (a.C + 63) >> 6;   // of 64 columns
   const int u0 = (int)((int64_t)units * split / a.splits), u1 = (int)((int64_t)units * (split + 1) / a.splits);
-  LoraItems items;
-  items.start(a.ids, t0, a.T, a.L, l, false, lists[wave]);
+  LoraItems<TM> items;
+  items.start(a.ids, t0, a.T, a.L, l, false, blockIdx.z, gridDim.z, lists[wave]);
   const __amdgpu_buffer_rsrc_t rz = w4_rsrc(a.z + t0 * a.ldz, (uint32_t)(((rows - 1) * a.ldz + a.C) * 2));
   uint8_t *const zl = lds + wave * WAVE, *const wl = zl + 2048 * TM;
   const int put = (l >> 3) * 128 + (((l & 7) ^ swz8q(l >> 3)) << 4);   // of 8 rows of 128 bytes
   int e, n;
-  for (int d = 0; items.next<TM>(l, e, n); ++d) {
-    if (d % gridDim.z != blockIdx.z) continue;
+  while (items.next(l, e, n)) {
     const uint16_t* const w = a.w + (int64_t)e * a.r * a.C;
     // KC: rows of ranks past r are outside; KS: its rows hold all ranks
     const __amdgpu_buffer_rsrc_t rw =
@@ -324,11 +338,10 @@ __device__ __forceinline__ void lora_up(const LoraUp& a, LoraUpLds<KS>& shared, 
   const int64_t t0 = (int64_t)bx * 64;
   const int n0 = (by * 4 + wave) * 64;
   if (n0 >= a.C) return;   // no barrier follows
-  LoraItems items;
-  items.start(a.ids, t0, a.T, a.L, l, a.y != a.base, shared.lists[wave]);
+  LoraItems<TM> items;
+  items.start(a.ids, t0, a.T, a.L, l, a.y != a.base, bz, gz, shared.lists[wave]);
   int e, count;
-  for (int d = 0; items.next<TM>(l, e, count); ++d) {
-    if (d % gz != bz) continue;
+  while (items.next(l, e, count)) {
     int tok[TM];   // of column 16 j + lr, -1: none
     uint4 base[TM][2];
 #pragma unroll
@@ -448,14 +461,13 @@ __global__ void __launch_bounds__(512) k_lora_both(LoraBoth b) {
   const int rows = (int)min((int64_t)64, a.T - t0);
   const int units = (a.C + 63) >> 6;
   const int s0 = blockIdx.y * b.slice, s1 = min(s0 + b.slice, y.C);
-  LoraItems items;
-  items.start(a.ids, t0, a.T, a.L, l, y.y != y.base, lists[wave]);
+  LoraItems<1> items;
+  items.start(a.ids, t0, a.T, a.L, l, y.y != y.base, blockIdx.z, gridDim.z, lists[wave]);
   const __amdgpu_buffer_rsrc_t rz = w4_rsrc(a.z + t0 * a.ldz, (uint32_t)(((rows - 1) * a.ldz + a.C) * 2));
   uint8_t *const zl = lds + wave * WAVE, *const wl = zl + 2048;
   const int put = (l >> 3) * 128 + (((l & 7) ^ swz8q(l >> 3)) << 4);   // of 8 rows of 128 bytes
   int e, n;
-  for (int d = 0; items.next<1>(l, e, n); ++d) {
-    if (d % gridDim.z != blockIdx.z) continue;
+  while (items.next(l, e, n)) {
     const int place0 = items.list[l >> 3], place1 = items.list[8 + (l >> 3)];   // of the lane's pieces of rows
     // what the second product reads of memory: adapter rows and base of 64 columns
     const __amdgpu_buffer_rsrc_t r2 = w4_rsrc(y.w + (int64_t)e * a.r * y.C, e >= 0 ? (uint32_t)(a.r * y.C * 2) : 0u);
@@ -782,7 +794,9 @@ __global__ void __launch_bounds__(256) k_lora_sum(LoraSum a, LoraSum b, int a_x,
 #endif
 }
 
-// The parts of both gradients, added in order.  n: values of one part, of dA then dB.
+// The parts of both gradients, added in order.  (With dx's workgroups here, behind these,
+// and not beside the sums: 4096 x 4096 x 4096, rank 16 57 us for 58, but two of rank 64 92 for 77.)
+// n: values of one part, of dA then dB.
 struct LoraJoin {
   const float* sums[2];
   void* out[2];
