@@ -4,7 +4,8 @@ linear-layer GEMMs for AMD Instinct MI355X (gfx950).
 A thin Python binding over the C ABI of ``libsg.so`` (declared in
 ``include/sg.h``; the measurement helpers in ``include/sg_probe.h``; the
 mixture-of-experts operators in ``sparse_gemm_layers_amd/include/sg_moe.h``, the
-gated projections in ``sg_gated.h`` beside it, the low-rank adapters in ``sg_lora.h``).  The functions only marshal arguments: PyTorch supplies
+gated projections in ``sg_gated.h`` beside it, the low-rank adapters in
+``sg_lora.h``).  The functions only marshal arguments: PyTorch supplies
 device memory and the current HIP stream; every step runs in the library's
 HIP kernels.  There is no CPU fallback: if ``libsg.so`` is missing or the
 tensors are not on a GPU, the call raises.

@@ -140,7 +140,7 @@ def lora_gemm_backward(dy, x, ids, a, b, scale=None, base=None, need_dx: bool = 
     if da is not None or db is not None:
         if da is None or db is None:
             raise SgError("da and db go together")
-        if da.dtype not in _CODE:
+        if not isinstance(da, torch.Tensor) or da.dtype not in _CODE:
             _refuse(da, "da", _FB, (L, r, K), dev)
         pda = _rows(da, "da", da.dtype, (L, r, K), dev)
         pdb = _rows(db, "db", da.dtype, (L, N, r), dev)

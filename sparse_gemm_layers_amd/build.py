@@ -9,7 +9,8 @@ _build/san/libsg_hostsan.so, whose HOST code (argument checks, launch set-up)
 is instrumented with AddressSanitizer and UndefinedBehaviorSanitizer; device
 code is built as usual and not instrumented.  Load it with the sanitizer
 runtime preloaded (HOST_SANITIZER_RUNTIME) and SG_LIBRARY pointing at it; the
-CPU-only ABI tests run that way (tests/test_abi_sanitized.py, test_moe_abi_sanitized.py).
+CPU-only ABI tests run that way (tests/test_abi_sanitized.py, test_moe_abi_sanitized.py,
+test_adapt_abi_sanitized.py).
 """
 import concurrent.futures
 import glob

@@ -307,6 +307,8 @@ def test_shapes_of_the_backward_pass_reach_every_way():
     lambda t: sg.lora_gemm_backward(t(4, 8), t(4, 16), None, t(2, 8, 16), t(2, 16, 8)),
     lambda t: sg.lora_gemm_backward(t(4, 16), t(4, 16), None, t(2, 8, 16), t(2, 16, 8), da=t(2, 8, 16)),
     lambda t: sg.lora_gemm_backward(t(4, 16), t(4, 16), None, t(2, 8, 16), t(2, 16, 8), grad_dtype=torch.float16),
+    lambda t: sg.lora_gemm_backward(t(4, 16), t(4, 16), None, t(2, 8, 16), t(2, 16, 8), da=1, db=1),
+    lambda t: sg.lora_gemm_backward(t(4, 16), t(4, 16), None, t(2, 8, 16), t(2, 16, 8), da=t(2, 8, 16), db=t(2, 16, 8).float()),
 ])
 def test_refusals(call):
     with pytest.raises(sg.SgError):
