@@ -6,8 +6,8 @@ import functools
 import torch
 
 from ._binding import SgError, _FB, _check, _i64, _int, _ptr, lib
-from ._gated import _launch
-from ._moe import _BF, _CODE, _matrix, _refuse, _result, _rows
+from ._gated import _at, _launch, _ld, _space
+from ._moe import _BF, _CODE, _matrix, _refuse
 
 _SIGS = {
     "sg_lora_gemm_workspace": ([_i64, _i64, _i64, _int, _i64], _i64),
@@ -54,32 +54,19 @@ def _need(back, t, k, n, r, l):
 
 
 def _adapters(x, ids, a, b, scale):
-    """(T, K, N, r, L, row stride of x, addresses of ids, a, b and scale)."""
+    """(T, K, N, r, L, row stride of x, addresses of ids, a, b and scale, index of their GPU)."""
     T, K, ldx = _matrix(x, "x", _BF)
-    dev = x.device
+    dev = x.get_device()
     if not isinstance(a, torch.Tensor) or a.dim() != 3 or not isinstance(b, torch.Tensor) or b.dim() != 3:
         raise SgError("a and b must be GPU tensors [L, r, K] and [L, N, r]")
-    L, r, Ka = a.shape
-    Lb, N, rb = b.shape
+    L, r, _ = a.shape
+    N = b.shape[1]
     if L < 1 or r < 1 or N < 1:
         raise SgError(f"L, r and N must be at least 1, got {L}, {r} and {N}")
-    if not (a.is_cuda and a.dtype is torch.bfloat16 and Ka == K and a.is_contiguous() and a.device == dev):
-        _refuse(a, "a", _BF, (L, r, K), dev)
-    if not (b.is_cuda and b.dtype is torch.bfloat16 and Lb == L and rb == r and b.is_contiguous() and b.device == dev):
-        _refuse(b, "b", _BF, (L, N, r), dev)
-    pa, pb = a.data_ptr(), b.data_ptr()
-    pi = None if ids is None else _rows(ids, "ids", torch.int32, (T,), dev)
-    ps = None if scale is None else _rows(scale, "scale", torch.float32, (L,), dev)
-    return T, K, N, r, L, ldx, pi, pa, pb, ps
-
-
-def _space(workspace, need, x):
-    if workspace is None:
-        return x.new_empty(need, dtype=torch.uint8)
-    if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or not workspace.is_contiguous() \
-            or workspace.numel() < need or workspace.device != x.device:
-        raise SgError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {x.device}")
-    return workspace
+    pa, pb = _at(a, "a", torch.bfloat16, (L, r, K), dev), _at(b, "b", torch.bfloat16, (L, N, r), dev)
+    pi = None if ids is None else _at(ids, "ids", torch.int32, (T,), dev)
+    ps = None if scale is None else _at(scale, "scale", torch.float32, (L,), dev)
+    return T, K, N, r, L, ldx, pi, pa, pb, ps, dev
 
 
 def lora_gemm(x, ids, a, b, scale=None, base=None, out_dtype=torch.bfloat16, y=None, workspace=None):
@@ -93,21 +80,20 @@ def lora_gemm(x, ids, a, b, scale=None, base=None, out_dtype=torch.bfloat16, y=N
     inner product included; y is rounded once.  workspace: uint8, at least
     lora_gemm_workspace(T, K, N, r, L) bytes where that is not 0 (allocated if not
     given; keep it to one stream)."""
-    T, K, N, r, L, ldx, pi, pa, pb, ps = _adapters(x, ids, a, b, scale)
-    dev = x.device
-    ldb = 0 if base is None else _result(base, "base", _FB, (T, N), dev)
+    T, K, N, r, L, ldx, pi, pa, pb, ps, dev = _adapters(x, ids, a, b, scale)
+    ldb = 0 if base is None else _ld(base, "base", _FB, (T, N), dev)
     if y is None:
         if out_dtype not in _CODE:
             raise SgError(f"out_dtype {out_dtype} not supported (float32 or bfloat16)")
         y = x.new_empty((T, N), dtype=out_dtype)
         ldy = N
     else:
-        ldy = _result(y, "y", _FB, (T, N), dev)
+        ldy = _ld(y, "y", _FB, (T, N), dev)
     need, pw, wn = _need(False, T, K, N, r, L), None, 0
     if need:
-        workspace = _space(workspace, need, x)
+        workspace = _space(workspace, need, x, dev)
         pw, wn = workspace.data_ptr(), workspace.numel()
-    st = _launch(x, _lib().sg_lora_gemm, T, K, N, r, L, x.data_ptr(), ldx, pi, pa, pb, ps,
+    st = _launch(dev, _lib().sg_lora_gemm, T, K, N, r, L, x.data_ptr(), ldx, pi, pa, pb, ps,
                  None if base is None else base.data_ptr(), 0 if base is None else _CODE[base.dtype], ldb, y.data_ptr(),
                  _CODE[y.dtype], ldy, pw, wn)
     if st:
@@ -125,29 +111,32 @@ def lora_gemm_backward(dy, x, ids, a, b, scale=None, base=None, need_dx: bool = 
     grad_dtype, are sums over the adapter's own tokens, zeros where it has none.
     workspace: uint8, at least lora_gemm_backward_workspace(T, K, N, r, L) bytes
     (allocated if not given; keep it to one stream)."""
-    T, K, N, r, L, ldx, pi, pa, pb, ps = _adapters(x, ids, a, b, scale)
-    dev = x.device
-    ld_dy = _result(dy, "dy", _BF, (T, N), dev)
-    ldb = 0 if base is None else _result(base, "base", _BF, (T, K), dev)
+    T, K, N, r, L, ldx, pi, pa, pb, ps, dev = _adapters(x, ids, a, b, scale)
+    ld_dy = _ld(dy, "dy", _BF, (T, N), dev)
+    ldb = 0 if base is None else _ld(base, "base", _BF, (T, K), dev)
     if grad_dtype not in _CODE:
         raise SgError(f"grad_dtype {grad_dtype} not supported (float32 or bfloat16)")
-    if need_dx and dx is None:
+    pdx, ldd = None, K
+    if dx is not None:
+        ldd, pdx = _ld(dx, "dx", _BF, (T, K), dev), dx.data_ptr()
+    elif need_dx:
         dx = x.new_empty((T, K))
-    if need_dab and da is None and db is None:
-        da, db = x.new_empty((L, r, K), dtype=grad_dtype), x.new_empty((L, N, r), dtype=grad_dtype)
-    pdx, ldd = (None, 0) if dx is None else (dx.data_ptr(), _result(dx, "dx", _BF, (T, K), dev))
+        pdx = dx.data_ptr()
     pda = pdb = None
     if da is not None or db is not None:
         if da is None or db is None:
             raise SgError("da and db go together")
         if not isinstance(da, torch.Tensor) or da.dtype not in _CODE:
-            _refuse(da, "da", _FB, (L, r, K), dev)
-        pda = _rows(da, "da", da.dtype, (L, r, K), dev)
-        pdb = _rows(db, "db", da.dtype, (L, N, r), dev)
+            _refuse(da, "da", _FB, (L, r, K), x.device)
+        pda = _at(da, "da", da.dtype, (L, r, K), dev)
+        pdb = _at(db, "db", da.dtype, (L, N, r), dev)
+    elif need_dab:
+        da, db = x.new_empty((L, r, K), dtype=grad_dtype), x.new_empty((L, N, r), dtype=grad_dtype)
+        pda, pdb = da.data_ptr(), db.data_ptr()
     if pdx is None and pda is None:
         return None, None, None
-    workspace = _space(workspace, _need(True, T, K, N, r, L), x)
-    st = _launch(x, _lib().sg_lora_gemm_backward, T, K, N, r, L, dy.data_ptr(), ld_dy, x.data_ptr(), ldx, pi, pa, pb, ps,
+    workspace = _space(workspace, _need(True, T, K, N, r, L), x, dev)
+    st = _launch(dev, _lib().sg_lora_gemm_backward, T, K, N, r, L, dy.data_ptr(), ld_dy, x.data_ptr(), ldx, pi, pa, pb, ps,
                  None if base is None else base.data_ptr(), ldb, pdx, ldd, pda, pdb, 0 if pda is None else _CODE[da.dtype],
                  workspace.data_ptr(), workspace.numel())
     if st:
