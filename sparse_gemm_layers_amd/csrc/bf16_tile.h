@@ -153,7 +153,9 @@ struct KsOp {
 #endif  // SG_DEVICE_PASS
 
 // WN x WM waves of NI x MJ sub-tiles each; SL and SR places for blocks of the operands (a wait
-// counts loads in their order: one operand further ahead than the other by two would gain nothing).
+// counts loads in their order: one operand further ahead than the other by two would gain nothing.
+// With each operand loaded by half of the waves, the weights four to seven blocks ahead: 128 x 11008 x
+// 4096 53 us for 52, 256 tokens 67 for 62).
 // LRow: the left operand's rows, where it is KC.
 template <bool LKS_, bool RKS_, bool LAG_, int WN_, int WM_, int NI_, int MJ_, int SL_, int SR_, typename LRow = void>
 struct Bf16Tile {
