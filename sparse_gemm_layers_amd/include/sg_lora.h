@@ -21,7 +21,8 @@ extern "C" {
  *   y[t] = base[t] + scale[e] (x[t] . A_e^T) . B_e^T
  * The inner product x . A^T is a fp32 sum and is not rounded: its scaled value
  * enters the second product as a sum of bf16 parts, two for a bf16 y (2^-16 of the
- * value is left out at most), three for a fp32 y (2^-24).
+ * value is left out at most), three for a fp32 y (2^-24).  Infinities and NaN of any operand
+ * go where the formula takes them.
  * A token whose id is outside [0, L) has no adapter: its y is base, or 0.  A row of x
  * reaches its own row of y alone, and no adapter but its own.
  *   x     : bf16 [T, K], leading dim ldx;  ids: int32 [T], or NULL: adapter 0 for all
