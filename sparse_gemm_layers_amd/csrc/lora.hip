@@ -565,8 +565,9 @@ __global__ void __launch_bounds__(512) k_lora_both(LoraBoth b) {
         const int rho = 16 * wave + 4 * g;
         const float scale = y.scale ? y.scale[e] : 1.0f;
         float v[4];
+        // ranks past r are nothing, also where an infinity of x has met their zeros
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = s[k] * scale;
+        for (int k = 0; k < 4; ++k) v[k] = rho < a.r ? s[k] * scale : 0.0f;
         uint32_t p[NP][2];
         lora_parts<NP>(v, p);
 #pragma unroll
