@@ -48,8 +48,9 @@ def lora_gemm_backward_workspace(t: int, k: int, n: int, r: int, l: int) -> int:
 def _need(back, t, k, n, r, l):
     need = (lora_gemm_backward_workspace if back else lora_gemm_workspace)(t, k, n, r, l)
     if need < 0:
+        more = ", and ceil(max(K, N) / 256) (2 L ceil(r / 64) + ceil(T / 64)) under 2^24 - 4096" if back else ""
         raise SgError(f"low-rank adapters: sizes out of range (T = {t}, K = {k}, N = {n}, r = {r}, L = {l}; K, N and r "
-                      "multiples of 8, r at most 256)")
+                      f"multiples of 8, r at most 256, L at most 65535, T, K and N under 2^22{more})")
     return need
 
 

@@ -987,11 +987,13 @@ static void launch_both(LoraBoth b, hipStream_t st) {
 
 static bool lora_shape_ok(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
   if (T < 1 || K < 8 || N < 8 || r < 8 || L < 1 || K % 8 || N % 8 || r % 8) return false;
-  if (T >= (1LL << 22) || K >= (1LL << 22) || N >= (1LL << 22) || r > 256 || L > 65535) return false;
-  // workgroups of the sums and of dx, in one launch (parts of the tokens, and of a block's items,
-  // are only where there are few)
+  return T < (1LL << 22) && K < (1LL << 22) && N < (1LL << 22) && r <= 256 && L <= 65535;
+}
+static bool lora_back_ok(int64_t T, int64_t K, int64_t N, int64_t r, int64_t L) {
+  // workgroups of the sums and of dx, in one launch along x (parts of the tokens, and of a block's
+  // items, are only where there are few)
   const int64_t c = K > N ? K : N;
-  return launch_fits(cdiv(c, 256) * (2 * L * cdiv(r, 64) + cdiv(T, 64)) + 4096, 256);
+  return lora_shape_ok(T, K, N, r, L) && launch_fits(cdiv(c, 256) * (2 * L * cdiv(r, 64) + cdiv(T, 64)) + 4096, 256);
 }
 static bool lora_ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld < (1LL << 22); }
 
@@ -1005,7 +1007,7 @@ extern "C" int64_t sg_lora_gemm_workspace(int64_t T, int64_t K, int64_t N, int r
 }
 
 extern "C" int64_t sg_lora_gemm_backward_workspace(int64_t T, int64_t K, int64_t N, int r, int64_t L) {
-  if (!lora_shape_ok(T, K, N, r, L)) return -1;
+  if (!lora_back_ok(T, K, N, r, L)) return -1;
   return LoraSpace(T, K, N, r, L, true).bytes;
 }
 
@@ -1050,7 +1052,7 @@ extern "C" sg_status sg_lora_gemm_backward(int64_t T, int64_t K, int64_t N, int 
                                            int64_t workspace_bytes, hipStream_t stream) {
   if (!dy || !x || !a || !b || !workspace || (!dx && !da) || !da != !db) return SG_ERR_NULL;
   if (da && grad_dt != SG_F32 && grad_dt != SG_BF16) return SG_ERR_UNSUPPORTED;
-  if (!lora_shape_ok(T, K, N, r, L) || !lora_ld_ok(ldx, K) || !lora_ld_ok(ld_dy, N) || (dx && !lora_ld_ok(ld_dx, K)) ||
+  if (!lora_back_ok(T, K, N, r, L) || !lora_ld_ok(ldx, K) || !lora_ld_ok(ld_dy, N) || (dx && !lora_ld_ok(ld_dx, K)) ||
       (dx && base && !lora_ld_ok(ld_base, K)) || (dx && base == dx && ld_base != ld_dx))
     return SG_ERR_SHAPE;
   const LoraSpace ws(T, K, N, r, L, true);

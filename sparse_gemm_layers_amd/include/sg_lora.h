@@ -61,7 +61,8 @@ sg_status sg_lora_gemm(int64_t T, int64_t K, int64_t N, int r, int64_t L, const 
  *          the shapes of a and b, contiguous, or both NULL
  *   workspace : at least sg_lora_gemm_backward_workspace(T, K, N, r, L) bytes, as above
  * No output may overlap an input, but for dx that is base.
- * Requires what sg_lora_gemm does.
+ * Requires what sg_lora_gemm does, and
+ * ceil(max(K, N) / 256) * (2 L ceil(r / 64) + ceil(T / 64)) < 2^24 - 4096: the workgroups of one launch.
  */
 int64_t sg_lora_gemm_backward_workspace(int64_t T, int64_t K, int64_t N, int r, int64_t L);
 
