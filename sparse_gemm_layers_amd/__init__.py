@@ -55,6 +55,8 @@ from ._gated import (
     gated_gemm,
     gated_gemm_backward_workspace,
     gated_gemm_backward,
+    gated_gemm_plan,
+    gated_gemm_backward_plan,
 )
 from ._lora import (
     lora_gemm_workspace,
@@ -77,5 +79,6 @@ __all__ = [
     "moe_route", "moe_route_backward", "w4_packed_bytes", "w4_pack", "w4a16_gemm_groupwise_packed",
     "w4a16_moe_mlp_workspace", "w4a16_moe_mlp",
     "gated_gemm", "gated_gemm_backward_workspace", "gated_gemm_backward",
+    "gated_gemm_plan", "gated_gemm_backward_plan",
     "lora_gemm_workspace", "lora_gemm", "lora_gemm_backward_workspace", "lora_gemm_backward",
 ]

@@ -1,6 +1,7 @@
 """ctypes binding of the gated projections' entry points of libsg.so
 (``sparse_gemm_layers_amd/include/sg_gated.h``).  Argument marshalling only."""
 
+import ctypes
 import functools
 
 import torch
@@ -15,6 +16,8 @@ _SIGS = {
     "sg_gated_gemm_backward": ([_i64, _i64, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _ptr, _i64, _int, _ptr, _ptr,
                                 _i64, _ptr, _ptr, _i64, _ptr, _ptr, _i64, _ptr, _i64, _ptr, _ptr, _i64, _ptr, _i64,
                                 _ptr], _int),
+    "sg_gated_gemm_plan": ([_i64, _i64, _i64, _ptr, _ptr], _int),
+    "sg_gated_gemm_backward_plan": ([_i64, _i64, _i64, _int, _ptr, _ptr], _int),
 }
 
 _ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
@@ -69,6 +72,15 @@ def _space(workspace, need, x, dev):
             or workspace.numel() < need or workspace.get_device() != dev:
         raise SgError(f"workspace must be a contiguous uint8 tensor of at least {need} bytes on {x.device}")
     return workspace
+
+
+def _plan(name, count, *args):
+    """What plan query `name` says of args: count whole numbers."""
+    out = (ctypes.c_int32 * count)()
+    st = getattr(_lib(), name)(*args, *(ctypes.addressof(out) + 4 * i for i in range(count)))
+    if st:
+        _check(st, name)
+    return tuple(out)
 
 
 def _act_code(act):
@@ -200,3 +212,15 @@ def gated_gemm_backward(dh, x, gate, up, act: str = "silu", g=None, u=None, gate
     if st:
         _check(st, "sg_gated_gemm_backward")
     return dx, dgate, dup, dg, du
+
+
+def gated_gemm_plan(t: int, f: int, d: int):
+    """(tokens, hidden values) of one workgroup of gated_gemm, and of a gated_gemm_backward call
+    that computes G and U again."""
+    return _plan("sg_gated_gemm_plan", 2, t, f, d)
+
+
+def gated_gemm_backward_plan(t: int, f: int, d: int, need_dw: bool = True):
+    """(rows and columns of a gradient that one workgroup computes, parts of dx's sum) of
+    gated_gemm_backward; more than one part take 4 parts T D bytes of workspace."""
+    return _plan("sg_gated_gemm_backward_plan", 2, t, f, d, int(need_dw))

@@ -437,19 +437,23 @@ static void launch_gated_tile(const GatedArgs& a, hipStream_t st) {
 // that order: 128 x 11008 x 4096 79 / 58 / 51 / 61; 256 tokens 81 / 63 / 85 / 94; 512 96 / 114 /
 // 121 / 166; 1024 x 4096 x 4096 80 / 65 / 82 / 121; 333 x 2760 x 1032 30 / 20 / 16 / 18; 200 x 2000 x
 // 3000 58 / 41 / 31 / 18; 64 x 5512 x 2040 51 / 32 / 28 / 20; 64 x 14336 x 4096 - / - / 54 / 53.
-template <bool BACK>
-static void launch_gated(const GatedArgs& a, hipStream_t st) {
-  if (a.T <= 16) {
-    launch_gated_rows<BACK>(a, st);
-    return;
-  }
-  const auto tiles = [&](int bm, int bf) { return cdiv(a.T, bm) * cdiv(a.F, bf); };
+enum GatedWay { GATED_ROWS, GATED_A, GATED_B, GATED_C, GATED_D };
+static GatedWay gated_way(int64_t T, int64_t F) {
+  if (T <= 16) return GATED_ROWS;
+  const auto tiles = [&](int bm, int bf) { return cdiv(T, bm) * cdiv(F, bf); };
   const int64_t A = 127 * cdiv(tiles(256, 128), 256), C = 93 * cdiv(tiles(256, 64), 256);
   const int64_t B = 75 * cdiv(tiles(128, 64), 256), d = tiles(64, 32), D = d <= 256 ? 50 : 73 * cdiv(d, 512);
-  if (A <= B && A <= C && A <= D) launch_gated_tile<TileA<false, false, GatedRow<8, 8>>, BACK>(a, st);
-  else if (C <= B && C <= D) launch_gated_tile<TileC<false, false, GatedRow<4, 8>>, BACK>(a, st);
-  else if (B <= D) launch_gated_tile<TileB<false, false, GatedRow<4, 8>>, BACK>(a, st);
-  else launch_gated_tile<TileD<false, false, GatedRow<4, 4>>, BACK>(a, st);
+  return A <= B && A <= C && A <= D ? GATED_A : C <= B && C <= D ? GATED_C : B <= D ? GATED_B : GATED_D;
+}
+template <bool BACK>
+static void launch_gated(const GatedArgs& a, hipStream_t st) {
+  switch (gated_way(a.T, a.F)) {
+    case GATED_ROWS: return launch_gated_rows<BACK>(a, st);
+    case GATED_A: return launch_gated_tile<TileA<false, false, GatedRow<8, 8>>, BACK>(a, st);
+    case GATED_B: return launch_gated_tile<TileB<false, false, GatedRow<4, 8>>, BACK>(a, st);
+    case GATED_C: return launch_gated_tile<TileC<false, false, GatedRow<4, 8>>, BACK>(a, st);
+    case GATED_D: return launch_gated_tile<TileD<false, false, GatedRow<4, 4>>, BACK>(a, st);
+  }
 }
 
 // How dX and dW are computed: tiles of 256 (one a compute unit) or 128 (two), and parts of
@@ -499,6 +503,25 @@ static bool ld_ok(int64_t ld, int64_t cols) { return ld >= cols && ld < (1LL << 
 }  // namespace sg
 
 using namespace sg;
+
+extern "C" sg_status sg_gated_gemm_plan(int64_t T, int64_t F, int64_t D, int32_t* tokens, int32_t* values) {
+  if (!tokens || !values) return SG_ERR_NULL;
+  if (!gated_shape_ok(T, F, D)) return SG_ERR_SHAPE;
+  const GatedWay way = gated_way(T, F);
+  *tokens = way == GATED_ROWS ? 16 : way == GATED_D ? 64 : way == GATED_B ? 128 : 256;
+  *values = way == GATED_ROWS ? 16 : way == GATED_D ? 32 : way == GATED_A ? 128 : 64;
+  return SG_OK;
+}
+
+extern "C" sg_status sg_gated_gemm_backward_plan(int64_t T, int64_t F, int64_t D, int with_dw, int32_t* tile,
+                                                 int32_t* parts) {
+  if (!tile || !parts) return SG_ERR_NULL;
+  if (!gated_back_ok(T, F, D)) return SG_ERR_SHAPE;
+  const GradPlan plan(T, F, D, with_dw != 0);
+  *tile = plan.big ? 256 : 128;
+  *parts = plan.splits;
+  return SG_OK;
+}
 
 extern "C" sg_status sg_gated_gemm(int64_t T, int64_t F, int64_t D, const uint16_t* x, int64_t ldx,
                                    const uint16_t* gate, int64_t ldg, const uint16_t* up, int64_t ldu, sg_act act,

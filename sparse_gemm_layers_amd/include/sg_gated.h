@@ -67,6 +67,19 @@ sg_status sg_gated_gemm_backward(int64_t T, int64_t F, int64_t D, const uint16_t
                                  uint16_t* dgate, uint16_t* dup, int64_t ld_dw, void* workspace,
                                  int64_t workspace_bytes, hipStream_t stream);
 
+/*
+ * How calls of these sizes go, for tests and measurements; nothing is launched.
+ *   sg_gated_gemm_plan : *tokens and *values, the tokens and hidden values of one workgroup of
+ *       the forward product, and of that product computed again by the backward call
+ *   sg_gated_gemm_backward_plan : *tile, the rows and columns of dx or of a weight's gradient that
+ *       one workgroup computes; *parts, those of dx's sum.  More than one take 4 * parts * T * D
+ *       bytes of workspace; sg_gated_gemm_backward_workspace is the larger of with and without dw.
+ * SG_ERR_NULL, or SG_ERR_SHAPE for sizes that the calls refuse.
+ */
+sg_status sg_gated_gemm_plan(int64_t T, int64_t F, int64_t D, int32_t* tokens, int32_t* values);
+
+sg_status sg_gated_gemm_backward_plan(int64_t T, int64_t F, int64_t D, int with_dw, int32_t* tile, int32_t* parts);
+
 #ifdef __cplusplus
 }
 #endif
