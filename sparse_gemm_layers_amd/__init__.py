@@ -63,6 +63,8 @@ from ._lora import (
     lora_gemm,
     lora_gemm_backward_workspace,
     lora_gemm_backward,
+    lora_gemm_plan,
+    lora_gemm_backward_plan,
 )
 
 __all__ = [
@@ -81,4 +83,5 @@ __all__ = [
     "gated_gemm", "gated_gemm_backward_workspace", "gated_gemm_backward",
     "gated_gemm_plan", "gated_gemm_backward_plan",
     "lora_gemm_workspace", "lora_gemm", "lora_gemm_backward_workspace", "lora_gemm_backward",
+    "lora_gemm_plan", "lora_gemm_backward_plan",
 ]

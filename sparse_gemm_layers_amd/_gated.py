@@ -74,15 +74,6 @@ def _space(workspace, need, x, dev):
     return workspace
 
 
-def _plan(name, count, *args):
-    """What plan query `name` says of args: count whole numbers."""
-    out = (ctypes.c_int32 * count)()
-    st = getattr(_lib(), name)(*args, *(ctypes.addressof(out) + 4 * i for i in range(count)))
-    if st:
-        _check(st, name)
-    return tuple(out)
-
-
 def _act_code(act):
     if act not in _ACTS:
         raise SgError(f"act must be one of {', '.join(map(repr, _ACTS))}, got {act!r}")
@@ -217,10 +208,15 @@ def gated_gemm_backward(dh, x, gate, up, act: str = "silu", g=None, u=None, gate
 def gated_gemm_plan(t: int, f: int, d: int):
     """(tokens, hidden values) of one workgroup of gated_gemm, and of a gated_gemm_backward call
     that computes G and U again."""
-    return _plan("sg_gated_gemm_plan", 2, t, f, d)
+    a, b = ctypes.c_int32(), ctypes.c_int32()
+    _check(_lib().sg_gated_gemm_plan(t, f, d, ctypes.addressof(a), ctypes.addressof(b)), "sg_gated_gemm_plan")
+    return a.value, b.value
 
 
 def gated_gemm_backward_plan(t: int, f: int, d: int, need_dw: bool = True):
     """(rows and columns of a gradient that one workgroup computes, parts of dx's sum) of
     gated_gemm_backward; more than one part take 4 parts T D bytes of workspace."""
-    return _plan("sg_gated_gemm_backward_plan", 2, t, f, d, int(need_dw))
+    a, b = ctypes.c_int32(), ctypes.c_int32()
+    _check(_lib().sg_gated_gemm_backward_plan(t, f, d, int(need_dw), ctypes.addressof(a), ctypes.addressof(b)),
+           "sg_gated_gemm_backward_plan")
+    return a.value, b.value

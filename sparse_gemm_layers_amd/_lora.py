@@ -1,6 +1,7 @@
 """ctypes binding of the low-rank adapters' entry points of libsg.so
 (``sparse_gemm_layers_amd/include/sg_lora.h``).  Argument marshalling only."""
 
+import ctypes
 import functools
 
 import torch
@@ -16,6 +17,8 @@ _SIGS = {
     "sg_lora_gemm_backward_workspace": ([_i64, _i64, _i64, _int, _i64], _i64),
     "sg_lora_gemm_backward": ([_i64, _i64, _i64, _int, _i64, _ptr, _i64, _ptr, _i64, _ptr, _ptr, _ptr, _ptr, _ptr, _i64,
                                _ptr, _i64, _ptr, _ptr, _int, _ptr, _i64, _ptr], _int),
+    "sg_lora_gemm_plan": ([_i64, _i64, _i64, _int, _i64, _ptr], _int),
+    "sg_lora_gemm_backward_plan": ([_i64, _i64, _i64, _int, _i64, _ptr], _int),
 }
 
 _typed = None
@@ -143,3 +146,23 @@ def lora_gemm_backward(dy, x, ids, a, b, scale=None, base=None, need_dx: bool = 
     if st:
         _check(st, "sg_lora_gemm_backward")
     return dx, da, db
+
+
+def _plan(name, fields, t, k, n, r, l):
+    out = (ctypes.c_int32 * len(fields))()
+    _check(getattr(_lib(), name)(t, k, n, r, l, ctypes.addressof(out)), name)
+    return dict(zip(fields, out))
+
+
+def lora_gemm_plan(t: int, k: int, n: int, r: int, l: int):
+    """How lora_gemm goes at these sizes: launches (1: both products in one), tokens of an adapter
+    taken at a time, ranks of a workgroup of x . a^T, parts of its sum."""
+    return _plan("sg_lora_gemm_plan", ("launches", "tokens", "ranks", "parts"), t, k, n, r, l)
+
+
+def lora_gemm_backward_plan(t: int, k: int, n: int, r: int, l: int):
+    """How lora_gemm_backward goes at these sizes: tokens taken at a time and ranks of a workgroup of
+    dy . b and x . a^T, the parts of either sum, ranks of a workgroup of da and db, parts of
+    their tokens."""
+    return _plan("sg_lora_gemm_backward_plan", ("tokens", "ranks", "parts_v", "parts_u", "sum_ranks", "token_parts"), t, k, n,
+                 r, l)

@@ -911,11 +911,16 @@ struct LoraSpace {
   }
 };
 
+// Tokens of a down workgroup's item in 16s.
+static int lora_tm(int64_t T, int64_t r) { return T >= 512 && r > 32 ? 2 : 1; }
 // Ranks of a down workgroup in 16s: more where there are many, so that z is read less often.
 static int lora_rm(int64_t T, int64_t r, int splits) {
   const int64_t tiles = splits * cdiv(T, 16) * cdiv(r, 16);
-  return r <= 16 || tiles <= 256 ? 1 : r <= 32 || tiles <= 512 ? 2 : 4;
+  const int rm = r <= 16 || tiles <= 256 ? 1 : r <= 32 || tiles <= 512 ? 2 : 4;
+  return rm == 1 && lora_tm(T, r) == 2 ? 2 : rm;
 }
+// Of a workgroup of the sums, of one launch for both products.
+static int lora_rm(int64_t r) { return r <= 16 ? 1 : r <= 32 ? 2 : 4; }
 template <int TM, int RM>
 static void launch_down_tm(const LoraDown* v, const LoraDown* u, hipStream_t st) {
   const LoraDown& a = v ? *v : *u;
@@ -930,8 +935,8 @@ static void launch_down_tm(const LoraDown* v, const LoraDown* u, hipStream_t st)
 static void launch_down(const LoraDown* v, const LoraDown* u, hipStream_t st) {
   const LoraDown& a = v ? *v : *u;
   const int rm = lora_rm(a.T, a.r, a.splits);
-  if (a.T >= 512 && a.r > 32) {
-    if (rm <= 2) launch_down_tm<2, 2>(v, u, st);
+  if (lora_tm(a.T, a.r) == 2) {
+    if (rm == 2) launch_down_tm<2, 2>(v, u, st);
     else launch_down_tm<2, 4>(v, u, st);
   } else {
     if (rm == 1) launch_down_tm<1, 1>(v, u, st);
@@ -961,8 +966,9 @@ static void launch_sum(const LoraSum& a, const LoraSum& b, const LoraUp* dx, hip
   const auto sums = [&](int rm) { return LoraGrid{ax + bx, (int)(a.L * cdiv(a.r, 16 * rm)), a.tsplits}; };
   const auto all = [&](int rm) { return (unsigned)(sums(rm).all() + ups.all()); };
   const LoraUp& u = dx ? *dx : none;
-  if (a.r <= 16) k_lora_sum<1, NP><<<all(1), 256, 0, st>>>(a, b, ax, sums(1), u, ups);
-  else if (a.r <= 32) k_lora_sum<2, NP><<<all(2), 256, 0, st>>>(a, b, ax, sums(2), u, ups);
+  const int rm = lora_rm(a.r);
+  if (rm == 1) k_lora_sum<1, NP><<<all(1), 256, 0, st>>>(a, b, ax, sums(1), u, ups);
+  else if (rm == 2) k_lora_sum<2, NP><<<all(2), 256, 0, st>>>(a, b, ax, sums(2), u, ups);
   else k_lora_sum<4, NP><<<all(4), 256, 0, st>>>(a, b, ax, sums(4), u, ups);
 }
 
@@ -980,8 +986,9 @@ static void launch_both(LoraBoth b, hipStream_t st) {
   slices = slices < 1 ? 1 : slices > most ? most : slices;
   b.slice = (int)cdiv(cdiv(b.u.C, 64), slices) * 64;
   const dim3 grid((unsigned)cdiv(T, 64), (unsigned)cdiv(b.u.C, b.slice), (unsigned)items);
-  if (b.d.r <= 16) launch_both_rm<1>(b, grid, st);
-  else if (b.d.r <= 32) launch_both_rm<2>(b, grid, st);
+  const int rm = lora_rm(b.d.r);
+  if (rm == 1) launch_both_rm<1>(b, grid, st);
+  else if (rm == 2) launch_both_rm<2>(b, grid, st);
   else launch_both_rm<4>(b, grid, st);
 }
 
@@ -1009,6 +1016,31 @@ extern "C" int64_t sg_lora_gemm_workspace(int64_t T, int64_t K, int64_t N, int r
 extern "C" int64_t sg_lora_gemm_backward_workspace(int64_t T, int64_t K, int64_t N, int r, int64_t L) {
   if (!lora_back_ok(T, K, N, r, L)) return -1;
   return LoraSpace(T, K, N, r, L, true).bytes;
+}
+
+extern "C" sg_status sg_lora_gemm_plan(int64_t T, int64_t K, int64_t N, int r, int64_t L, int32_t* plan) {
+  if (!plan) return SG_ERR_NULL;
+  if (!lora_shape_ok(T, K, N, r, L)) return SG_ERR_SHAPE;
+  const bool both = lora_both(T, K, r);
+  const int parts = both ? 1 : lora_splits(T, K);
+  plan[0] = both ? 1 : 2;
+  plan[1] = both ? 16 : 16 * lora_tm(T, r);
+  plan[2] = 16 * (both ? lora_rm(r) : lora_rm(T, r, parts));
+  plan[3] = parts;
+  return SG_OK;
+}
+
+extern "C" sg_status sg_lora_gemm_backward_plan(int64_t T, int64_t K, int64_t N, int r, int64_t L, int32_t* plan) {
+  if (!plan) return SG_ERR_NULL;
+  if (!lora_back_ok(T, K, N, r, L)) return SG_ERR_SHAPE;
+  const LoraSpace ws(T, K, N, r, L, true);
+  plan[0] = 16 * lora_tm(T, r);
+  plan[1] = 16 * lora_rm(T, r, ws.sv);
+  plan[2] = ws.sv;
+  plan[3] = ws.su;
+  plan[4] = 16 * lora_rm(r);
+  plan[5] = ws.ts;
+  return SG_OK;
 }
 
 extern "C" sg_status sg_lora_gemm(int64_t T, int64_t K, int64_t N, int r, int64_t L, const uint16_t* x, int64_t ldx,

@@ -72,6 +72,19 @@ sg_status sg_lora_gemm_backward(int64_t T, int64_t K, int64_t N, int r, int64_t 
                                 uint16_t* dx, int64_t ld_dx, void* da, void* db, sg_dtype grad_dt, void* workspace,
                                 int64_t workspace_bytes, hipStream_t stream);
 
+/*
+ * How calls of these sizes go, for tests and measurements; nothing is launched.
+ *   sg_lora_gemm_plan, plan[4] : launches (1: both products in one); tokens of one adapter that
+ *       are taken at a time; ranks of a workgroup of x . A^T; parts of its sum
+ *   sg_lora_gemm_backward_plan, plan[6] : tokens taken at a time and ranks of a workgroup of the
+ *       first launch; parts of dy . B and of x . A^T; ranks of a workgroup of dA and dB; parts
+ *       of their sums over tokens
+ * SG_ERR_NULL, or SG_ERR_SHAPE for sizes that the calls refuse.
+ */
+sg_status sg_lora_gemm_plan(int64_t T, int64_t K, int64_t N, int r, int64_t L, int32_t* plan);
+
+sg_status sg_lora_gemm_backward_plan(int64_t T, int64_t K, int64_t N, int r, int64_t L, int32_t* plan);
+
 #ifdef __cplusplus
 }
 #endif

@@ -3,6 +3,7 @@ import pytest
 
 import sparse_gemm_layers_amd as sg
 import test_gpu_gated_ways as gated
+import test_gpu_lora_ways as lora
 
 
 def test_gated_forward_ways_are_reached():
@@ -21,6 +22,33 @@ def test_gated_backward_ways_are_reached():
         assert gated.backward_way(T, F, D, dw) == way, (T, F, D, dw)
     assert {(dw, way) for *_, dw, way in gated.BACKWARD} == {(d, (t, p)) for d in (True, False) for t in (128, 256)
                                                              for p in (True, False)}
+
+
+def lora_sizes():
+    return [(T, K, N, r, L) for T in (1, 40, 64, 65, 100, 300, 500, 511, 512, 700, 1500, 2048, 2049, 4100, 9000)
+            for K, N in ((72, 136), (1032, 72), (72, 1032), (1032, 2056), (4096, 4096), (14336, 4096))
+            for r in (8, 16, 24, 32, 40, 64, 72, 128, 200, 256) for L in (1, 2, 20)]
+
+
+def test_adapter_ways_are_reached():
+    for size, forward, backward in lora.CASES:
+        assert lora.forward_way(*size[:5]) == forward and lora.backward_way(*size[:5]) == backward, size
+    assert {f for _, f, _ in lora.CASES} == {lora.forward_way(*s) for s in lora_sizes()}
+
+    def ways(b):
+        tokens, ranks, v, u, sum_ranks, parts = b
+        return {("first launch", tokens, ranks), ("parts of dy . B", v), ("parts of x . A^T", u),
+                ("sums", sum_ranks, parts > 1)}
+
+    reached = set().union(*(ways(b) for *_, b in lora.CASES))
+    assert reached == set().union(*(ways(lora.backward_way(*s)) for s in lora_sizes()))
+
+
+@pytest.mark.parametrize("bad", [(0, 8, 8, 8, 1), (1, 12, 8, 8, 1), (1, 8, 12, 8, 1), (1, 8, 8, 264, 1), (1, 8, 8, 8, 65536)])
+def test_adapter_plans_refuse_what_the_calls_refuse(bad):
+    for call in (sg.lora_gemm_plan, sg.lora_gemm_backward_plan):
+        with pytest.raises(sg.SgError):
+            call(*bad)
 
 
 @pytest.mark.parametrize("bad", [(0, 8, 8), (1, 12, 8), (1, 8, 12), (1 << 31, 8, 8)])
