@@ -863,16 +863,24 @@ __global__ void __launch_bounds__(256) k_lora_join(LoraJoin a) {
 
 // ------------------------------------------------------------------ sizes
 
+// Times below are of the launches alone, one call after another from a graph, K = N = 4096 where not said.
+
 // Workgroups that share the items of a block of 64 tokens: as many as it may have,
-// while that does not come to more than 1024.
+// while that does not come to more than 1024.  Limits of 256 / 512 / 1024 / 2048 / 4096, mixed order, us:
+// 37 tokens of 16 adapters, rank 64, N = 14336 21 / 17 / 15.6 / 15.7 / 15.7; 300 of 16, rank 32 23 / 17.6 /
+// 16.4 / 18.5 / 18.5; 700 of 100, rank 32 119 / 77 / 65 / 74 / 93, gradients 193 / 136 / 114 / 116 / 143;
+// but 1000 of 16, rank 16, gradients 48 / 34.7 / 36.4 / 39 / 43.
 static int lora_slots(int64_t T, int64_t L, int64_t groups, int tm) {
   const int64_t n = T < 64 ? T : 64, most = (L < n ? L : n) + n / (16 * tm);
   int64_t s = 1024 / (groups < 1 ? 1 : groups);
   return (int)(s < 1 ? 1 : s > most ? most : s);
 }
 
-// Parts of a down product's sum: 256 workgroups where 16-token items give fewer, at
-// least two units of 64 columns a wave each.
+// Parts of a down product's sum: 256 workgroups where 16-token items give fewer, and only where one
+// part would give its waves more than two units of 64 columns (1032 columns, two parts: one unit a
+// wave).  1 / 2 parts, us: 1 token, K = 14336, rank 16 15.4 / 11.1; 40, rank 16 9.9 / 8.6; 1000, rank 16 12.9 /
+// 11.8; 1000, rank 64, K = 14336 36 / 30; nothing is gained at 1032 (1 token 7.3 / 7.2), and many ranks lose by it
+// (500 tokens of rank 64 14.1 / 14.8; 2048, K = 1032 26 / 29).
 static int lora_splits(int64_t T, int64_t C) {
   int64_t s = 256 / cdiv(T, 16);
   const int64_t most = cdiv(C, 64 * 2 * LORA_WAVES);
@@ -881,7 +889,10 @@ static int lora_splits(int64_t T, int64_t C) {
 }
 
 // Parts of the tokens in the sums over them: 256 workgroups, 256 tokens of an adapter each
-// at least, so that small calls need no launch to join them.
+// at least, so that small calls need no launch to join them.  Which adapters the tokens have is not
+// known here; the rule takes them as even.  4096 tokens, rank 16, 1 / 2 / 4 / 8 parts, us: one adapter 157 / 91 /
+// 58 / 47 (16, the rule: 52); 8, even 54 / 57 (the rule) / 59 / 65, all tokens of one 158 / 103 / 83 / 59; 32,
+// even 58 (the rule) / 73 / 81 / 109, all of one 159 / 109 / 83 / 102.
 static int lora_tsplits(int64_t T, int64_t C, int64_t L) {
   int64_t s = 256 / (cdiv(C, 256) * L);
   const int64_t most = T / (256 * L);
@@ -911,9 +922,16 @@ struct LoraSpace {
   }
 };
 
-// Tokens of a down workgroup's item in 16s.
+// Tokens of a down workgroup's item in 16s: an adapter read for 32 where there are many in a row.  16 / 32 at
+// 64 ranks a workgroup, runs of 4 adapters, us: 2048 tokens, rank 64 37.6 / 34.0, rank 128 62.5 / 57.2; gradients
+// of 4096, rank 256 283 / 245; 500, rank 64 15.9 / 17.0 (the edge: 600, rank 256 47.8 / 43.5).  In mixed order
+// the items are not full and 32 lose: 1000 of 16 adapters, rank 48 41 / 50, 2048, rank 64 91 / 94.
 static int lora_tm(int64_t T, int64_t r) { return T >= 512 && r > 32 ? 2 : 1; }
-// Ranks of a down workgroup in 16s: more where there are many, so that z is read less often.
+// Ranks of a down workgroup in 16s: more where there are many, so that z is read less often, fewer
+// where more workgroups are wanted.  1 / 2 / 4, runs of 4 adapters, us: 300 tokens, rank 32 10.0 / 10.5 / 11.4, rank
+// 128 18.1 / 17.2 / 19.4; 2048, rank 32 23.4 / 22.4 / 21.5; gradients of 4096, rank 32 73.4 / 70.9 / 73.0; with 32-token
+// items 2 / 4: 600, rank 64 18.8 / 20.7, 2048, rank 64 36.6 / 34.0, gradients of 2048, rank 128 95.3 / 92.6.
+// Off by most at the edges: gradients of 300, rank 64 (1: 23.2, 2: 19.1), 500, rank 256 (4: 39.3, 2: 36.2).
 static int lora_rm(int64_t T, int64_t r, int splits) {
   const int64_t tiles = splits * cdiv(T, 16) * cdiv(r, 16);
   const int rm = r <= 16 || tiles <= 256 ? 1 : r <= 32 || tiles <= 512 ? 2 : 4;
@@ -972,7 +990,12 @@ static void launch_sum(const LoraSum& a, const LoraSum& b, const LoraUp* dx, hip
   else k_lora_sum<4, NP><<<all(4), 256, 0, st>>>(a, b, ax, sums(4), u, ups);
 }
 
-// Whether a call's two products go in one launch.
+// Whether a call's two products go in one launch: up to 256 KB of an adapter's A, which every workgroup goes
+// through.  Two launches / one, us a call alone of its kind from the host, and from a graph: 1 token, rank 16 12.2 / 8.9,
+// 7.8 / 7.1; rank 32 (the edge) 12.0 / 8.8, 7.7 / 8.1; rank 64 11.8 / 11.3, 8.9 / 10.9; 64 tokens, rank 32, N = 14336 11.7 /
+// 11.1, 9.8 / 10.8; 37, rank 64 11.5 / 12.9, 10.3 / 13.0; 1, rank 8, K = 14336 11.8 / 12.8, 10.7 / 12.7.  From the host the
+// second launch counts, so the edge is where a graph would already do better with two.  More than 64
+// tokens or ranks have no such kernel.
 static bool lora_both(int64_t T, int64_t C, int64_t r) { return T <= 64 && r <= 64 && 2 * C * r <= 256 * 1024; }
 
 template <int RM>
