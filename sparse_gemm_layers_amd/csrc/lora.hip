@@ -990,12 +990,12 @@ static void launch_sum(const LoraSum& a, const LoraSum& b, const LoraUp* dx, hip
   else k_lora_sum<4, NP><<<all(4), 256, 0, st>>>(a, b, ax, sums(4), u, ups);
 }
 
-// Whether a call's two products go in one launch: up to 256 KB of an adapter's A, which every workgroup goes
-// through.  Two launches / one, us a call alone of its kind from the host, and from a graph: 1 token, rank 16 12.2 / 8.9,
-// 7.8 / 7.1; rank 32 (the edge) 12.0 / 8.8, 7.7 / 8.1; rank 64 11.8 / 11.3, 8.9 / 10.9; 64 tokens, rank 32, N = 14336 11.7 /
-// 11.1, 9.8 / 10.8; 37, rank 64 11.5 / 12.9, 10.3 / 13.0; 1, rank 8, K = 14336 11.8 / 12.8, 10.7 / 12.7.  From the host the
-// second launch counts, so the edge is where a graph would already do better with two.  More than 64
-// tokens or ranks have no such kernel.
+// Whether a call's two products go in one launch: up to 256 KB of an adapter's A, which every workgroup
+// goes through.  Two launches / one, us, calls one after another from the host; from a graph: 1 token, rank 16
+// 12.2 / 8.9; 7.8 / 7.1.  Rank 32 (the edge) 12.0 / 8.8; 7.7 / 8.1.  Rank 64 11.8 / 11.3; 8.9 / 10.9.  64 tokens, rank
+// 32, N = 14336 11.7 / 11.1; 9.8 / 10.8.  37, rank 64 11.5 / 12.9; 10.3 / 13.0.  1, rank 8, K = 14336 11.8 / 12.8;
+// 10.7 / 12.7.  From the host the second launch counts, so the edge is where a graph would already do
+// better with two.  More than 64 tokens or ranks have no such kernel.
 static bool lora_both(int64_t T, int64_t C, int64_t r) { return T <= 64 && r <= 64 && 2 * C * r <= 256 * 1024; }
 
 template <int RM>
