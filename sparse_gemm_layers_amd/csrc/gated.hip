@@ -79,6 +79,11 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
 }
 
 // Token m, hidden values f .. f + 7: from the sums of both products to what is stored.
+// BACK: dG and dU are rounded to bf16 here, once, and as such are what is returned, what an adapter's
+// backward pass takes for its dy, and the operands of dX and dW.  The matrix core takes 8 bits a value;
+// two parts of each, as in lora.hip, would double its instructions, which are what the large
+// gradients wait for (2048 x 11008 x 4096 540 us of 600).  Over the whole output dX and dW are off
+// by 0.0023 then, where rounding them alone gives 0.0017 (tests/test_gpu_gated_formula.py).
 template <bool BACK>
 __device__ __forceinline__ void gated_finish(const GatedArgs& a, int64_t m, int f, float (&g)[8], float (&u)[8]) {
   float t[8];
