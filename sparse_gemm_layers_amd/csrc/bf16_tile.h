@@ -21,7 +21,8 @@
 // reads a third less from LDS, has its sums moved about by the compiler (690).
 // Without LAG a wave takes a whole block's operands at once and there is one barrier a block: better where
 // products are short (40 x 1000 x 8000 in tiles of 64 28 us for 38, 128 x 11008 x 4096 in tiles of 128 with the
-// weights in the cache 37 for 43), no better with 256 (256 x 11008 x 4096 65 for 63).
+// weights in the cache 34 for 38), no better with 256 (256 x 11008 x 4096 65 for 63: here and below one launch
+// after another from a graph, other weights each time where not said).
 // What bounds a block is LDS: a KB written by a load or read costs it 8 cycles (measured), so 128 x
 // 128 takes 1024 cycles (0.45 us a block), 128 x 256 1408 (0.60), 256 x 256 2048, as its products do.
 // What is left in the largest: the card's power.  It holds 1.75 to 1.9 GHz under this load, with the

@@ -439,9 +439,11 @@ static void launch_gated_tile(const GatedArgs& a, hipStream_t st) {
 // Which tiles: a block of 64 k takes a workgroup about as long however many others there
 // are, until they take turns.  us a block, in hundredths: 256 x 256 127, 128 x 256 93,
 // 128 x 128 75, 64 x 64 50 (one a compute unit) or 73 (two).  Measured, us, tiles in
-// that order: 128 x 11008 x 4096 79 / 58 / 51 / 61; 256 tokens 81 / 63 / 85 / 94; 512 96 / 114 /
-// 121 / 166; 1024 x 4096 x 4096 80 / 65 / 82 / 121; 333 x 2760 x 1032 30 / 20 / 16 / 18; 200 x 2000 x
-// 3000 58 / 41 / 31 / 18; 64 x 5512 x 2040 51 / 32 / 28 / 20; 64 x 14336 x 4096 - / - / 54 / 53.
+// that order, one launch after another from a graph with other weights each time (a program whose other
+// data goes through the caches too sees up to 70 for the 63 of 256 tokens): 128 x 11008 x 4096 81 / 59 /
+// 51 / 60; 256 tokens 81 / 63 / 85 / 96; 512 93 / 114 / 124 / 165; 1024 x 4096 x 4096 82 / 66 / 82 / 120; 333 x
+// 2760 x 1032 31 / 20 / 16 / 18; 200 x 2000 x 3000 58 / 41 / 31 / 19; 64 x 5512 x 2040 53 / 33 / 30 / 21; 64 x
+// 14336 x 4096 80 / 59 / 52 / 54 (the rule takes the last).
 enum GatedWay { GATED_ROWS, GATED_A, GATED_B, GATED_C, GATED_D };
 static GatedWay gated_way(int64_t T, int64_t F) {
   if (T <= 16) return GATED_ROWS;
@@ -466,10 +468,11 @@ static void launch_gated(const GatedArgs& a, hipStream_t st) {
 // least (us a block of 64 k as above and for a tile's start and end), and that of writing,
 // reading and adding the parts.  With the many shorter workgroups of dW behind them, dX's
 // need no parts to fill the card: 2048 x 11008 x 4096, 2 parts and their sum 591 us, none 560.
-// The constants are those with which the choice is closest to the best one measured, 1.5% on
-// average over 23 sizes with and without dW (20 x 512 x 1000 to 2048 x 11008 x 4096; 64 x 11008 x
-// 4096 the furthest, 100 us for 98).  333 x 2760 x 1032, whole call: 256 with 13 parts 35 us, 128
-// with 8 parts 32, with 1 part 83; 2048 x 4096 x 1024: 256 with 4 parts 78, 128 with 2 93.
+// Over 23 sizes with and without dW (20 x 512 x 1000 to 2048 x 11008 x 4096, plans in turn) the choice is 2.9%
+// off the best one measured on average; furthest with dW at few tokens of wide projections: 64 x 11008 x
+// 4096 125 us for 96, 128 tokens 135 for 107, 256 160 for 136, all with tiles of 256 and 8 parts; 1200 x 7168 x
+// 2048 157 for 145.  333 x 2760 x 1032, whole call: 128 with 6 or 8 parts 34 us, with 16 36;
+// 2048 x 4096 x 1024: 256 with 4 parts 83, 128 with 2 97.
 struct GradPlan {
   bool big;
   int splits;
