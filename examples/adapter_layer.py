@@ -61,7 +61,8 @@ class Block:
         self.d, self.gate, self.up = d, w(f, d).to(BF16), w(f, d).to(BF16)
         codes, scales = sg.int4_quant_groupwise(w(d, f), gc=GC)
         self.down = sg.w4_pack(codes, scales, GC)
-        # what the packed weight stands for, for the input gradient of fine-tuning
+        # what the packed weight stands for, for the input gradient of fine-tuning: the library has no
+        # product with a packed weight's columns, so this costs the memory that 4 bits save
         eye = torch.eye(f, dtype=BF16, device=DEV)
         self.down_t = sg.w4a16_gemm_groupwise_packed(eye, self.down, d, GC)        # [F, D]
         self.on_gate, self.on_up, self.on_down = (Adapters(count, n, k, rank, gen) for n, k in ((f, d), (f, d), (d, f)))
