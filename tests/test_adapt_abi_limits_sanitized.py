@@ -11,7 +11,7 @@ from sparse_gemm_layers_amd import build as B
 from test_abi_sanitized import ROOT, _stale
 from test_adapt_abi_sanitized import HEADERS
 
-FILES = ["test_adapt_abi_limits.py"]
+FILES = ["test_adapt_abi_limits.py", "test_adapt_plans.py"]
 
 
 @pytest.mark.timeout(600)
